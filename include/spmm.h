@@ -29,6 +29,10 @@
  * companion of SpMM on the Magicube page ("Efficient Quantized Sparse Matrix
  * Operations on Tensor Cores", abstract).
  *
+ * The same block sparsity applied to attention, where the two products share
+ * one pattern (Q K^T sampled on it, its softmax times V), is served by the
+ * spmm_*_attn* calls at the end of this file.
+ *
  * Usage: pack A once on the host (spmm_pack_*), build a device plan for a
  * given number of columns n (spmm_plan), then multiply any number of dense B
  * by it (spmm_execute) on the caller's HIP stream.
@@ -63,14 +67,21 @@ typedef enum {
   SPMM_ERR_INTERNAL = 5
 } spmm_status_t;
 
-typedef enum { SPMM_F32 = 0, SPMM_BF16 = 1, SPMM_I8 = 2, SPMM_I32 = 3 } spmm_dtype_t;
+typedef enum {
+  SPMM_F32 = 0,
+  SPMM_BF16 = 1,
+  SPMM_I8 = 2,
+  SPMM_I32 = 3,
+  SPMM_F16 = 4  /* attention only */
+} spmm_dtype_t;
 
 typedef enum {
   SPMM_FORMAT_BCSR = 0,
   SPMM_FORMAT_WCSR = 1,
   SPMM_FORMAT_24 = 2,
   SPMM_FORMAT_TVW = 3,   /* tile-vector-wise: 2:4 inside the stored tiles of a tile grid */
-  SPMM_FORMAT_SLIDE = 4  /* (2N-2):2N as overlapping 2:4 windows                        */
+  SPMM_FORMAT_SLIDE = 4, /* (2N-2):2N as overlapping 2:4 windows                        */
+  SPMM_FORMAT_ATTN = 5   /* plans of spmm_plan_attn: no packed matrix                   */
 } spmm_format_t;
 
 /* Packed sparse operand: immutable host arrays in the canonical layout below,
@@ -358,6 +369,123 @@ spmm_status_t spmm_plan_sddmm(spmm_matrix_t a, int64_t kd, spmm_dtype_t dtype, i
  * refused here and SDDMM plans by spmm_execute (INVALID_ARG). */
 spmm_status_t spmm_execute_sddmm(spmm_plan_t p, const void *x_dev, int64_t ldx, const void *y_dev,
                                  int64_t ldy, void *out_dev, hipStream_t stream);
+
+/* ---- block-sparse attention ----
+ *
+ * Keys come in blocks of 64.  A list names the blocks that a query block of
+ * q_block consecutive queries reads for one key/value head; heads_q /
+ * heads_kv query heads share a key head.  Query t of sequence i stands at
+ * position starts[i] + t, and sees key j when
+ *   j < lens[i],  j <= starts[i] + t,  and j's block is in the list.
+ * With s_tj = scale * (q_t . k_j) over those keys,
+ *   lse_t = log(sum_j exp(s_tj)),   o_t = sum_j exp(s_tj - lse_t) v_j.
+ * A query that sees no key, or whose position is not in [0, lens[i]), has
+ * o = 0, lse = -infinity and takes no part in the gradients.
+ *
+ * Tensors of heads are [batch][tokens][heads][dim] (or [pages][64][heads][dim]
+ * for a cache) with strides in elements, multiples of 8 and not negative, the
+ * dim elements consecutive, 16-byte aligned.  Heads of an input may share
+ * memory (stride_head = 0, a broadcast); a gradient is given per head.  Keys
+ * past a sequence's length are never used, whatever stands there.
+ * lens and starts are int32[batch] on the device; NULL means lens[i] = keys,
+ * starts[i] = 0.  A length outside [0, keys] is taken as the nearer bound.
+ *
+ * A list is int32[max_blocks], ascending, filled up with -1.  Entries below 0
+ * or at or past the sequence's last block read nothing; a block named twice
+ * counts twice.  Lists are [batch][heads_kv][ceil(queries / q_block)][max_blocks].
+ * A table is int32[batch][ceil(keys / 64)]: the page of each block of a
+ * sequence.  An entry that is no page of the cache (outside [0, pages)) reads
+ * nothing and writes nothing.
+ *
+ * Products run on bf16 or f16 operands with fp32 sums; softmax statistics are
+ * fp32; weights and their gradients are rounded to the element type (nearest
+ * even) for the products that take them.  Same inputs, same bits.
+ * Every execute only launches kernels on `stream`: it allocates nothing, does
+ * not synchronise and can be captured into a graph.  A plan's workspace
+ * allows one execute in flight at a time. */
+typedef struct {
+  int64_t batch, queries, keys;  /* sequences; queries and (at most) keys of each   */
+  int32_t heads_q, heads_kv;     /* heads_q a multiple of heads_kv                  */
+  int32_t dim;                   /* 64 or 128 (else UNSUPPORTED)                    */
+  int32_t dtype;                 /* SPMM_BF16 or SPMM_F16 (else UNSUPPORTED)        */
+  int32_t q_block;               /* queries of a list: 1, 2, 4, .. 64               */
+  int32_t max_blocks;            /* entries of a list                               */
+  int32_t sink_blocks;           /* first blocks that spmm_execute_attn_select keeps */
+  int32_t local_blocks;          /* last blocks it keeps, at least 1 (the queries' own) */
+  int32_t backward;              /* 1: with workspace for spmm_execute_attn_backward */
+  float scale;                   /* of the scores; 0: 1 / sqrt(dim)                 */
+} spmm_attn_desc_t;
+
+typedef struct {
+  void *data;
+  int64_t stride_batch, stride_token, stride_head;  /* elements; batch: sequences or pages */
+} spmm_attn_tensor_t;
+
+/* A plan for attention of one shape on `device`: checks, tile choice and
+ * workspace (spmm_plan_info: m = batch * queries, k = keys, n = dim, tile_m
+ * rows of a workgroup, tile_n keys of a step).  spmm_execute and
+ * spmm_execute_sddmm refuse it (INVALID_ARG). */
+spmm_status_t spmm_plan_attn(const spmm_attn_desc_t *desc, int32_t device, spmm_plan_t *out);
+
+/* Mean keys of the blocks in 8 bits: with sum_c = sum over the block's keys
+ * below lens[i] of k[j][c], top = max_c |sum_c| and n of those keys,
+ *   pooled[c] = round(127 sum_c / top),  pooled_scale = top / (127 n)
+ * (zeros for top = 0; a sum that is not finite gives the values 0 and that
+ * scale), sums in 64 bits.  pooled is int8[slots][heads_kv][dim], pooled_scale
+ * float[slots][heads_kv]; slot = the block's page with a table, else
+ * i * ceil(keys / 64) + block.  first (int32[batch], or NULL: all blocks)
+ * pools only the blocks from key first[i] on, those that `queries` new keys
+ * can have changed.  Blocks without a key below the length are not written.
+ * table == NULL: k is [batch][keys][heads_kv][dim] and pages is not read. */
+spmm_status_t spmm_execute_attn_pool(spmm_plan_t p, const spmm_attn_tensor_t *k, int64_t pages,
+                                     int8_t *pooled_dev, float *pooled_scale_dev, const int32_t *table,
+                                     const int32_t *lens, const int32_t *first, hipStream_t stream);
+
+/* The lists of every query block: with Q_c = sum over the block's queries in
+ * [0, lens[i]) and the heads that share the key head of q[t][h][c], and q8 =
+ * round(127 Q / max|Q|), block j scores float(q8 . pooled_j) * pooled_scale_j.
+ * Of the blocks up to the last query's own, the max_blocks highest are
+ * listed, ties to the lower block; the first sink_blocks and the last
+ * local_blocks always are.  A score that is not a number, or of a block
+ * without a page, ranks lowest.  sink_blocks + local_blocks must be at most
+ * max_blocks (else INVALID_ARG).  At most 32768 blocks a sequence (else
+ * UNSUPPORTED). */
+spmm_status_t spmm_execute_attn_select(spmm_plan_t p, const spmm_attn_tensor_t *q,
+                                       const int8_t *pooled_dev, const float *pooled_scale_dev,
+                                       int64_t pages, int32_t *lists_dev, const int32_t *table,
+                                       const int32_t *lens, const int32_t *starts, hipStream_t stream);
+
+/* o and lse (float[batch][heads_q][queries]) over the listed blocks; every
+ * element of both is written. */
+spmm_status_t spmm_execute_attn(spmm_plan_t p, const spmm_attn_tensor_t *q, const spmm_attn_tensor_t *k,
+                                const spmm_attn_tensor_t *v, const int32_t *lists_dev,
+                                const spmm_attn_tensor_t *o, float *lse_dev, const int32_t *lens,
+                                const int32_t *starts, hipStream_t stream);
+
+/* Gradients of q, k and v from grad = that of o, with the o and lse of the
+ * forward call on the same inputs; every element of dq, dk and dv is written
+ * (zeros where nothing flows).  q and grad of a sequence must span less than
+ * 4 GiB (else UNSUPPORTED). */
+spmm_status_t spmm_execute_attn_backward(spmm_plan_t p, const spmm_attn_tensor_t *grad,
+                                         const spmm_attn_tensor_t *q, const spmm_attn_tensor_t *k,
+                                         const spmm_attn_tensor_t *v, const int32_t *lists_dev,
+                                         const spmm_attn_tensor_t *o, const float *lse_dev,
+                                         const spmm_attn_tensor_t *dq, const spmm_attn_tensor_t *dk,
+                                         const spmm_attn_tensor_t *dv, const int32_t *lens,
+                                         const int32_t *starts, hipStream_t stream);
+
+/* Attention of new tokens over a cache of pages: every block (lists NULL) or
+ * the listed ones.  k and v are [pages][64][heads_kv][dim] reached through
+ * the table, or without one [batch][keys][heads_kv][dim].  tree (uint64
+ * [batch][queries], at most 64 queries, or NULL) replaces j <= starts[i] + t
+ * for drafted tokens: keys before starts[i] are seen, and key starts[i] + u
+ * when bit u of tree[i][t] is set. */
+spmm_status_t spmm_execute_attn_cache(spmm_plan_t p, const spmm_attn_tensor_t *q,
+                                      const spmm_attn_tensor_t *k, const spmm_attn_tensor_t *v,
+                                      int64_t pages, const spmm_attn_tensor_t *o, float *lse_dev,
+                                      const int32_t *table, const int32_t *lists_dev,
+                                      const uint64_t *tree, const int32_t *lens, const int32_t *starts,
+                                      hipStream_t stream);
 
 /* ---- errors ---- */
 const char *spmm_status_str(spmm_status_t s);

@@ -13,18 +13,21 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 import numpy as np
 
 __all__ = [
-    "SpmmError", "Matrix", "Plan", "F32", "BF16", "I8", "I32",
-    "FORMAT_BCSR", "FORMAT_WCSR", "FORMAT_24", "FORMAT_TVW", "FORMAT_SLIDE",
+    "SpmmError", "Matrix", "Plan", "F32", "BF16", "I8", "I32", "F16",
+    "FORMAT_BCSR", "FORMAT_WCSR", "FORMAT_24", "FORMAT_TVW", "FORMAT_SLIDE", "FORMAT_ATTN",
     "ARRAY_ROW_PTR", "ARRAY_COL_IDX", "ARRAY_VALS", "ARRAY_META",
     "ARRAY_CHUNK_WINDOW", "ARRAY_CHUNK_BEGIN", "ARRAY_ROW_PERM", "ARRAY_COL_PERM",
     "spmm_pack_bcsr", "spmm_pack_bcsr_csr", "spmm_pack_wcsr", "spmm_pack_24", "spmm_pack_tvw", "spmm_pack_slide",
     "spmm_matrix_info",
     "spmm_matrix_array", "spmm_plan", "spmm_plan_info", "spmm_execute", "spmm_execute_noalloc",
     "spmm_plan_sddmm", "spmm_execute_sddmm",
+    "spmm_plan_attn", "spmm_execute_attn_pool", "spmm_execute_attn_select", "spmm_execute_attn",
+    "spmm_execute_attn_backward", "spmm_execute_attn_cache",
     "spmm_status_str", "spmm_last_error", "LIB_PATH", "EXPORTS",
 ]
 
@@ -32,9 +35,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 # SPMM_LIBRARY may point at another build of the same library
 LIB_PATH = os.environ.get("SPMM_LIBRARY") or os.path.join(HERE, "libspmm.so")
 
-F32, BF16, I8, I32 = 0, 1, 2, 3
+F32, BF16, I8, I32, F16 = 0, 1, 2, 3, 4
 _ELEM = {F32: 4, BF16: 2, I8: 1, I32: 4}  # bytes per element of each type
-FORMAT_BCSR, FORMAT_WCSR, FORMAT_24, FORMAT_TVW, FORMAT_SLIDE = 0, 1, 2, 3, 4
+FORMAT_BCSR, FORMAT_WCSR, FORMAT_24, FORMAT_TVW, FORMAT_SLIDE, FORMAT_ATTN = 0, 1, 2, 3, 4, 5
 (ARRAY_ROW_PTR, ARRAY_COL_IDX, ARRAY_VALS, ARRAY_META, ARRAY_CHUNK_WINDOW,
  ARRAY_CHUNK_BEGIN, ARRAY_ROW_PERM, ARRAY_COL_PERM) = range(8)
 
@@ -50,6 +53,8 @@ EXPORTS = (
     "spmm_matrix_array", "spmm_matrix_destroy", "spmm_plan", "spmm_plan_info",
     "spmm_plan_destroy", "spmm_execute", "spmm_execute_noalloc", "spmm_plan_sddmm",
     "spmm_execute_sddmm",
+    "spmm_plan_attn", "spmm_execute_attn_pool", "spmm_execute_attn_select", "spmm_execute_attn",
+    "spmm_execute_attn_backward", "spmm_execute_attn_cache",
     "spmm_status_str", "spmm_last_error",
 )
 
@@ -68,6 +73,14 @@ class PlanInfo(C.Structure):
                 ("workspace_bytes", C.c_int64), ("num_split_rows", C.c_int64),
                 ("num_slots", C.c_int64), ("tile_m", C.c_int32), ("tile_n", C.c_int32),
                 ("grid", C.c_int64)]
+
+
+class AttnDesc(C.Structure):
+    _fields_ = [("batch", C.c_int64), ("queries", C.c_int64), ("keys", C.c_int64),
+                ("heads_q", C.c_int32), ("heads_kv", C.c_int32), ("dim", C.c_int32),
+                ("dtype", C.c_int32), ("q_block", C.c_int32), ("max_blocks", C.c_int32),
+                ("sink_blocks", C.c_int32), ("local_blocks", C.c_int32), ("backward", C.c_int32),
+                ("scale", C.c_float)]
 
 
 def _load():
@@ -101,6 +114,12 @@ def _load():
         "spmm_execute_noalloc": (st, [P, P, i64, P, i64, P]),
         "spmm_plan_sddmm": (st, [P, i64, st, i32, C.POINTER(P)]),
         "spmm_execute_sddmm": (st, [P, P, i64, P, i64, P, P]),
+        "spmm_plan_attn": (st, [C.POINTER(AttnDesc), i32, C.POINTER(P)]),
+        "spmm_execute_attn_pool": (st, [P, P, i64, P, P, P, P, P, P]),
+        "spmm_execute_attn_select": (st, [P, P, P, P, i64, P, P, P, P, P]),
+        "spmm_execute_attn": (st, [P] * 10),
+        "spmm_execute_attn_backward": (st, [P] * 14),
+        "spmm_execute_attn_cache": (st, [P, P, P, P, i64] + [P] * 8),
         "spmm_status_str": (C.c_char_p, [st]),
         "spmm_last_error": (C.c_char_p, []),
     }
@@ -425,3 +444,164 @@ def spmm_execute_sddmm(plan: Plan, x, y, out, stream=None, ldx: int | None = Non
         stream = stream.cuda_stream
     _check(_lib.spmm_execute_sddmm(plan.handle, C.c_void_p(xp), ldx, C.c_void_p(yp), ldy,
                                    C.c_void_p(op), C.c_void_p(stream)), "spmm_execute_sddmm")
+
+
+def spmm_plan_attn(batch: int, queries: int, keys: int, heads_q: int, heads_kv: int, dim: int,
+                   dtype: int = BF16, q_block: int = 64, max_blocks: int = 16, sink_blocks: int = 1,
+                   local_blocks: int = 1, scale: float | None = None, backward: bool = False,
+                   device: int = 0) -> Plan:
+    """Plan block-sparse attention of `batch` sequences of `queries` queries
+    over at most `keys` keys, in blocks of 64 keys; one list of max_blocks
+    blocks for each q_block queries and key head.  dtype is BF16 or F16,
+    scale defaults to 1 / sqrt(dim).  With a cache, keys is the table's width
+    times 64."""
+    if scale is not None and not scale > 0:
+        raise ValueError("scale must be positive")
+    d = AttnDesc(batch, queries, keys, heads_q, heads_kv, dim, dtype, q_block, max_blocks,
+                 sink_blocks, local_blocks, int(bool(backward)), 0.0 if scale is None else scale)
+    h = C.c_void_p()
+    _check(_lib.spmm_plan_attn(C.byref(d), device, C.byref(h)), "spmm_plan_attn")
+    return Plan(h, _attn_expect(d, device))
+
+
+def _attn_expect(d: AttnDesc, device: int) -> dict:
+    """Shapes and types of an attention plan's tensors."""
+    import torch
+    b, nq, nk, hq, hk, dim = d.batch, d.queries, d.keys, d.heads_q, d.heads_kv, d.dim
+    t = torch.bfloat16 if d.dtype == BF16 else torch.float16
+    nkb, nqb = -(-nk // 64), -(-nq // d.q_block)
+    return {"device": device, "attn": {
+        "q": ((b, nq, hq, dim), t), "k": ((b, nk, hk, dim), t), "page": ((64, hk, dim), t),
+        "lse": ((b, hq, nq), torch.float32), "lists": ((b, hk, nqb, d.max_blocks), torch.int32),
+        "table": ((b, nkb), torch.int32), "seq": ((b,), torch.int32), "tree": ((b, nq), torch.int64),
+        "slots": b * nkb}}
+
+
+_pack_tensor = struct.Struct("=4q").pack
+
+
+class _AttnCall:
+    """Marshals one call: every tensor against the plan, then pointers."""
+
+    def __init__(self, plan: Plan):
+        self.want = plan.expect.get("attn")
+        if self.want is None:
+            raise ValueError("not a plan of spmm_plan_attn")
+        self.device = plan.expect["device"]
+
+    def _check(self, name: str, t, shape, dtype):
+        if t.dtype is not dtype:
+            raise ValueError(f"{name} is {t.dtype}; the plan takes {dtype}")
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}; the plan takes {shape}")
+        if t.get_device() != self.device:
+            raise ValueError(f"{name} must be on cuda:{self.device}")
+
+    def heads(self, name: str, t, like: str, paged: bool = False):
+        """A tensor of heads: its strides go along."""
+        shape, dtype = self.want[like]
+        if paged:
+            shape, dtype = self.want["page"]
+            shape = (t.shape[0],) + shape
+        self._check(name, t, shape, dtype)
+        sb, st, sh, sd = t.stride()
+        if sd != 1 and t.numel():
+            raise ValueError(f"{name}: the elements of a head must be consecutive")
+        return _pack_tensor(t.data_ptr(), sb, st, sh)
+
+    def whole(self, name: str, t, like: str, optional: bool = False):
+        """A contiguous tensor of the plan's shape."""
+        if t is None and optional:
+            return None
+        shape, dtype = self.want[like]
+        return self.flat(name, t, shape, dtype)
+
+    def flat(self, name: str, t, shape, dtype):
+        self._check(name, t, shape, dtype)
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr()
+
+    def pooled(self, pooled, scale, slots: int):
+        import torch
+        _, hk, dim = self.want["page"][0]
+        return (self.flat("pooled", pooled, (slots, hk, dim), torch.int8),
+                self.flat("pooled_scale", scale, (slots, hk), torch.float32))
+
+    def stream(self, stream):
+        if stream is None:
+            import torch
+            stream = torch.cuda.current_stream(self.device)
+        return getattr(stream, "cuda_stream", stream)
+
+
+def spmm_execute_attn_pool(plan: Plan, k, pooled, pooled_scale, lens=None, table=None, first=None,
+                           stream=None):
+    """Mean keys of the blocks in 8 bits, pooled [slots, heads_kv, dim] int8
+    with pooled_scale [slots, heads_kv] float32.  k is [batch, keys, heads_kv,
+    dim] (slots = batch * blocks), or with a table [pages, 64, heads_kv, dim]
+    (slots = pages).  first [batch]: only the blocks from that key on."""
+    c = _AttnCall(plan)
+    kp = c.heads("k", k, "k", table is not None)
+    pages = k.shape[0] if table is not None else 0
+    pp, sp = c.pooled(pooled, pooled_scale, pages if table is not None else c.want["slots"])
+    _check(_lib.spmm_execute_attn_pool(
+        plan.handle, kp, pages, pp, sp, c.whole("table", table, "table", True),
+        c.whole("lens", lens, "seq", True), c.whole("first", first, "seq", True), c.stream(stream)),
+        "spmm_execute_attn_pool")
+
+
+def spmm_execute_attn_select(plan: Plan, q, pooled, pooled_scale, lists, lens=None, starts=None,
+                             table=None, stream=None):
+    """lists [batch, heads_kv, query blocks, max_blocks] int32: the blocks of
+    the highest scores, ascending, filled up with -1."""
+    c = _AttnCall(plan)
+    slots = pooled.shape[0] if table is not None else c.want["slots"]
+    pp, sp = c.pooled(pooled, pooled_scale, slots)
+    _check(_lib.spmm_execute_attn_select(
+        plan.handle, c.heads("q", q, "q"), pp, sp, slots if table is not None else 0,
+        c.whole("lists", lists, "lists"), c.whole("table", table, "table", True),
+        c.whole("lens", lens, "seq", True), c.whole("starts", starts, "seq", True), c.stream(stream)),
+        "spmm_execute_attn_select")
+
+
+def spmm_execute_attn(plan: Plan, q, k, v, lists, o, lse, lens=None, starts=None, stream=None):
+    """o (as q) and lse [batch, heads_q, queries] float32 of attention over
+    the listed blocks.  Query t stands at position starts + t."""
+    c = _AttnCall(plan)
+    _check(_lib.spmm_execute_attn(
+        plan.handle, c.heads("q", q, "q"), c.heads("k", k, "k"), c.heads("v", v, "k"),
+        c.whole("lists", lists, "lists"), c.heads("o", o, "q"), c.whole("lse", lse, "lse"),
+        c.whole("lens", lens, "seq", True), c.whole("starts", starts, "seq", True), c.stream(stream)),
+        "spmm_execute_attn")
+
+
+def spmm_execute_attn_backward(plan: Plan, grad, q, k, v, lists, o, lse, dq, dk, dv, lens=None,
+                               starts=None, stream=None):
+    """dq, dk and dv from grad, the gradient of o; o and lse are the forward
+    call's.  The plan must have been made with backward=True."""
+    c = _AttnCall(plan)
+    _check(_lib.spmm_execute_attn_backward(
+        plan.handle, c.heads("grad", grad, "q"), c.heads("q", q, "q"), c.heads("k", k, "k"),
+        c.heads("v", v, "k"), c.whole("lists", lists, "lists"), c.heads("o", o, "q"),
+        c.whole("lse", lse, "lse"), c.heads("dq", dq, "q"), c.heads("dk", dk, "k"),
+        c.heads("dv", dv, "k"), c.whole("lens", lens, "seq", True),
+        c.whole("starts", starts, "seq", True), c.stream(stream)), "spmm_execute_attn_backward")
+
+
+def spmm_execute_attn_cache(plan: Plan, q, k, v, o, lse, table=None, lists=None, tree=None, lens=None,
+                            starts=None, stream=None):
+    """o and lse of new tokens over a cache: k and v are pages [pages, 64,
+    heads_kv, dim] with a table [batch, blocks], else [batch, keys, heads_kv,
+    dim]; every block, or the lists'.  tree [batch, queries] int64: bit u of a
+    drafted token's word is set where it sees drafted token u."""
+    c = _AttnCall(plan)
+    paged = table is not None
+    if paged and k.shape[0] != v.shape[0]:
+        raise ValueError("k and v must have the same pages")
+    _check(_lib.spmm_execute_attn_cache(
+        plan.handle, c.heads("q", q, "q"), c.heads("k", k, "k", paged), c.heads("v", v, "k", paged),
+        k.shape[0] if paged else 0, c.heads("o", o, "q"), c.whole("lse", lse, "lse"),
+        c.whole("table", table, "table", True), c.whole("lists", lists, "lists", True),
+        c.whole("tree", tree, "tree", True), c.whole("lens", lens, "seq", True),
+        c.whole("starts", starts, "seq", True), c.stream(stream)), "spmm_execute_attn_cache")

@@ -58,41 +58,6 @@ void release(Matrix *a) {
     delete static_cast<spmm_matrix_s *>(a);
 }
 
-namespace {
-
-template <class F>
-spmm_status_t guarded(F &&f) {
-  try {
-    return f();
-  } catch (const std::bad_alloc &) {
-    return fail(SPMM_ERR_OUT_OF_MEMORY, "host allocation failed");
-  } catch (const std::exception &e) {
-    return fail(SPMM_ERR_INTERNAL, e.what());
-  } catch (...) {
-    return fail(SPMM_ERR_INTERNAL, "unknown exception");
-  }
-}
-
-// A new packed operand, owned until it is handed to the caller.
-std::unique_ptr<spmm_matrix_s> new_matrix() {
-  if (alloc_hook_fail()) throw std::bad_alloc();
-  return std::unique_ptr<spmm_matrix_s>(new spmm_matrix_s());
-}
-
-// Restores the caller's current device on scope exit.
-struct DeviceScope {
-  int prev = -1;
-  hipError_t err = hipSuccess;
-  explicit DeviceScope(int dev) {
-    err = hipGetDevice(&prev);
-    if (err == hipSuccess && prev != dev) err = hipSetDevice(dev);
-  }
-  ~DeviceScope() {
-    int cur = -1;
-    if (prev >= 0 && hipGetDevice(&cur) == hipSuccess && cur != prev) (void)hipSetDevice(prev);
-  }
-};
-
 void free_plan(spmm_plan_s *p) {
   if (!p) return;
   if (!p->allocations.empty()) {
@@ -101,6 +66,38 @@ void free_plan(spmm_plan_s *p) {
   }
   release(p->a);
   delete p;
+}
+
+spmm_status_t plan_workspace(spmm_plan_s *p, size_t bytes, void **dst) {
+  *dst = nullptr;
+  if (bytes == 0) return SPMM_OK;
+  p->allocations.push_back(nullptr);  // may throw; nothing is allocated yet
+  void *d = nullptr;
+  hipError_t e = alloc_hook_fail() ? hipErrorOutOfMemory : hipMalloc(&d, bytes);
+  if (e != hipSuccess) {
+    p->allocations.pop_back();
+    return hip_fail(e, "hipMalloc");
+  }
+  p->allocations.back() = d;
+  p->info.workspace_bytes += static_cast<int64_t>(bytes);
+  *dst = d;
+  return SPMM_OK;
+}
+
+// SPMM_LOG set to anything but "" or "0": every plan that succeeds prints
+// its decisions (kernel, tile, grid, schedule, device and workspace bytes)
+// as one line on stderr.  Read at each call.
+bool plan_log_on() {
+  const char *v = std::getenv("SPMM_LOG");
+  return v && v[0] && std::strcmp(v, "0") != 0;
+}
+
+namespace {
+
+// A new packed operand, owned until it is handed to the caller.
+std::unique_ptr<spmm_matrix_s> new_matrix() {
+  if (alloc_hook_fail()) throw std::bad_alloc();
+  return std::unique_ptr<spmm_matrix_s>(new spmm_matrix_s());
 }
 
 // hipMalloc + copy; the pointer is owned by the plan.
@@ -542,14 +539,6 @@ spmm_status_t plan_tvw(spmm_plan_s *p) {
 
 bool aligned16(const void *ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
 
-// SPMM_LOG set to anything but "" or "0": every plan that succeeds prints
-// its decisions (kernel, tile, grid, schedule, device and workspace bytes)
-// as one line on stderr.  Read at each call.
-bool plan_log_on() {
-  const char *v = std::getenv("SPMM_LOG");
-  return v && v[0] && std::strcmp(v, "0") != 0;
-}
-
 void plan_log(const char *fn, const spmm_plan_s *p) {
   static const char *const kFormat[] = {"bcsr", "wcsr", "24", "tvw", "slide"};
   const Matrix &a = *p->a;
@@ -796,6 +785,8 @@ spmm_status_t spmm_matrix_array(spmm_matrix_t a, int32_t which, const void **dat
         return a->dtype == SPMM_BF16 ? give(a->vals24_bf16) : give(a->vals24);
       if (which == SPMM_ARRAY_META) return give(a->meta24);
       break;
+    case SPMM_FORMAT_ATTN:  // plans only: no matrix has it
+      break;
   }
   return fail(SPMM_ERR_INVALID_ARG, "spmm_matrix_array: no such array for this format");
 }
@@ -879,6 +870,7 @@ spmm_status_t execute(const char *fn, spmm_plan_t p, const void *b_dev, int64_t 
   const std::string name(fn);
   if (!p) return fail(SPMM_ERR_INVALID_ARG, name + ": plan is NULL");
   if (p->sddmm) return fail(SPMM_ERR_INVALID_ARG, name + ": plan is an SDDMM plan");
+  if (p->attn) return fail(SPMM_ERR_INVALID_ARG, name + ": plan is an attention plan");
   const Matrix &a = *p->a;
   const int64_t n = p->n;
   if (n == 0 || a.m == 0) return SPMM_OK;

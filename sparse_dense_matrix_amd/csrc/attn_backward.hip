@@ -1,0 +1,617 @@
+// attn_backward.hip -- gradients of attention over listed blocks.  With
+// p_tj = exp(scale q_t . k_j - lse_t) over what query t sees, and
+// delta_t = do_t . o_t = sum_j p_tj (do_t . v_j):
+//   dv_j = sum_t p_tj do_t          ds_tj = p_tj (do_t . v_j - delta_t)
+//   dq_t = scale sum_j ds_tj k_j    dk_j = scale sum_t ds_tj q_t
+//
+// Three launches.  attn_dq walks each query block's list as the forward does
+// and keeps dq in registers; its first workgroups invert the lists (for each
+// key block the query blocks that name it, ascending).  attn_dkv walks the
+// inverse list of a key block and keeps dk and dv in registers.  A block that
+// many lists name (the first of a sequence is in all of them) is cut into
+// items of `chunk` query blocks, whose partial sums attn_dkv_merge adds in
+// order: no atomics, so the same inputs give the same bits.
+//
+// p and ds are rounded to the element type for their products, at most half a
+// step each; sums, statistics and delta stay in 32 bits.
+#include <algorithm>
+
+#include "attn_dev.h"
+#include "internal.h"
+
+namespace sdm {
+namespace attn {
+namespace {
+
+constexpr int kMaxChunk = 1024;         // query blocks of an item
+constexpr uint32_t kDeadRow = 0xffffff00u;  // offset past every buffer: a direct load gives zeros
+
+// Sequence length, position of the first query, and last key that query block
+// qb sees.
+__device__ __forceinline__ int32_t last_key_of(const AttnArgs &a, int qb, int32_t len, int32_t start) {
+  return min(len - 1, start + min(a.nq - 1, qb * a.q_block + a.q_block - 1));
+}
+
+// Inverse list of key block kb of head bh, and its items.  A thread takes a
+// list at a time; lists run in order over threads, so ids come out ascending.
+__device__ void invert(const AttnArgs &a, int64_t which, char *lds) {
+  const int kb = which % a.nkb;
+  const int64_t bh = which / a.nkb;
+  const int b = bh / a.hk;
+  const int32_t len = attn_len(a.lens, b, a.nk), start = attn_start(a.starts, b, a.nq, a.nk);
+  const int64_t entries = static_cast<int64_t>(a.nqb) * a.max_blocks;
+  const int32_t *lists = a.lists + bh * entries;
+  int *sums = reinterpret_cast<int *>(lds);  // [waves][2]
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 63, wave = tid >> 6, waves = nt >> 6;
+
+  int less = 0, same = 0;
+  for (int qb = tid; qb < a.nqb; qb += nt) {
+    const int32_t last = last_key_of(a, qb, len, start);
+    for (int j = 0; j < a.max_blocks; ++j) {
+      const int32_t id = lists[static_cast<int64_t>(qb) * a.max_blocks + j];
+      if (!attn_names(id, last)) continue;
+      less += id < kb;
+      same += id == kb;
+    }
+  }
+#pragma unroll
+  for (int m = 1; m < 64; m *= 2) {
+    less += __shfl_xor(less, m);
+    same += __shfl_xor(same, m);
+  }
+  if (lane == 0) {
+    sums[2 * wave] = less;
+    sums[2 * wave + 1] = same;
+  }
+  __syncthreads();
+  less = same = 0;
+  for (int w = 0; w < waves; ++w) {
+    less += sums[2 * w];
+    same += sums[2 * w + 1];
+  }
+  __syncthreads();
+
+  int32_t *ids = a.inv_ids + bh * entries + less;
+  int base = 0;
+  if (same > 0) {
+    for (int q0 = 0; q0 < a.nqb; q0 += nt) {
+      const int qb = q0 + tid;
+      int mine = 0;
+      if (qb < a.nqb) {
+        const int32_t last = last_key_of(a, qb, len, start);
+        for (int j = 0; j < a.max_blocks; ++j) {
+          const int32_t id = lists[static_cast<int64_t>(qb) * a.max_blocks + j];
+          mine += id == kb && attn_names(id, last);
+        }
+      }
+      int upto = mine;
+#pragma unroll
+      for (int m = 1; m < 64; m *= 2) {
+        const int x = __shfl_up(upto, m);
+        if (lane >= m) upto += x;
+      }
+      if (lane == 63) sums[wave] = upto;
+      __syncthreads();
+      int before = base, all = 0;
+      for (int w = 0; w < waves; ++w) {
+        if (w < wave) before += sums[w];
+        all += sums[w];
+      }
+      for (int j = 0; j < mine; ++j) ids[before + upto - mine + j] = qb;
+      base += all;
+      __syncthreads();
+    }
+  }
+  // Items stand at kb + less / chunk on: that leaves room for max(1,
+  // ceil(same / chunk)) of them before the next key block's.
+  int32_t *items = a.items + bh * a.slots * 2;
+  const int first = kb + less / a.chunk;
+  const int next = kb + 1 == a.nkb ? a.slots : kb + 1 + (less + same) / a.chunk;
+  const int n = max(1, (same + a.chunk - 1) / a.chunk);
+  for (int i = tid; i < next - first; i += nt) {
+    items[2 * (first + i)] = i < n ? kb : -1;
+    items[2 * (first + i) + 1] = i;
+  }
+  if (tid == 0) {
+    a.inv_ptr[2 * (bh * a.nkb + kb)] = less;
+    a.inv_ptr[2 * (bh * a.nkb + kb) + 1] = same;
+  }
+}
+
+// dq, and the inverse lists: workgroups below b * hk * nkb invert.  Waves and
+// tiles as in the forward kernel.
+template <class T, int D, int RW, int KW, int KT>
+__global__ __launch_bounds__(64 * RW * KW) void attn_dq(const AttnArgs a) {
+  using L = Tile<D>;
+  constexpr int kHalf = KT * L::kRowBytes;
+  constexpr int kLoads = kHalf / 1024 / RW;
+  static_assert(kLoads >= 1 && kLoads * RW * 1024 == kHalf, "loads of a stage");
+  constexpr int kSubs = kAttnPage / KT;
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+
+  int64_t item = blockIdx.x;
+  const int64_t inverts = static_cast<int64_t>(a.b) * a.hk * a.nkb;
+  if (item < inverts) {
+    invert(a, item, lds);
+    return;
+  }
+  item -= inverts;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rw = wave % RW, kw = wave / RW;
+  const int h2 = lane >> 5;
+  const int h = item % a.hk;
+  item /= a.hk;
+  const int rt = item % a.rtiles;
+  item /= a.rtiles;
+  const int qb = item % a.nqb;
+  const int b = static_cast<int>(item / a.nqb);
+  const int32_t len = attn_len(a.lens, b, a.nk);
+  const int32_t start = attn_start(a.starts, b, a.nq, a.nk);
+
+  const int row = rt * (32 * RW) + rw * 32 + (lane & 31);
+  const int tok = qb * a.q_block + row / a.group;
+  const int head = h * a.group + row % a.group;
+  const bool real = row < a.rows && tok < a.nq;
+  const int32_t pos = start + tok;
+  const bool live = real && pos >= 0 && pos < len;
+  const int last_row = min(a.rows, (rt + 1) * (32 * RW)) - 1;
+  const int last_tok = min(a.nq - 1, qb * a.q_block + last_row / a.group);
+  const int32_t last_key = min(len - 1, start + last_tok);
+  int32_t open = live ? pos + 1 : INT32_MAX;
+#pragma unroll
+  for (int m = 1; m < 32; m *= 2) open = min(open, __shfl_xor(open, m));
+  open = __builtin_amdgcn_readfirstlane(open);
+
+  const int64_t rid = (static_cast<int64_t>(b) * a.hq + head) * a.nq + tok;
+  u32x4 q[D / 16], g[D / 16];
+  float delta = 0.0f, lse2 = INFINITY;  // a row that sees nothing: every weight 0
+  {
+    const char *qp = a.q.p + (real ? b * a.q.sb + tok * a.q.st + head * a.q.sh : 0) + 16 * h2;
+    const char *gp = a.g.p + (real ? b * a.g.sb + tok * a.g.st + head * a.g.sh : 0) + 16 * h2;
+    const char *op = a.o.p + (real ? b * a.o.sb + tok * a.o.st + head * a.o.sh : 0) + 16 * h2;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+      q[s] = *reinterpret_cast<const u32x4 *>(qp + 32 * s);
+      g[s] = *reinterpret_cast<const u32x4 *>(gp + 32 * s);
+    }
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+      const u32x4 o = *reinterpret_cast<const u32x4 *>(op + 32 * s);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) delta += elem<T>(g[s][i / 2], i & 1) * elem<T>(o[i / 2], i & 1);
+    }
+    delta = add_halves(delta);
+    if (live) {
+      const float x = a.lse[rid];
+      if (x != -INFINITY) lse2 = x * kLog2e;
+    }
+    if (lse2 == INFINITY) delta = 0.0f;
+    if (real && kw == 0 && h2 == 0) a.delta[rid] = delta;
+  }
+
+  const uint32_t stage0 = lds_addr(lds) + kw * 4 * kHalf;
+  const char *stage_p = lds + kw * 4 * kHalf;
+  uint32_t koff[kLoads], voff[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int r = L::load_row(rw * kLoads + i, lane), c = L::load_byte(rw * kLoads + i, lane);
+    koff[i] = static_cast<uint32_t>(r * a.k.st + c);
+    voff[i] = static_cast<uint32_t>(r * a.v.st + c);
+  }
+  f32x16 dq[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) dq[i] = zero16();
+  const float c = a.scale * kLog2e;
+  const int32_t *list = a.lists + ((static_cast<int64_t>(b) * a.hk + h) * a.nqb + qb) * a.max_blocks;
+
+  for (int32_t e = 0; e < a.max_blocks; e += 64) {
+    const Named blocks = named_blocks(list, nullptr, 0, e, a.max_blocks, last_key, lane);
+    const int tiles = blocks.n * kSubs;
+    const int rounds = (tiles - (RW > 1 ? 0 : kw) + KW - 1) / KW;
+    auto issue = [&](int round) {
+      const int t = round * KW + kw;
+      const int id = __builtin_amdgcn_readlane(blocks.id, t < tiles ? t / kSubs : 0);
+      const int64_t key = static_cast<int64_t>(id) * kAttnPage + (t % kSubs) * KT;
+      const int32_t kept = t < tiles ? static_cast<int32_t>(min(static_cast<int64_t>(KT), len - key)) : 0;
+      const i32x4 kbuf = buffer(a.k.p + b * a.k.sb + key * a.k.st + h * a.k.sh,
+                                kept > 0 ? static_cast<int32_t>((kept - 1) * a.k.st + D * 2) : 0);
+      const i32x4 vbuf = buffer(a.v.p + b * a.v.sb + key * a.v.st + h * a.v.sh,
+                                kept > 0 ? static_cast<int32_t>((kept - 1) * a.v.st + D * 2) : 0);
+      const uint32_t st = stage0 + (round & 1) * 2 * kHalf;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        load_lds16(__builtin_amdgcn_readfirstlane(st + (rw * kLoads + i) * 1024), kbuf, koff[i]);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        load_lds16(__builtin_amdgcn_readfirstlane(st + kHalf + (rw * kLoads + i) * 1024), vbuf, voff[i]);
+    };
+    if (rounds > 0) issue(0);
+    for (int round = 0; round < rounds; ++round) {
+      wait_vm<0>();
+      if constexpr (RW > 1) barrier();
+      else wait_lds();
+      if (round + 1 < rounds) issue(round + 1);
+      const char *kt = stage_p + (round & 1) * 2 * kHalf, *vt = kt + kHalf;
+      const int t = round * KW + kw;
+      if (t >= tiles) continue;
+      const int32_t key0 = __builtin_amdgcn_readlane(blocks.id, t / kSubs) * kAttnPage + (t % kSubs) * KT;
+      const bool masked = key0 + KT > open;
+#pragma unroll
+      for (int n = 0; n < KT / 32; ++n) {
+        f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          s = T::mma(L::operand(kt, 32 * n, x, lane), q[x], s);
+          dp = T::mma(L::operand(vt, 32 * n, x, lane), g[x], dp);
+        }
+#pragma unroll
+        for (int e2 = 0; e2 < 16; ++e2) {
+          float p = exp2_(__builtin_fmaf(s[e2], c, -lse2));
+          if (masked) p = key0 + 32 * n + 8 * (e2 >> 2) + 4 * h2 + (e2 & 3) <= min(pos, len - 1) ? p : 0.0f;
+          s[e2] = p * (dp[e2] - delta);
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const u32x4 ds = pack8<T>(s, x);
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) dq[i] = T::mma(L::operand_t(kt, 32 * n + 16 * x, i, lane), ds, dq[i]);
+        }
+      }
+    }
+    if constexpr (RW > 1) barrier();
+    else wait_lds();
+  }
+  if constexpr (KW > 1) {
+    constexpr int kRowsF = D / 2;
+    float *buf = reinterpret_cast<float *>(lds);
+    barrier();
+    if (kw > 0) {
+      float *p = buf + (wave - RW) * kRowsF * 64 + lane;
+#pragma unroll
+      for (int i = 0; i < kRowsF; ++i) p[i * 64] = dq[i / 16][i % 16];
+    }
+    __syncthreads();
+    if (kw > 0) return;
+#pragma unroll
+    for (int gr = 1; gr < KW; ++gr) {
+      const float *p = buf + (gr * RW + rw - RW) * kRowsF * 64 + lane;
+#pragma unroll
+      for (int i = 0; i < kRowsF; ++i) dq[i / 16][i % 16] += p[i * 64];
+    }
+  }
+  if (!real) return;
+  char *out = a.dq.p + b * a.dq.sb + tok * a.dq.st + head * a.dq.sh;
+  const bool none = lse2 == INFINITY;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+    for (int g4 = 0; g4 < 4; ++g4) {
+      u32x2 w;
+      w[0] = none ? 0 : pack2<T>(dq[i][4 * g4] * a.scale, dq[i][4 * g4 + 1] * a.scale);
+      w[1] = none ? 0 : pack2<T>(dq[i][4 * g4 + 2] * a.scale, dq[i][4 * g4 + 3] * a.scale);
+      *reinterpret_cast<u32x2 *>(out + (32 * i + 8 * g4 + 4 * h2) * 2) = w;
+    }
+}
+
+// dk and dv of one item: 64 keys, up to `chunk` query blocks of the inverse
+// list.  RG row groups of two waves; a wave owns 32 keys (K and V rows in
+// registers as B operands) and 32 of the 32 RG rows staged at a time, so that
+// S = Q K^T and dP = dO V^T come out with a key a lane, and P and dS feed
+// dv^T += dO^T P and dk^T += Q^T dS from registers, with dO and Q read
+// transposed from LDS.
+template <class T, int D, int RG>
+__global__ __launch_bounds__(128 * RG) void attn_dkv(const AttnArgs a) {
+  using L = Tile<D>;
+  constexpr int kRows = 32 * RG;
+  constexpr int kHalf = kRows * L::kRowBytes;     // Q or dO of a stage
+  constexpr int kLoads = kHalf / 1024 / (2 * RG);  // direct loads of each, of a wave
+  static_assert(kLoads >= 1 && kLoads * 2 * RG * 1024 == kHalf, "loads of a stage");
+  constexpr int kRowsF = D / 2;
+  static_assert(kRowsF * 2 * 64 * 4 * 2 * (RG - 1) <= 4 * kHalf, "sums of the row groups fit the stages");
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  struct Rows {
+    uint32_t qoff[kRows], goff[kRows];
+  };
+  struct Stats {
+    float lse2[kRows], delta[kRows];
+    int32_t lim[kRows];
+    int32_t open[4];  // 1: every row sees the whole key block
+  };
+  Rows *rows = reinterpret_cast<Rows *>(lds + 4 * kHalf);      // [2]
+  Stats *stats = reinterpret_cast<Stats *>(rows + 2);          // [2]
+  int32_t *ids = reinterpret_cast<int32_t *>(stats + 2);       // [chunk]
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kh = wave & 1, rg = wave >> 1;
+  const int h2 = lane >> 5;
+  int64_t at = blockIdx.x;
+  const int h = at % a.hk;
+  at /= a.hk;
+  const int slot = at % a.slots;
+  const int b = static_cast<int>(at / a.slots);
+  const int64_t bh = static_cast<int64_t>(b) * a.hk + h;
+  const int kb = a.items[2 * (bh * a.slots + slot)];
+  if (kb < 0) return;
+  const int part = a.items[2 * (bh * a.slots + slot) + 1];
+  const int less = a.inv_ptr[2 * (bh * a.nkb + kb)], same = a.inv_ptr[2 * (bh * a.nkb + kb) + 1];
+  const int count = min(a.chunk, same - part * a.chunk);
+  const int32_t len = attn_len(a.lens, b, a.nk);
+  const int32_t start = attn_start(a.starts, b, a.nq, a.nk);
+  {
+    const int32_t *from = a.inv_ids + bh * a.nqb * a.max_blocks + less + part * a.chunk;
+    for (int i = threadIdx.x; i < count; i += 128 * RG) ids[i] = from[i];
+  }
+  const int32_t key = kb * kAttnPage + 32 * kh + (lane & 31);
+  u32x4 kf[D / 16], vf[D / 16];
+#pragma unroll
+  for (int x = 0; x < D / 16; ++x) {
+    kf[x] = vf[x] = u32x4{0, 0, 0, 0};
+    if (key < len) {
+      kf[x] = *reinterpret_cast<const u32x4 *>(a.k.p + b * a.k.sb + key * a.k.st + h * a.k.sh + 32 * x + 16 * h2);
+      vf[x] = *reinterpret_cast<const u32x4 *>(a.v.p + b * a.v.sb + key * a.v.st + h * a.v.sh + 32 * x + 16 * h2);
+    }
+  }
+  __syncthreads();
+
+  const i32x4 qbuf = buffer(a.q.p + b * a.q.sb,
+                            static_cast<int32_t>((a.nq - 1) * a.q.st + (a.hq - 1) * a.q.sh + D * 2));
+  const i32x4 gbuf = buffer(a.g.p + b * a.g.sb,
+                            static_cast<int32_t>((a.nq - 1) * a.g.st + (a.hq - 1) * a.g.sh + D * 2));
+  const int total = count * a.rows;
+  const int rounds = (total + kRows - 1) / kRows;
+  // the row that thread < kRows looks after in a round
+  struct RowOf {
+    int64_t rid;
+    int32_t lim;
+  };
+  auto find = [&](int round) {
+    const int flat = round * kRows + threadIdx.x;
+    RowOf r{0, -1};
+    uint32_t qo = kDeadRow, go = kDeadRow;
+    if (flat < total) {
+      const int e = flat / a.rows, row = flat - e * a.rows;
+      const int t = row / a.group, tok = ids[e] * a.q_block + t, head = h * a.group + row - t * a.group;
+      const int32_t pos = start + tok;
+      if (tok < a.nq && pos >= 0 && pos < len) {
+        r.rid = (static_cast<int64_t>(b) * a.hq + head) * a.nq + tok;
+        r.lim = pos;
+        qo = static_cast<uint32_t>(tok * a.q.st + head * a.q.sh);
+        go = static_cast<uint32_t>(tok * a.g.st + head * a.g.sh);
+      }
+    }
+    rows[round & 1].qoff[threadIdx.x] = qo;
+    rows[round & 1].goff[threadIdx.x] = go;
+    return r;
+  };
+  const bool finder = threadIdx.x < kRows;
+  RowOf mine{0, -1}, later{0, -1};
+  float lse = -INFINITY, delta = 0.0f;
+  auto fetch = [&](const RowOf &r) {
+    lse = r.lim >= 0 ? a.lse[r.rid] : -INFINITY;
+    delta = r.lim >= 0 ? a.delta[r.rid] : 0.0f;
+  };
+  auto issue = [&](int round) {
+    const uint32_t st = lds_addr(lds) + (round & 1) * 2 * kHalf;
+    const Rows &r = rows[round & 1];
+    uint32_t qo[kLoads], go[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int n = wave * kLoads + i;
+      qo[i] = r.qoff[L::load_row(n, lane)] + L::load_byte(n, lane);
+      go[i] = r.goff[L::load_row(n, lane)] + L::load_byte(n, lane);
+    }
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      load_lds16(__builtin_amdgcn_readfirstlane(st + (wave * kLoads + i) * 1024), qbuf, qo[i]);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      load_lds16(__builtin_amdgcn_readfirstlane(st + kHalf + (wave * kLoads + i) * 1024), gbuf, go[i]);
+  };
+  f32x16 dk[D / 32], dv[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    dk[i] = zero16();
+    dv[i] = zero16();
+  }
+  const float c = a.scale * kLog2e;
+  if (rounds > 0) {
+    if (finder) {
+      mine = find(0);
+      fetch(mine);
+      later = find(1);
+    }
+    __syncthreads();
+    issue(0);
+  }
+  for (int round = 0; round < rounds; ++round) {
+    wait_vm<0>();
+    if (finder) {
+      Stats &s = stats[round & 1];
+      s.lse2[threadIdx.x] = lse == -INFINITY ? INFINITY : lse * kLog2e;
+      s.delta[threadIdx.x] = lse == -INFINITY ? 0.0f : delta;
+      s.lim[threadIdx.x] = mine.lim;
+      const bool all = __all(mine.lim < 0 || mine.lim >= kb * kAttnPage + kAttnPage - 1);
+      if (lane == 0) s.open[wave] = all;
+    }
+    barrier();
+    if (round + 1 < rounds) {
+      issue(round + 1);
+      if (finder) {
+        mine = later;
+        fetch(mine);
+        later = find(round + 2);
+      }
+    }
+    const char *qt = lds + (round & 1) * 2 * kHalf, *gt = qt + kHalf;
+    const Stats &st = stats[round & 1];
+    f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+    for (int x = 0; x < D / 16; ++x) {
+      s = T::mma(L::operand(qt, 32 * rg, x, lane), kf[x], s);
+      dp = T::mma(L::operand(gt, 32 * rg, x, lane), vf[x], dp);
+    }
+    const bool masked = st.open[rg / 2] == 0;
+#pragma unroll
+    for (int g4 = 0; g4 < 4; ++g4) {
+      const int r0 = 32 * rg + 8 * g4 + 4 * h2;
+      const f32x4 l4 = *reinterpret_cast<const f32x4 *>(&st.lse2[r0]);
+      const f32x4 d4 = *reinterpret_cast<const f32x4 *>(&st.delta[r0]);
+      const i32x4 m4 = *reinterpret_cast<const i32x4 *>(&st.lim[r0]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float p = exp2_(__builtin_fmaf(s[4 * g4 + i], c, -l4[i]));
+        if (masked) p = key <= m4[i] ? p : 0.0f;
+        s[4 * g4 + i] = p;
+        dp[4 * g4 + i] = p * (dp[4 * g4 + i] - d4[i]);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const u32x4 p = pack8<T>(s, x), ds = pack8<T>(dp, x);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        dv[i] = T::mma(L::operand_t(gt, 32 * rg + 16 * x, i, lane), p, dv[i]);
+        dk[i] = T::mma(L::operand_t(qt, 32 * rg + 16 * x, i, lane), ds, dk[i]);
+      }
+    }
+  }
+  // the row groups' sums, added by the first of them in group order
+  float *buf = reinterpret_cast<float *>(lds);
+  barrier();
+  if (rg > 0) {
+    float *p = buf + (wave - 2) * 2 * kRowsF * 64 + lane;
+#pragma unroll
+    for (int i = 0; i < kRowsF; ++i) {
+      p[i * 64] = dk[i / 16][i % 16];
+      p[(kRowsF + i) * 64] = dv[i / 16][i % 16];
+    }
+  }
+  __syncthreads();
+  if (rg > 0) return;
+#pragma unroll
+  for (int g = 1; g < RG; ++g) {
+    const float *p = buf + (2 * (g - 1) + kh) * 2 * kRowsF * 64 + lane;
+#pragma unroll
+    for (int i = 0; i < kRowsF; ++i) {
+      dk[i / 16][i % 16] += p[i * 64];
+      dv[i / 16][i % 16] += p[(kRowsF + i) * 64];
+    }
+  }
+  if (same > a.chunk) {
+    float *p = a.part_kv + (bh * a.slots + slot) * 2 * kAttnPage * D + (32 * kh + (lane & 31)) * D + 4 * h2;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int g4 = 0; g4 < 4; ++g4) {
+        *reinterpret_cast<f32x4 *>(p + 32 * i + 8 * g4) =
+            f32x4{dk[i][4 * g4], dk[i][4 * g4 + 1], dk[i][4 * g4 + 2], dk[i][4 * g4 + 3]};
+        *reinterpret_cast<f32x4 *>(p + kAttnPage * D + 32 * i + 8 * g4) =
+            f32x4{dv[i][4 * g4], dv[i][4 * g4 + 1], dv[i][4 * g4 + 2], dv[i][4 * g4 + 3]};
+      }
+    return;
+  }
+  if (key >= a.nk) return;
+  char *kp = a.dk.p + b * a.dk.sb + key * a.dk.st + h * a.dk.sh + 8 * h2;
+  char *vp = a.dv.p + b * a.dv.sb + key * a.dv.st + h * a.dv.sh + 8 * h2;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+    for (int g4 = 0; g4 < 4; ++g4) {
+      u32x2 w;
+      w[0] = pack2<T>(dk[i][4 * g4] * a.scale, dk[i][4 * g4 + 1] * a.scale);
+      w[1] = pack2<T>(dk[i][4 * g4 + 2] * a.scale, dk[i][4 * g4 + 3] * a.scale);
+      *reinterpret_cast<u32x2 *>(kp + (32 * i + 8 * g4) * 2) = w;
+      w[0] = pack2<T>(dv[i][4 * g4], dv[i][4 * g4 + 1]);
+      w[1] = pack2<T>(dv[i][4 * g4 + 2], dv[i][4 * g4 + 3]);
+      *reinterpret_cast<u32x2 *>(vp + (32 * i + 8 * g4) * 2) = w;
+    }
+}
+
+// dk and dv of the key blocks that were cut into items: their partial sums in
+// order, four elements a thread.
+template <class T, int D>
+__global__ __launch_bounds__(256) void attn_dkv_merge(const AttnArgs a) {
+  constexpr int kPer = 2 * kAttnPage * D / 4 / 256;  // workgroups of a key block
+  const int64_t which = blockIdx.x / kPer;
+  const int kb = which % a.nkb;
+  const int64_t bh = which / a.nkb;
+  const int less = a.inv_ptr[2 * which], same = a.inv_ptr[2 * which + 1];
+  if (same <= a.chunk) return;
+  const int n = (same + a.chunk - 1) / a.chunk;
+  const int at = ((blockIdx.x % kPer) * 256 + threadIdx.x) * 4;  // in [2][64][D]
+  const float *p = a.part_kv + (bh * a.slots + kb + less / a.chunk) * 2 * kAttnPage * D + at;
+  f32x4 sum = *reinterpret_cast<const f32x4 *>(p);
+  for (int i = 1; i < n; ++i) {
+    const f32x4 x = *reinterpret_cast<const f32x4 *>(p + static_cast<int64_t>(i) * 2 * kAttnPage * D);
+    for (int j = 0; j < 4; ++j) sum[j] += x[j];
+  }
+  const bool is_v = at >= kAttnPage * D;
+  const int32_t key = kb * kAttnPage + (at / D) % kAttnPage;
+  if (key >= a.nk) return;
+  const AttnView &d = is_v ? a.dv : a.dk;
+  const float f = is_v ? 1.0f : a.scale;
+  u32x2 w;
+  w[0] = pack2<T>(sum[0] * f, sum[1] * f);
+  w[1] = pack2<T>(sum[2] * f, sum[3] * f);
+  *reinterpret_cast<u32x2 *>(d.p + (bh / a.hk) * d.sb + key * d.st + (bh % a.hk) * d.sh + (at % D) * 2) = w;
+}
+
+template <class T, int D, int RW, int KW, int KT>
+hipError_t run_dq(const AttnArgs &a, hipStream_t s) {
+  constexpr size_t kLds = static_cast<size_t>(KW) * 4 * KT * D * 2;
+  const int64_t grid = static_cast<int64_t>(a.b) * a.hk * (static_cast<int64_t>(a.nqb) * a.rtiles + a.nkb);
+  if (grid == 0) return hipSuccess;
+  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  hipError_t e = allow_dynamic_lds(reinterpret_cast<const void *>(&attn_dq<T, D, RW, KW, KT>), kLds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((attn_dq<T, D, RW, KW, KT>), dim3(static_cast<unsigned>(grid)), dim3(64 * RW * KW), kLds, s, a);
+  return hipGetLastError();
+}
+
+template <class T, int D>
+hipError_t run_backward(const AttnArgs &a, hipStream_t s) {
+  hipError_t e;
+  switch (attn_tile(a.rows).row_waves) {
+    case 1: e = run_dq<T, D, 1, 4, 32>(a, s); break;
+    case 2: e = run_dq<T, D, 2, 2, 32>(a, s); break;
+    case 4: e = run_dq<T, D, 4, 1, 64>(a, s); break;
+    default: e = run_dq<T, D, 8, 1, 64>(a, s); break;
+  }
+  if (e != hipSuccess || a.nkb == 0) return e;
+  constexpr int kRG = 2;
+  const size_t lds = 4 * 32 * kRG * D * 2 + 2 * (2 * 32 * kRG * 4) + 2 * (3 * 32 * kRG * 4 + 16) +
+                     static_cast<size_t>(a.chunk) * 4;
+  const int64_t grid = static_cast<int64_t>(a.b) * a.hk * a.slots;
+  const int64_t merge = static_cast<int64_t>(a.b) * a.hk * a.nkb * (2 * kAttnPage * D / 4 / 256);
+  if (grid > 0x7fffffff || merge > 0x7fffffff) return hipErrorInvalidValue;
+  e = allow_dynamic_lds(reinterpret_cast<const void *>(&attn_dkv<T, D, kRG>), lds + (kMaxChunk - a.chunk) * 4);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((attn_dkv<T, D, kRG>), dim3(static_cast<unsigned>(grid)), dim3(128 * kRG), lds, s, a);
+  e = hipGetLastError();
+  if (e != hipSuccess || a.slots == a.nkb) return e;
+  hipLaunchKernelGGL((attn_dkv_merge<T, D>), dim3(static_cast<unsigned>(merge)), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace attn
+
+void attn_chunks(int64_t heads, int64_t entries, int32_t rows, int32_t nkb, int32_t *chunk, int32_t *slots) {
+  // about 2048 items (8 a CU), but at least 512 rows an item: its partial
+  // sums cost as much traffic as 128 rows' q and do
+  const int64_t most = heads * entries / 2048 + 1, least = (511 + rows) / rows;
+  const int64_t c = std::min<int64_t>(attn::kMaxChunk, std::max(most, least));
+  *chunk = static_cast<int32_t>(c);
+  // items of key block kb start at kb + (entries before it) / chunk
+  *slots = static_cast<int32_t>(nkb + entries / c);
+}
+
+hipError_t launch_attn_backward(const AttnArgs &a, spmm_dtype_t t, int d, hipStream_t s) {
+  if (t == SPMM_BF16)
+    return d == 64 ? attn::run_backward<attn::Bf16, 64>(a, s) : attn::run_backward<attn::Bf16, 128>(a, s);
+  return d == 64 ? attn::run_backward<attn::F16, 64>(a, s) : attn::run_backward<attn::F16, 128>(a, s);
+}
+
+}  // namespace sdm

@@ -1,0 +1,216 @@
+// attn_dev.h -- device pieces the attention kernels share: element types,
+// staged tiles and their swizzle, direct loads, lists.
+//
+// Every product is an MFMA 32x32x16 with the operands in the order that lets
+// a result feed the next product from its own registers: lane l holds column
+// l % 32, and its element e is row 8 (e / 4) + 4 (l / 32) + e % 4.  Where
+// those rows are contracted next, the 8 elements 8s .. 8s+7 are the B operand
+// of one MFMA if the A operand takes its contraction in the same order, rows
+// 16s + 4h + 0..3 and 16s + 8 + 4h + 0..3 for half-wave h, which is what two
+// transposing 8-byte reads of a staged tile give (operand_t below).
+#pragma once
+
+#include "attn.h"
+
+// load_lds16 names m0 as clobbered on purpose (it sets m0 for the LDS-DMA
+// instruction); clang warns about clobbering a reserved register.
+#pragma clang diagnostic ignored "-Winline-asm"
+
+namespace sdm {
+namespace attn {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct Bf16 {
+  using E = __bf16;
+  __device__ static f32x16 mma(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  }
+};
+struct F16 {
+  using E = _Float16;
+  __device__ static f32x16 mma(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  }
+};
+
+// two floats to the element type, round to nearest even, first in the low half
+template <class T>
+__device__ __forceinline__ unsigned pack2(float x, float y) {
+  typedef typename T::E E2 __attribute__((ext_vector_type(2)));
+  E2 v = {static_cast<typename T::E>(x), static_cast<typename T::E>(y)};
+  return __builtin_bit_cast(unsigned, v);
+}
+// elements 8s .. 8s+7 of a result as an operand
+template <class T>
+__device__ __forceinline__ u32x4 pack8(const f32x16 &x, int s) {
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = pack2<T>(x[8 * s + 2 * i], x[8 * s + 2 * i + 1]);
+  return r;
+}
+template <class T>
+__device__ __forceinline__ float elem(unsigned v, int i) {
+  typedef typename T::E E2 __attribute__((ext_vector_type(2)));
+  return static_cast<float>(__builtin_bit_cast(E2, v)[i]);
+}
+
+__device__ __forceinline__ f32x16 zero16() {
+  f32x16 z;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) z[e] = 0.0f;
+  return z;
+}
+
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// x of this lane and of lane ^ 32, combined.  The halves go through values of
+// their own: a bit cast of a vector's element reads element 0.
+struct Halves {
+  float lo, hi;
+};
+__device__ __forceinline__ Halves halves(float x) {
+  const unsigned u = __builtin_bit_cast(unsigned, x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const unsigned lo = r[0], hi = r[1];
+  return {__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi)};
+}
+__device__ __forceinline__ float max_halves(float x) {
+  const Halves h = halves(x);
+  return fmaxf(h.lo, h.hi);
+}
+__device__ __forceinline__ float add_halves(float x) {
+  const Halves h = halves(x);
+  return h.lo + h.hi;
+}
+
+// s_waitcnt vmcnt(n), leaving the other counters alone
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"i"(N) : "memory");
+}
+
+// Workgroup barrier after this wave's LDS reads have completed (so no read
+// of a stage can still be in flight when another wave refills it), without
+// waiting for the direct loads in flight (their waits are explicit).
+__device__ __forceinline__ void barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// The same for a stage that no other wave reads.
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t lds_addr(const void *p) {
+  return static_cast<uint32_t>(
+      reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) char *)(p)));
+}
+
+// A buffer of `bytes` bytes from base: direct loads past its end write zeros.
+__device__ __forceinline__ i32x4 buffer(const char *base, int32_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  i32x4 r;
+  r[0] = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<uint32_t>(a)));
+  r[1] = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<uint32_t>(a >> 32) & 0xffffu));
+  r[2] = __builtin_amdgcn_readfirstlane(bytes);
+  r[3] = 0x00020000;
+  return r;
+}
+
+// Direct load of 16 bytes per lane: LDS[lds + 16 * lane] = buffer[voff].
+// Inline asm, so the compiler neither waits on it (the kernels count vmcnt
+// themselves) nor assumes later LDS reads depend on it.
+__device__ __forceinline__ void load_lds16(uint32_t lds, i32x4 buf, uint32_t voff) {
+  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :
+               : "s"(lds), "v"(voff), "s"(buf)
+               : "memory", "m0");
+}
+// The same from an address of the lane's own.
+__device__ __forceinline__ void load_lds16(uint32_t lds, const char *p) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off"
+               :
+               : "s"(lds), "v"(p)
+               : "memory", "m0");
+}
+
+// A staged tile: rows of d elements in 16-byte pieces, piece c of row r at
+// piece c ^ f(r).  One f serves both kinds of reads without bank conflicts:
+// 16 consecutive rows at one piece land on 16 distinct pieces of the 256-byte
+// bank row (f is a bijection of r % 16, with two rows to a bank row at d =
+// 64), and so do 4 aligned rows at 4 aligned pieces (the transposing reads),
+// because those rows differ in f's upper bits.
+template <int D>
+struct Tile {
+  static constexpr int kRowBytes = D * 2;
+  static constexpr int kPieces = kRowBytes / 16;
+  static constexpr int kRowsPerLoad = 64 / kPieces;  // rows of a 1 KB direct load
+  __device__ static __forceinline__ int f(int r) {
+    return D == 128 ? (((r & 3) << 2) | ((r >> 2) & 3)) : ((((r >> 1) & 1) << 2) | ((r >> 2) & 3));
+  }
+  // the row and byte of a row that this lane fetches in 1 KB load i
+  __device__ static __forceinline__ int load_row(int i, int lane) { return kRowsPerLoad * i + lane / kPieces; }
+  __device__ static __forceinline__ int load_byte(int i, int lane) {
+    return ((lane % kPieces) ^ f(load_row(i, lane))) * 16;
+  }
+  // A operand over the row: lane l gives row row0 + l % 32, elements
+  // 16 step + 8 (l / 32) + 0..7.  row0 is a multiple of 32.
+  __device__ static __forceinline__ u32x4 operand(const char *t, int row0, int step, int lane) {
+    const int r = lane & 31;
+    return *reinterpret_cast<const u32x4 *>(t + row0 * kRowBytes + r * kRowBytes +
+                                            ((2 * step + (lane >> 5)) ^ f(r)) * 16);
+  }
+  // A operand of the tile's transpose: lane l gives element 32 dt + l % 32 of
+  // rows row0 + 4 (l / 32) + 0..3 and row0 + 8 + 4 (l / 32) + 0..3.  row0 is
+  // a multiple of 16.
+  __device__ static __forceinline__ u32x4 operand_t(const char *t, int row0, int dt, int lane) {
+    const int r = ((lane >> 2) & 3) + 4 * (lane >> 5);
+    const int piece = 4 * dt + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+    const char *p = t + row0 * kRowBytes + (lane & 1) * 8;
+    const u32x2 lo = tr(p + r * kRowBytes + (piece ^ f(r)) * 16);
+    const u32x2 hi = tr(p + (r + 8) * kRowBytes + (piece ^ f(r + 8)) * 16);
+    return u32x4{lo[0], lo[1], hi[0], hi[1]};
+  }
+  __device__ static __forceinline__ u32x2 tr(const char *p) {
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                         (__attribute__((address_space(3))) s16x4 *)(p)));
+  }
+};
+
+// Up to 64 entries e0 .. e1 of a list, one a lane: the blocks they name with
+// a key at or below last_key whose page exists, in order in the first n lanes.
+struct Named {
+  int id, page, n;
+};
+__device__ __forceinline__ Named named_blocks(const int32_t *list, const int32_t *table_row, int32_t pages,
+                                              int32_t e0, int32_t e1, int32_t last_key, int lane) {
+  const int32_t e = e0 + lane;
+  int id = -1, page = -1;
+  if (e < e1) id = list ? list[e] : e;
+  if (attn_names(id, last_key)) page = attn_page(table_row, id, pages);
+  const uint64_t ok = __ballot(page >= 0);
+  const uint32_t lo = static_cast<uint32_t>(ok), hi = static_cast<uint32_t>(ok >> 32);
+  const int before = __builtin_amdgcn_mbcnt_hi(hi, __builtin_amdgcn_mbcnt_lo(lo, 0));
+  const int n = __builtin_popcountll(ok);
+  const int to = page >= 0 ? before : n + lane - before;  // every lane has a place of its own
+  Named r;
+  r.id = __builtin_amdgcn_ds_permute(4 * to, id);
+  r.page = __builtin_amdgcn_ds_permute(4 * to, page);
+  r.n = __builtin_amdgcn_readfirstlane(n);
+  return r;
+}
+
+}  // namespace attn
+}  // namespace sdm

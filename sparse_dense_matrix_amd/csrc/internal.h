@@ -11,6 +11,7 @@
 #include <vector>
 
 #include "../../include/spmm.h"
+#include "attn.h"
 
 namespace sdm {
 
@@ -325,6 +326,7 @@ hipError_t launch_sp24(const Sp24Launch &a, hipStream_t s);
 // ---------------------------------------------------------------------------
 struct spmm_plan_s {
   sdm::Matrix *a = nullptr;
+  bool attn = false;   // plan of spmm_plan_attn: no matrix
   bool sddmm = false;  // plan of spmm_plan_sddmm rather than spmm_plan
   spmm_dtype_t sddmm_dtype = SPMM_F32;  // element type of X and Y
   int32_t device = 0;
@@ -336,6 +338,51 @@ struct spmm_plan_s {
   sdm::Sp24Launch sp24{};
   sdm::SddmmLaunch sdd{};
   sdm::SddmmBcsrLaunch sddb{};
+  spmm_attn_desc_t attn_desc{};
+  sdm::AttnArgs attn_args{};  // shape and workspace; the executes fill in the rest
+  int32_t attn_split_listed[2] = {1, 0};  // ranges and entries of each: lists
+  int32_t attn_split_all[2] = {1, 0};     // ... and every block of a cache
 };
 
 struct spmm_matrix_s : sdm::Matrix {};
+
+// ---------------------------------------------------------------------------
+// what the entry points share (api.cpp, attn.cpp)
+// ---------------------------------------------------------------------------
+namespace sdm {
+
+template <class F>
+spmm_status_t guarded(F &&f) {
+  try {
+    return f();
+  } catch (const std::bad_alloc &) {
+    return fail(SPMM_ERR_OUT_OF_MEMORY, "host allocation failed");
+  } catch (const std::exception &e) {
+    return fail(SPMM_ERR_INTERNAL, e.what());
+  } catch (...) {
+    return fail(SPMM_ERR_INTERNAL, "unknown exception");
+  }
+}
+
+// Restores the caller's current device on scope exit.
+struct DeviceScope {
+  int prev = -1;
+  hipError_t err = hipSuccess;
+  explicit DeviceScope(int dev) {
+    err = hipGetDevice(&prev);
+    if (err == hipSuccess && prev != dev) err = hipSetDevice(dev);
+  }
+  ~DeviceScope() {
+    int cur = -1;
+    if (prev >= 0 && hipGetDevice(&cur) == hipSuccess && cur != prev) (void)hipSetDevice(prev);
+  }
+};
+
+void free_plan(spmm_plan_s *p);
+// hipMalloc of `bytes` of workspace that the plan owns (null for 0 bytes).
+spmm_status_t plan_workspace(spmm_plan_s *p, size_t bytes, void **dst);
+bool plan_log_on();
+// Checks an attention descriptor and fills in the plan's shape (no device).
+spmm_status_t attn_shape(const spmm_attn_desc_t &d, spmm_plan_s *p);
+
+}  // namespace sdm

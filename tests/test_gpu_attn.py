@@ -1,0 +1,535 @@
+"""Block-sparse attention on the GPU against the plain 64-bit form
+(attn_ref.py), whose bounds count the roundings of each output."""
+import math
+
+import pytest
+import torch
+
+import attn_ref as R
+
+pytestmark = pytest.mark.gpu
+PAGE = 64
+
+
+@pytest.fixture(scope="module")
+def S():
+    import sparse_dense_matrix_amd as S
+    assert torch.cuda.is_available()
+    return S
+
+
+def case(b=1, nq=64, nk=None, hq=4, hk=2, d=64, dtype=torch.bfloat16, q_block=64, blocks=4, **kw):
+    return dict(b=b, nq=nq, nk=nq if nk is None else nk, hq=hq, hk=hk, d=d, dtype=dtype, q_block=q_block,
+                blocks=blocks, **kw)
+
+
+def code(S, c):
+    return S.BF16 if c["dtype"] == torch.bfloat16 else S.F16
+
+
+def plan(S, c, **kw):
+    return S.spmm_plan_attn(c["b"], c["nq"], c["nk"], c["hq"], c["hk"], c["d"], dtype=code(S, c),
+                            q_block=c["q_block"], max_blocks=c["blocks"], scale=c.get("scale"), **kw)
+
+
+def inputs(c, seed):
+    g = torch.Generator().manual_seed(seed)
+
+    def make(*shape):
+        return torch.randn(shape, generator=g).to(c["dtype"])
+
+    return (make(c["b"], c["nq"], c["hq"], c["d"]), make(c["b"], c["nk"], c["hk"], c["d"]),
+            make(c["b"], c["nk"], c["hk"], c["d"]), make(c["b"], c["nq"], c["hq"], c["d"]), g)
+
+
+def random_lists(c, g, empty=0.0):
+    """Ascending blocks of the whole sequence, some lists short or empty."""
+    nkb, nqb = -(-c["nk"] // PAGE), -(-c["nq"] // c["q_block"])
+    lists = torch.full((c["b"], c["hk"], nqb, c["blocks"]), -1, dtype=torch.int32)
+    for x in lists.reshape(-1, c["blocks"]):
+        n = 0 if torch.rand(1, generator=g) < empty else int(torch.randint(1, min(nkb, c["blocks"]) + 1, (1,), generator=g))
+        x[:n] = torch.randperm(nkb, generator=g)[:n].sort().values.int()
+    return lists
+
+
+def poison(x):
+    return torch.full_like(x, float("nan"))
+
+
+def dev(x):
+    return None if x is None else x.cuda()
+
+
+def run_forward(S, c, q, k, v, lists, lens, starts, P=None, stream=None):
+    P = P or plan(S, c)
+    o = torch.full((c["b"], c["nq"], c["hq"], c["d"]), float("nan"), dtype=c["dtype"], device="cuda")
+    lse = torch.full((c["b"], c["hq"], c["nq"]), float("nan"), device="cuda")
+    S.spmm_execute_attn(P, q, k, v, lists, o, lse, lens=lens, starts=starts, stream=stream)
+    return o, lse
+
+
+FORWARD = [
+    case(nq=1, nk=1, blocks=1), case(nq=1, nk=65, hq=8, hk=1, d=128), case(nq=63, hq=3, hk=3, q_block=16),
+    case(b=2, nq=130, hq=6, hk=2, q_block=16, dtype=torch.float16), case(nq=200, d=128, hq=8, hk=2),
+    case(nq=129, hq=16, hk=1, q_block=1, blocks=2, d=128), case(nq=40, nk=300, hq=5, hk=1, q_block=4, blocks=5),
+    case(b=3, nq=70, nk=257, hq=8, hk=8, q_block=32, blocks=3, d=128, dtype=torch.float16),
+    case(nq=64, nk=640, hq=10, hk=2, blocks=10, d=128, scale=0.3), case(nq=257, hq=4, hk=4, q_block=64, blocks=70),
+    case(nq=96, nk=4800, hq=2, hk=1, blocks=75, q_block=32),
+]
+
+
+def lengths(c, g, kind):
+    b, nq, nk = c["b"], c["nq"], c["nk"]
+    if kind == "full":
+        lens, starts = [nk] * b, [nk - nq] * b
+    elif kind == "ragged":
+        lens = [int(torch.randint(1, nk + 1, (1,), generator=g)) for _ in range(b)]
+        starts = [max(0, n - nq) for n in lens]
+    else:  # rows before the first key and past the last, empty sequences, odd values
+        lens = [[0, nk // 2, nk + 7][(i + 1) % 3] for i in range(b)]
+        starts = [[-3, nk // 2 - nq // 2, -(2 ** 31)][i % 3] for i in range(b)]
+    return torch.tensor(lens, dtype=torch.int32), torch.tensor(starts, dtype=torch.int32)
+
+
+@pytest.mark.parametrize("kind", ["full", "ragged", "odd"])
+@pytest.mark.parametrize("n", range(len(FORWARD)))
+def test_forward(S, n, kind):
+    c = FORWARD[n]
+    q, k, v, _, g = inputs(c, 100 + n)
+    lens, starts = lengths(c, g, kind)
+    lists = random_lists(c, g, empty=0.2)
+    o, lse = run_forward(S, c, q.cuda(), k.cuda(), v.cuda(), lists.cuda(), lens.cuda(), starts.cuda())
+    w = R.sees(c, lists, lens, starts, None)
+    want = R.attention(c, q.double(), k.double(), v.double(), w)
+    R.check("o", o, *want["o"])
+    R.check("lse", lse, *want["lse"])
+
+
+def test_forward_without_lens(S):
+    c = case(nq=100, blocks=2)
+    q, k, v, _, g = inputs(c, 7)
+    lists = random_lists(c, g)
+    o, lse = run_forward(S, c, q.cuda(), k.cuda(), v.cuda(), lists.cuda(), None, None)
+    want = R.attention(c, q.double(), k.double(), v.double(), R.sees(c, lists, [100], [0], None))
+    R.check("o", o, *want["o"])
+    R.check("lse", lse, *want["lse"])
+
+
+def test_forward_list_entries_that_read_nothing(S):
+    """Ids out of range, gaps of -1, a block named twice."""
+    c = case(nq=64, nk=256, hq=2, hk=1, blocks=6)
+    q, k, v, _, g = inputs(c, 8)
+    lists = torch.tensor([-1, 1, 1, -7, 2 ** 31 - 1, 4], dtype=torch.int32).reshape(1, 1, 1, 6)
+    starts, lens = torch.tensor([150], dtype=torch.int32), torch.tensor([214], dtype=torch.int32)
+    o, lse = run_forward(S, c, q.cuda(), k.cuda(), v.cuda(), lists.cuda(), lens.cuda(), starts.cuda())
+    want = R.attention(c, q.double(), k.double(), v.double(), R.sees(c, lists, lens, starts, None))
+    R.check("o", o, *want["o"])
+    R.check("lse", lse, *want["lse"])
+
+
+def test_forward_ignores_what_stands_past_the_length(S):
+    c = case(b=2, nq=90, hq=4, hk=2, blocks=2, d=128)
+    q, k, v, _, g = inputs(c, 9)
+    lens, starts = torch.tensor([70, 1], dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    k[0, 70:], v[0, 70:], k[1, 1:], v[1, 1:] = float("nan"), float("inf"), float("inf"), float("nan")
+    q[0, 70:], q[1, 1:] = float("nan"), float("inf")
+    lists = torch.tensor([0, 1], dtype=torch.int32).expand(2, 2, 2, 2).contiguous()
+    o, lse = run_forward(S, c, q.cuda(), k.cuda(), v.cuda(), lists.cuda(), lens.cuda(), starts.cuda())
+    want = R.attention(c, q.double(), k.double(), v.double(), R.sees(c, lists, lens, starts, None))
+    R.check("o", o, *want["o"])
+    R.check("lse", lse, *want["lse"])
+
+
+def test_forward_scores_far_apart(S):
+    """Scores over hundreds: the maximum moves, weights underflow to zero."""
+    c = case(nq=64, nk=512, hq=2, hk=1, blocks=8, d=64)
+    q, k, v, _, g = inputs(c, 10)
+    k = (k.float() * torch.linspace(0.1, 40, 512)[None, :, None, None]).to(c["dtype"])
+    lists = torch.arange(8, dtype=torch.int32).reshape(1, 1, 1, 8)
+    starts = torch.tensor([448], dtype=torch.int32)
+    o, lse = run_forward(S, c, q.cuda(), k.cuda(), v.cuda(), lists.cuda(), None, starts.cuda())
+    want = R.attention(c, q.double(), k.double(), v.double(), R.sees(c, lists, [512], starts, None))
+    R.check("o", o, *want["o"])
+    R.check("lse", lse, *want["lse"])
+
+
+def strided(x, how):
+    """The same values with other strides."""
+    if how == "heads first":
+        return x.transpose(1, 2).contiguous().transpose(1, 2)
+    if how == "padded":
+        wide = torch.zeros((*x.shape[:2], x.shape[2] + 1, x.shape[3] + 8), dtype=x.dtype, device=x.device)
+        wide[:, :, 1:, 8:] = x
+        return wide[:, :, 1:, 8:]
+    wide = torch.zeros((x.shape[0], x.shape[1], 3, *x.shape[2:]), dtype=x.dtype, device=x.device)
+    wide[:, :, 1] = x
+    return wide[:, :, 1]
+
+
+@pytest.mark.parametrize("how", ["heads first", "padded", "packed"])
+def test_forward_backward_strides(S, how):
+    c = case(b=2, nq=100, hq=6, hk=2, q_block=16, blocks=2, d=64)
+    q, k, v, grad, g = inputs(c, 11)
+    lists = random_lists(c, g, empty=0.1)
+    base = [t.cuda() for t in (q, k, v, grad)]
+    other = [strided(t, how) for t in base]
+    outs = []
+    for q1, k1, v1, g1 in (base, other):
+        P = plan(S, c, backward=True)
+        o, lse = strided(torch.zeros_like(base[0]), how), torch.zeros((2, 6, 100), device="cuda")
+        if q1 is base[0]:
+            o = o.contiguous()
+        S.spmm_execute_attn(P, q1, k1, v1, lists.cuda(), o, lse)
+        dq, dk, dv = torch.empty_like(q1), torch.empty_like(k1), torch.empty_like(v1)
+        S.spmm_execute_attn_backward(P, g1, q1, k1, v1, lists.cuda(), o, lse, dq, dk, dv)
+        outs.append([t.clone().contiguous() for t in (o, lse, dq, dk, dv)])
+    for x, y in zip(*outs):
+        assert torch.equal(x, y)
+
+
+def test_forward_broadcast_heads(S):
+    c = case(nq=80, hq=4, hk=4, blocks=2)
+    q, k, v, _, g = inputs(c, 12)
+    k, v = k[:, :, :1], v[:, :, :1]
+    lists = random_lists(c, g)
+    o, lse = run_forward(S, c, q.cuda(), k.cuda().expand(-1, -1, 4, -1), v.cuda().expand(-1, -1, 4, -1),
+                         lists.cuda(), None, None)
+    o2, lse2 = run_forward(S, c, q.cuda(), k.cuda().repeat(1, 1, 4, 1), v.cuda().repeat(1, 1, 4, 1),
+                           lists.cuda(), None, None)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+BACKWARD = [
+    case(nq=1, nk=1, blocks=1), case(nq=63, hq=3, hk=3, q_block=16, blocks=1),
+    case(b=2, nq=130, hq=6, hk=2, q_block=16), case(nq=200, d=128, hq=8, hk=2),
+    case(nq=129, hq=16, hk=1, q_block=1, blocks=2, d=128), case(nq=40, nk=300, hq=5, hk=1, q_block=4, blocks=5),
+    case(b=3, nq=70, nk=257, hq=8, hk=8, q_block=32, blocks=3, d=128, dtype=torch.float16),
+    case(nq=64, nk=640, hq=10, hk=2, blocks=10, d=128, scale=0.3), case(nq=700, hq=1, hk=1, q_block=1, blocks=3),
+    case(nq=700, hq=2, hk=1, q_block=64, blocks=3, d=128),
+]
+
+
+@pytest.mark.parametrize("kind", ["full", "ragged", "odd"])
+@pytest.mark.parametrize("n", range(len(BACKWARD)))
+def test_backward(S, n, kind):
+    c = BACKWARD[n]
+    q, k, v, grad, g = inputs(c, 200 + n)
+    lens, starts = lengths(c, g, kind)
+    lists = random_lists(c, g, empty=0.2)
+    for i in range(c["b"]):  # what no query or key uses may hold anything
+        n_i = min(max(int(lens[i]), 0), c["nk"])
+        k[i, n_i:], v[i, n_i:] = float("nan"), float("inf")
+        for t in range(c["nq"]):
+            if not 0 <= int(starts[i]) + t < n_i:
+                q[i, t], grad[i, t] = float("nan"), float("inf")
+    P = plan(S, c, backward=True)
+    o, lse = run_forward(S, c, q.cuda(), k.cuda(), v.cuda(), lists.cuda(), lens.cuda(), starts.cuda(), P)
+    dq, dk, dv = (torch.full_like(t, float("nan")).cuda() for t in (q, k, v))
+    S.spmm_execute_attn_backward(P, grad.cuda(), q.cuda(), k.cuda(), v.cuda(), lists.cuda(), o, lse, dq, dk, dv,
+                                 lens=lens.cuda(), starts=starts.cuda())
+    w = R.sees(c, lists, lens, starts, None)
+    want = R.attention(c, q.double(), k.double(), v.double(), w, grad.double())
+    for name, got in (("o", o), ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv)):
+        R.check(name, got, *want[name])
+
+
+def test_backward_long_inverse_list(S):
+    """One block that every list names: its query blocks are cut into items."""
+    c = case(nq=2600, hq=2, hk=2, q_block=1, blocks=2)
+    q, k, v, grad, g = inputs(c, 30)
+    nqb = c["nq"]
+    lists = torch.zeros((1, 2, nqb, 2), dtype=torch.int32)
+    lists[..., 1] = torch.arange(nqb, dtype=torch.int32) // PAGE
+    lists[..., 1][lists[..., 1] == 0] = -1
+    P = plan(S, c, backward=True)
+    o, lse = run_forward(S, c, q.cuda(), k.cuda(), v.cuda(), lists.cuda(), None, None, P)
+    outs = []
+    for _ in range(2):
+        dq, dk, dv = (torch.full_like(t, float("nan")).cuda() for t in (q, k, v))
+        S.spmm_execute_attn_backward(P, grad.cuda(), q.cuda(), k.cuda(), v.cuda(), lists.cuda(), o, lse, dq, dk, dv)
+        outs.append((dq, dk, dv))
+    assert all(torch.equal(x, y) for x, y in zip(*outs)), "not the same bits twice"
+    nkb = -(-c["nk"] // PAGE)
+    key = torch.arange(c["nk"])
+    t = torch.arange(c["nq"])
+    w = ((key[None] <= t[:, None]) & ((key[None] // PAGE == 0) | (key[None] // PAGE == t[:, None] // PAGE)))
+    w = w.double().expand(1, 2, -1, -1)
+    assert nkb == 41
+    want = R.attention(c, q.double(), k.double(), v.double(), w, grad.double())
+    for name, got in (("o", o), ("lse", lse), ("dq", outs[0][0]), ("dk", outs[0][1]), ("dv", outs[0][2])):
+        R.check(name, got, *want[name])
+
+
+# ---- cache -----------------------------------------------------------------
+
+def paged(c, k, v, g, spare=3):
+    """Pages in an order of their own, NaN in the spare ones."""
+    nkb = -(-c["nk"] // PAGE)
+    pages = c["b"] * nkb + spare
+    table = torch.randperm(pages, generator=g)[:c["b"] * nkb].reshape(c["b"], nkb).int()
+    kp = torch.full((pages, PAGE, c["hk"], c["d"]), float("nan"), dtype=c["dtype"])
+    vp = kp.clone()
+    for x, xp in ((k, kp), (v, vp)):
+        pad = torch.full((c["b"], nkb * PAGE, c["hk"], c["d"]), float("nan"), dtype=c["dtype"])
+        pad[:, :c["nk"]] = x
+        xp[table.long()] = pad.reshape(c["b"], nkb, PAGE, c["hk"], c["d"])
+    return kp, vp, table
+
+
+CACHE = [
+    case(nq=1, nk=64, blocks=2), case(b=3, nq=1, nk=640, hq=8, hk=2, d=128, blocks=3),
+    case(b=2, nq=1, nk=5000 // 64 * 64, hq=4, hk=1, blocks=9), case(b=2, nq=5, nk=448, hq=16, hk=2, d=128, blocks=4),
+    case(b=4, nq=24, nk=384, hq=8, hk=2, d=128, blocks=4, dtype=torch.float16), case(nq=64, nk=1024, hq=16, hk=1, blocks=8),
+    case(b=2, nq=13, nk=192, hq=3, hk=3, blocks=2), case(nq=150, nk=640, hq=4, hk=4, blocks=6, d=128),
+]
+
+
+def run_cache(S, c, q, kp, vp, **kw):
+    o = torch.full((c["b"], c["nq"], c["hq"], c["d"]), float("nan"), dtype=c["dtype"], device="cuda")
+    lse = torch.full((c["b"], c["hq"], c["nq"]), float("nan"), device="cuda")
+    P = plan(S, c)
+    S.spmm_execute_attn_cache(P, q.cuda(), kp.cuda(), vp.cuda(), o, lse, **{n: dev(x) for n, x in kw.items()})
+    return o, lse
+
+
+@pytest.mark.parametrize("kind", ["full", "ragged", "odd"])
+@pytest.mark.parametrize("listed", [False, True])
+@pytest.mark.parametrize("n", range(len(CACHE)))
+def test_cache(S, n, listed, kind):
+    c = CACHE[n]
+    q, k, v, _, g = inputs(c, 300 + n)
+    lens, starts = lengths(c, g, kind)
+    kp, vp, table = paged(c, k, v, g)
+    for i in range(c["b"]):  # a page's keys past the length
+        n_i = min(max(int(lens[i]), 0), c["nk"])
+        if n_i < c["nk"]:
+            kp[table[i, n_i // PAGE].long(), n_i % PAGE:] = float("nan")
+            vp[table[i, n_i // PAGE].long(), n_i % PAGE:] = float("inf")
+    lists = random_lists(c, g, empty=0.1) if listed else None
+    o, lse = run_cache(S, c, q, kp, vp, table=table, lists=lists, lens=lens, starts=starts)
+    want = R.attention(c, q.double(), k.double(), v.double(), R.sees(c, lists, lens, starts, None))
+    R.check("o", o, *want["o"])
+    R.check("lse", lse, *want["lse"])
+
+
+@pytest.mark.parametrize("nq,listed", [(2, False), (24, False), (64, True), (33, True)])
+def test_cache_tree(S, nq, listed):
+    c = case(b=3, nq=nq, nk=320, hq=4, hk=2, d=128, blocks=3)
+    q, k, v, _, g = inputs(c, 400 + nq)
+    lens = torch.tensor([nq, 320, 200], dtype=torch.int32)
+    starts = lens - nq
+    tree = torch.randint(-2 ** 63, 2 ** 63 - 1, (3, nq), generator=g)
+    tree[0, 1] = 0  # no drafted token and no text: nothing is seen
+    kp, vp, table = paged(c, k, v, g)
+    lists = random_lists(c, g) if listed else None
+    o, lse = run_cache(S, c, q, kp, vp, table=table, lists=lists, lens=lens, starts=starts, tree=tree)
+    want = R.attention(c, q.double(), k.double(), v.double(), R.sees(c, lists, lens, starts, tree))
+    R.check("o", o, *want["o"])
+    R.check("lse", lse, *want["lse"])
+    assert torch.isinf(lse[0, :, 1]).all() and (o[0, 1] == 0).all()
+
+
+def test_cache_pages_out_of_range_read_nothing(S):
+    c = case(b=1, nq=2, nk=640, hq=4, hk=2, d=64, blocks=4)
+    q, k, v, _, g = inputs(c, 500)
+    kp, vp, table = paged(c, k, v, g)
+    table[0, 1], table[0, 4], table[0, 9] = -1, kp.shape[0], 2 ** 31 - 1
+    ok = torch.ones((1, 10))
+    ok[0, [1, 4, 9]] = 0
+    starts, lens = torch.tensor([600], dtype=torch.int32), torch.tensor([602], dtype=torch.int32)
+    o, lse = run_cache(S, c, q, kp, vp, table=table, lens=lens, starts=starts)
+    want = R.attention(c, q.double(), k.double(), v.double(), R.sees(c, None, lens, starts, None, ok))
+    R.check("o", o, *want["o"])
+    R.check("lse", lse, *want["lse"])
+
+
+def test_cache_without_pages(S):
+    c = case(b=2, nq=3, nk=300, hq=8, hk=2, d=128, blocks=2)
+    q, k, v, _, g = inputs(c, 501)
+    lens, starts = torch.tensor([300, 129], dtype=torch.int32), torch.tensor([297, 126], dtype=torch.int32)
+    o, lse = run_cache(S, c, q, k, v, lens=lens, starts=starts)
+    want = R.attention(c, q.double(), k.double(), v.double(), R.sees(c, None, lens, starts, None))
+    R.check("o", o, *want["o"])
+    R.check("lse", lse, *want["lse"])
+
+
+# ---- choice of blocks ------------------------------------------------------
+
+SELECT = [
+    case(nq=64, blocks=2), case(b=2, nq=700, hq=6, hk=2, q_block=16, blocks=4), case(nq=900, hq=4, hk=4, q_block=64, blocks=5, d=128),
+    case(nq=400, hq=16, hk=1, q_block=1, blocks=3, d=128, dtype=torch.float16), case(b=3, nq=1, nk=4096, hq=8, hk=2, blocks=16, d=128),
+    case(b=2, nq=9, nk=1000, hq=5, hk=1, blocks=7), case(nq=32, nk=40000, hq=2, hk=1, q_block=32, blocks=600),
+]
+
+
+@pytest.mark.parametrize("kind", ["full", "ragged", "odd"])
+@pytest.mark.parametrize("n", range(len(SELECT)))
+def test_pool_and_select(S, n, kind):
+    c = SELECT[n]
+    q, k, v, _, g = inputs(c, 600 + n)
+    lens, starts = lengths(c, g, kind)
+    nkb, nqb = -(-c["nk"] // PAGE), -(-c["nq"] // c["q_block"])
+    values = torch.zeros((c["b"] * nkb, c["hk"], c["d"]), dtype=torch.int8, device="cuda")
+    scale = torch.zeros((c["b"] * nkb, c["hk"]), device="cuda")
+    sink, local = (1, 1) if n % 2 else (0, 2)
+    P = plan(S, c, sink_blocks=sink, local_blocks=local)
+    S.spmm_execute_attn_pool(P, k.cuda(), values, scale, lens=lens.cuda())
+    rv, rs = R.pool(k, lens, c["nk"])
+    assert torch.equal(values.cpu().reshape(rv.shape), rv)
+    assert torch.equal(scale.cpu().reshape(rs.shape), rs)
+    lists = torch.full((c["b"], c["hk"], nqb, c["blocks"]), -9, dtype=torch.int32, device="cuda")
+    S.spmm_execute_attn_select(P, q.cuda(), values, scale, lists, lens=lens.cuda(), starts=starts.cuda())
+    assert torch.equal(lists.cpu(), R.select(c, q, rv, rs, lens, starts, sink, local))
+
+
+def test_pool_pages_from_first(S):
+    """Only the blocks from `first` on are written; bad pages are not."""
+    c = case(b=3, nq=3, nk=640, hq=4, hk=2, d=128, blocks=3)
+    q, k, v, _, g = inputs(c, 700)
+    kp, vp, table = paged(c, k, v, g)
+    lens = torch.tensor([640, 66, 130], dtype=torch.int32)
+    first = torch.tensor([600, 63, 127], dtype=torch.int32)
+    table[2, 2] = kp.shape[0] + 5
+    values = torch.full((kp.shape[0], 2, 128), 99, dtype=torch.int8, device="cuda")
+    scale = torch.full((kp.shape[0], 2), 99.0, device="cuda")
+    P = plan(S, c)
+    S.spmm_execute_attn_pool(P, kp.cuda(), values, scale, lens=lens.cuda(), table=table.cuda(), first=first.cuda())
+    rv, rs = R.pool(k, lens, c["nk"])
+    written = {int(table[0, 9]): (0, 9), int(table[1, 0]): (1, 0), int(table[1, 1]): (1, 1), int(table[2, 1]): (2, 1)}
+    for p in range(kp.shape[0]):
+        if p in written:
+            assert torch.equal(values[p].cpu(), rv[written[p]]) and torch.equal(scale[p].cpu(), rs[written[p]])
+        else:
+            assert (values[p] == 99).all() and (scale[p] == 99).all()
+
+
+def test_select_ties_and_bad_scores(S):
+    """Equal scores go to the lower block; zeros, infinities, missing pages."""
+    c = case(b=1, nq=1, nk=1280, hq=2, hk=1, d=64, blocks=6)
+    q, k, v, _, g = inputs(c, 701)
+    values = torch.zeros((20, 1, 64), dtype=torch.int8)
+    values[[4, 9, 11, 15], 0, 3] = 5
+    scale = torch.ones((20, 1))
+    scale[11], scale[2] = float("inf"), float("nan")
+    q = torch.zeros_like(q)
+    q[..., 3] = 1.0
+    table = torch.arange(20, dtype=torch.int32).reshape(1, 20)
+    table[0, 4] = -1
+    P = plan(S, c)
+    lists = torch.zeros((1, 1, 1, 6), dtype=torch.int32, device="cuda")
+    starts = torch.tensor([1279], dtype=torch.int32, device="cuda")
+    S.spmm_execute_attn_select(P, q.cuda(), values.cuda(), scale.cuda(), lists, starts=starts, table=table.cuda())
+    # 0 and 19 always; 11 (infinite), 9 and 15, then the lowest zero: 1
+    assert lists.flatten().tolist() == [0, 1, 9, 11, 15, 19]
+    q[..., 5] = float("inf")  # a sum that is not finite: values 0, all scores 0
+    S.spmm_execute_attn_select(P, q.cuda(), values.cuda(), scale.cuda(), lists, starts=starts, table=table.cuda())
+    assert lists.flatten().tolist() == [0, 1, 3, 5, 6, 19]
+
+
+# ---- streams, graphs, refusals ---------------------------------------------
+
+def test_another_stream_and_graph(S):
+    c = case(b=2, nq=200, hq=4, hk=2, q_block=16, blocks=3, d=128)
+    q, k, v, grad, g = inputs(c, 800)
+    lists = random_lists(c, g).cuda()
+    q, k, v, grad = (t.cuda() for t in (q, k, v, grad))
+    P = plan(S, c, backward=True)
+    o, lse = torch.zeros_like(q), torch.zeros((2, 4, 200), device="cuda")
+    dq, dk, dv = torch.zeros_like(q), torch.zeros_like(k), torch.zeros_like(v)
+    values = torch.zeros((2 * 4, 2, 128), dtype=torch.int8, device="cuda")
+    scale = torch.zeros((2 * 4, 2), device="cuda")
+    chosen = torch.zeros_like(lists)
+    outs = (o, lse, dq, dk, dv, values, scale, chosen)
+
+    def step(st):
+        S.spmm_execute_attn_pool(P, k, values, scale, stream=st)
+        S.spmm_execute_attn_select(P, q, values, scale, chosen, stream=st)
+        S.spmm_execute_attn(P, q, k, v, chosen, o, lse, stream=st)
+        S.spmm_execute_attn_backward(P, grad, q, k, v, chosen, o, lse, dq, dk, dv, stream=st)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    step(s)
+    torch.cuda.synchronize()
+    eager = [t.clone() for t in outs]
+    assert all(t.float().abs().sum() > 0 for t in eager)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        step(torch.cuda.current_stream())
+    for rep in range(3):
+        for t in outs:
+            t.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(outs, eager):
+            assert torch.equal(x, y), f"replay {rep}"
+
+
+def test_graph_cache_split(S):
+    c = case(b=1, nq=1, nk=4096, hq=8, hk=2, d=128, blocks=4)
+    q, k, v, _, g = inputs(c, 801)
+    q, k, v = q.cuda(), k.cuda(), v.cuda()
+    P = plan(S, c)
+    assert P.info()["workspace_bytes"] > 0, "the case must cut the sequence into ranges"
+    o, lse = torch.zeros_like(q), torch.zeros((1, 8, 1), device="cuda")
+    starts = torch.tensor([4095], dtype=torch.int32, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    S.spmm_execute_attn_cache(P, q, k, v, o, lse, starts=starts, stream=s)
+    torch.cuda.synchronize()
+    eager = (o.clone(), lse.clone())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        S.spmm_execute_attn_cache(P, q, k, v, o, lse, starts=starts, stream=torch.cuda.current_stream())
+    for rep in range(3):
+        o.zero_(), lse.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, eager[0]) and torch.equal(lse, eager[1])
+
+
+def test_empty_shapes(S):
+    for c in (case(b=0, nq=4, nk=64), case(nq=0, nk=64), case(nq=4, nk=0)):
+        P = plan(S, c, backward=True)
+        q, k, v, grad, _ = inputs(c, 1)
+        q, k, v, grad = (t.cuda() for t in (q, k, v, grad))
+        nqb = -(-c["nq"] // 64)
+        lists = torch.zeros((c["b"], 2, nqb, 4), dtype=torch.int32, device="cuda")
+        o, lse = torch.full_like(q, 9), torch.full((c["b"], 4, c["nq"]), 9.0, device="cuda")
+        S.spmm_execute_attn(P, q, k, v, lists, o, lse)
+        dq, dk, dv = torch.full_like(q, 9), torch.full_like(k, 9), torch.full_like(v, 9)
+        S.spmm_execute_attn_backward(P, grad, q, k, v, lists, o, lse, dq, dk, dv)
+        torch.cuda.synchronize()
+        for t in (o, dq, dk, dv):
+            assert (t == 0).all()
+        assert (lse == -math.inf).all()
+
+
+def test_refusals_of_tensors(S):
+    c = case(nq=8, nk=64)
+    P = plan(S, c)
+    q, k, v, grad, g = inputs(c, 2)
+    q, k, v, grad = (t.cuda() for t in (q, k, v, grad))
+    lists = torch.zeros((1, 2, 1, 4), dtype=torch.int32, device="cuda")
+    o, lse = torch.empty_like(q), torch.empty((1, 4, 8), device="cuda")
+    for bad in (dict(q=q.half()), dict(q=q[:, :7]), dict(k=k.cpu()), dict(lists=lists.long()), dict(lse=lse[:, :3]),
+                dict(v=v.transpose(2, 3).contiguous().transpose(2, 3)), dict(o=o.float())):
+        a = dict(q=q, k=k, v=v, lists=lists, o=o, lse=lse)
+        a.update(bad)
+        with pytest.raises(ValueError):
+            S.spmm_execute_attn(P, *a.values())
+    with pytest.raises(S.SpmmError) as e:  # made without backward
+        S.spmm_execute_attn_backward(P, grad, q, k, v, lists, o, lse, q.clone(), k.clone(), v.clone())
+    assert e.value.name == "SPMM_ERR_INVALID_ARG"
+    odd = torch.empty(q.numel() + 1, dtype=q.dtype, device="cuda")[1:].reshape(q.shape)
+    with pytest.raises(S.SpmmError) as e:
+        S.spmm_execute_attn(P, odd, k, v, lists, o, lse)
+    assert "aligned" in e.value.message
+    with pytest.raises(S.SpmmError):
+        S.spmm_execute(P, q[0, :, 0], o[0, :, 0])
+    with pytest.raises(S.SpmmError):
+        S.spmm_execute_sddmm(P, q[0, :, 0], o[0, :, 0], lse)
