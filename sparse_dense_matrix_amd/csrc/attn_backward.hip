@@ -301,7 +301,7 @@ __global__ __launch_bounds__(64 * RW * KW) void attn_dq(const AttnArgs a) {
 // dv^T += dO^T P and dk^T += Q^T dS from registers, with dO and Q read
 // transposed from LDS.
 template <class T, int D, int RG>
-__global__ __launch_bounds__(128 * RG) void attn_dkv(const AttnArgs a) {
+__global__ __launch_bounds__(128 * RG, 2) void attn_dkv(const AttnArgs a) {
   using L = Tile<D>;
   constexpr int kRows = 32 * RG;
   constexpr int kHalf = kRows * L::kRowBytes;     // Q or dO of a stage

@@ -268,28 +268,48 @@ __global__ __launch_bounds__(64 * RW * KW) void attn_forward(const AttnArgs a) {
   if (h2 == 0) a.lse[rid] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-// The ranges' sums of a row, joined in range order.  A wave takes 64 / (D / 4)
-// rows, four elements a lane.
-template <class T, int D>
-__global__ __launch_bounds__(256) void attn_merge(const AttnArgs a) {
-  constexpr int kLanes = D / 4;
-  const int64_t rows = static_cast<int64_t>(a.b) * a.hq * a.nq;
-  const int64_t rid = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / kLanes;
-  const int at = (threadIdx.x % kLanes) * 4;
-  if (rid >= rows) return;
-  float m = -INFINITY;
-  for (int s = 0; s < a.nsplit; ++s) m = fmaxf(m, a.part_ml[2 * (s * rows + rid)]);
-  float l = 0.0f;
-  f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int s = 0; s < a.nsplit; ++s) {
-    const float ms = a.part_ml[2 * (s * rows + rid)], ls = a.part_ml[2 * (s * rows + rid) + 1];
-    if (ms == -INFINITY && ls == 0.0f) continue;
-    const float f = exp2_(ms - m);
-    const f32x4 p = *reinterpret_cast<const f32x4 *>(a.part_o + (s * rows + rid) * D + at);
-    l += ls * f;
+// The sums m, l, o joined with others of the same row.
+__device__ __forceinline__ void join(float &m, float &l, f32x4 &o, float m2, float l2, f32x4 o2) {
+  if (m2 == -INFINITY && l2 == 0.0f) return;  // nothing was seen, and o2 not written
+  const float next = fmaxf(m, m2);
+  const float f1 = m == -INFINITY ? 0.0f : exp2_(m - next);
+  const float f2 = m2 == -INFINITY ? 0.0f : exp2_(m2 - next);
+  l = l * f1 + l2 * f2;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] += p[i] * f;
+  for (int i = 0; i < 4; ++i) o[i] = o[i] * f1 + o2[i] * f2;
+  m = next;
+}
+
+// The ranges' sums of a row.  `per_row` groups of D / 4 lanes (a power of
+// two, up to the workgroup's) share a row: each joins its ranges, all loads
+// in flight at once, and the first joins the groups in order.  Bound by
+// latency: launch, one round of loads, one exchange through LDS.
+template <class T, int D>
+__global__ __launch_bounds__(256) void attn_merge(const AttnArgs a, int per_row) {
+  constexpr int kLanes = D / 4, kGroups = 256 / kLanes;
+  __shared__ f32x4 so[kGroups][kLanes];
+  __shared__ float sm[kGroups], sl[kGroups];
+  const int64_t rows = static_cast<int64_t>(a.b) * a.hq * a.nq;
+  const int group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes, sub = group % per_row;
+  const int64_t rid = static_cast<int64_t>(blockIdx.x) * (kGroups / per_row) + group / per_row;
+  float m = -INFINITY, l = 0.0f;
+  f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (rid < rows) {
+#pragma unroll 4
+    for (int s = sub; s < a.nsplit; s += per_row) {
+      const int64_t at = s * rows + rid;
+      join(m, l, o, a.part_ml[2 * at], a.part_ml[2 * at + 1],
+           *reinterpret_cast<const f32x4 *>(a.part_o + at * D + 4 * lane));
+    }
   }
+  so[group][lane] = o;
+  if (lane == 0) {
+    sm[group] = m;
+    sl[group] = l;
+  }
+  __syncthreads();
+  if (rid >= rows || sub > 0) return;
+  for (int g = 1; g < per_row; ++g) join(m, l, o, sm[group + g], sl[group + g], so[group + g][lane]);
   const int tok = rid % a.nq;
   const int64_t bh = rid / a.nq;
   char *op = a.o.p + (bh / a.hq) * a.o.sb + tok * a.o.st + (bh % a.hq) * a.o.sh;
@@ -297,8 +317,8 @@ __global__ __launch_bounds__(256) void attn_merge(const AttnArgs a) {
   u32x2 w;
   w[0] = pack2<T>(o[0] * inv, o[1] * inv);
   w[1] = pack2<T>(o[2] * inv, o[3] * inv);
-  *reinterpret_cast<u32x2 *>(op + at * 2) = w;
-  if (at == 0) a.lse[rid] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+  *reinterpret_cast<u32x2 *>(op + lane * 8) = w;
+  if (lane == 0) a.lse[rid] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 template <class T, int D, int RW, int KW, int KT>
@@ -324,10 +344,13 @@ hipError_t run_tile(const AttnArgs &a, hipStream_t s) {
     default: e = run<T, D, 8, 1, 64>(a, s); break;
   }
   if (e != hipSuccess || a.nsplit == 1) return e;
+  constexpr int kGroups = 256 / (D / 4);
+  int per_row = 2;
+  while (per_row < a.nsplit && per_row < kGroups) per_row *= 2;
   const int64_t rows = static_cast<int64_t>(a.b) * a.hq * a.nq;
-  const int64_t grid = (rows * (D / 4) + 255) / 256;
+  const int64_t grid = (rows * per_row + kGroups - 1) / kGroups;
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((attn_merge<T, D>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((attn_merge<T, D>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, a, per_row);
   return hipGetLastError();
 }
 
@@ -335,16 +358,13 @@ hipError_t run_tile(const AttnArgs &a, hipStream_t s) {
 }  // namespace attn
 
 AttnTile attn_tile(int32_t rows) {
-  // the largest workgroup tile that pads the rows least: more rows share a
-  // staged tile of keys
-  int32_t best = 1;
-  int64_t least = INT64_MAX;
-  for (int32_t rw = 8; rw >= 1; rw /= 2) {
-    const int64_t padded = (static_cast<int64_t>(rows) + 32 * rw - 1) / (32 * rw) * (32 * rw);
-    if (padded < least) {
-      least = padded;
-      best = rw;
-    }
+  // one tile for all rows of a query block where that can be: rows in several
+  // tiles stage the same keys again.  Past 256 rows the tile that pads least.
+  int32_t best = 8;
+  if (rows <= 256) {
+    while (best > 1 && 32 * (best / 2) >= rows) best /= 2;
+  } else if ((rows + 127) / 128 % 2 == 1) {
+    best = 4;
   }
   AttnTile t;
   t.row_waves = best;

@@ -141,7 +141,7 @@ __global__ __launch_bounds__(kSelThreads) void attn_select(const AttnSelectArgs 
     double sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     const int rows = (t1 - t0) * a.group;
     const char *p = a.q.p + b * a.q.sb + static_cast<int64_t>(h) * a.group * a.q.sh + (tid % kPieces) * 16;
-#pragma unroll 4
+#pragma unroll 8
     for (int r = tid / kPieces; r < rows; r += kStep) {
       const int t = r / a.group;
       add8<T>(sum, *reinterpret_cast<const u32x4 *>(p + (t0 + t) * a.q.st + (r - t * a.group) * a.q.sh));
@@ -172,53 +172,71 @@ __global__ __launch_bounds__(kSelThreads) void attn_select(const AttnSelectArgs 
     }
     __syncthreads();
   }
-  // scores: D / 16 lanes a block, 16 bytes each
-  constexpr int kLanes = D / 16;
+  // scores: D / 16 lanes a block, 16 bytes each, kBatch blocks of a lane in
+  // flight at once (page, then keys and scale)
+  constexpr int kLanes = D / 16, kStride = kSelThreads / kLanes, kBatch = 8;
   const i32x4 mine = *reinterpret_cast<const i32x4 *>(q8 + 4 * (tid % kLanes));
   const int32_t *table_row = a.table ? a.table + b * a.nkb : nullptr;
-#pragma unroll 4
-  for (int j = tid / kLanes; j < (count + 63) / 64 * 64; j += kSelThreads / kLanes) {
-    int64_t slot = -1;
-    if (j < count) {
-      slot = attn_page(table_row, j, a.pages);
-      if (!table_row) slot += b * a.nkb;
-    }
-    i32x4 v = {0, 0, 0, 0};
-    float scale = NAN;
-    if (slot >= 0) {
-      v = *reinterpret_cast<const i32x4 *>(a.pooled + (slot * a.hk + h) * D + 16 * (tid % kLanes));
-      scale = a.pooled_scale[slot * a.hk + h];
-    }
-    int dot = 0;
+  for (int j0 = 0; j0 < count; j0 += kBatch * kStride) {
+    int64_t slot[kBatch];
+    i32x4 v[kBatch];
+    float scale[kBatch];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) dot = __builtin_amdgcn_sdot4(v[i], mine[i], dot, false);
+    for (int i = 0; i < kBatch; ++i) {
+      const int j = j0 + i * kStride + tid / kLanes;
+      slot[i] = j < count ? attn_page(table_row, j, a.pages) : -1;
+      if (!table_row && slot[i] >= 0) slot[i] += b * a.nkb;
+    }
 #pragma unroll
-    for (int m = 1; m < kLanes; m *= 2) dot += __shfl_xor(dot, m);
-    if (tid % kLanes == 0 && j < count) {
-      // + 0 makes a score of -0 equal to one of 0
-      unsigned k = ordered(static_cast<float>(dot) * scale + 0.0f);
-      if (j < a.sink || j >= count - a.local) k = 0xffffffffu;
-      keys[j] = k;
+    for (int i = 0; i < kBatch; ++i) {
+      v[i] = i32x4{0, 0, 0, 0};
+      scale[i] = NAN;
+      if (slot[i] >= 0) {
+        v[i] = *reinterpret_cast<const i32x4 *>(a.pooled + (slot[i] * a.hk + h) * D + 16 * (tid % kLanes));
+        scale[i] = a.pooled_scale[slot[i] * a.hk + h];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int j = j0 + i * kStride + tid / kLanes;
+      int dot = 0;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) dot = __builtin_amdgcn_sdot4(v[i][w], mine[w], dot, false);
+#pragma unroll
+      for (int m = 1; m < kLanes; m *= 2) dot += __shfl_xor(dot, m);
+      if (tid % kLanes == 0 && j < count) {
+        // + 0 makes a score of -0 equal to one of 0
+        unsigned k = ordered(static_cast<float>(dot) * scale[i] + 0.0f);
+        if (j < a.sink || j >= count - a.local) k = 0xffffffffu;
+        keys[j] = k;
+      }
     }
   }
   __syncthreads();
   if (wave > 0) return;
-  // the largest key that at least max_blocks scores reach
+  // the largest key that at least max_blocks scores reach; the first
+  // kHeld * 64 scores in registers, what is past them read again each time
+  constexpr int kHeld = 8;
+  unsigned held[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) held[i] = i * 64 + lane < count ? keys[i * 64 + lane] : 0;
+  auto reach = [&](unsigned want) {  // want > 0
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) n += __builtin_popcountll(__ballot(held[i] >= want));
+    for (int j = kHeld * 64; j < count; j += 64)
+      n += __builtin_popcountll(__ballot(j + lane < count && keys[j + lane] >= want));
+    return n;
+  };
   unsigned cut = 0;
-  int above = 0;
   for (int bit = 31; bit >= 0; --bit) {
     const unsigned want = cut | (1u << bit);
-    int n = 0;
-    for (int j = lane; j < count; j += 64) n += keys[j] >= want;
-#pragma unroll
-    for (int m = 1; m < 64; m *= 2) n += __shfl_xor(n, m);
+    const int n = reach(want);
     if (n >= a.max_blocks) cut = want;
     if (n == a.max_blocks) break;
   }
   // scores above the cut, and as many at the cut as still fit, lowest first
-  for (int j = lane; j < count; j += 64) above += keys[j] > cut;
-#pragma unroll
-  for (int m = 1; m < 64; m *= 2) above += __shfl_xor(above, m);
+  const int above = cut == 0xffffffffu ? 0 : reach(cut + 1);
   int room = a.max_blocks - above, at = 0;
   for (int j0 = 0; j0 < count && at < a.max_blocks; j0 += 64) {
     const int j = j0 + lane;
