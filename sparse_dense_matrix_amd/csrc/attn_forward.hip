@@ -22,61 +22,235 @@ namespace {
 
 constexpr float kSlack = 8.0f;
 
-// RW waves share each staged tile of KT keys, 32 rows a wave; KW groups of
-// them take the tiles in turn and join their sums at the end.
+// One workgroup's part of the work.  Heads run fastest: with 8 key heads each
+// XCD keeps to one of them.
+struct Item {
+  int h, rt, split, qb, b;
+};
+__device__ __forceinline__ Item item_of(const AttnArgs &a) {
+  int64_t i = blockIdx.x;
+  Item r;
+  r.h = i % a.hk;
+  i /= a.hk;
+  r.rt = i % a.rtiles;
+  i /= a.rtiles;
+  r.split = i % a.nsplit;
+  i /= a.nsplit;
+  r.qb = i % a.nqb;
+  r.b = static_cast<int>(i / a.nqb);
+  return r;
+}
+
+// A lane's row of a tile of tile_rows rows, and what the wave and the
+// workgroup know of their rows together.
+struct Row {
+  int32_t len, start;
+  int tok, head;
+  bool real, live;     // of the tensor; with a position in [0, len)
+  int32_t pos;
+  int32_t last_key;    // the last key any row of the workgroup sees
+  int32_t open;        // keys below it are seen by every live row of the wave
+  uint64_t bits;       // tree mask
+};
+__device__ __forceinline__ Row row_of(const AttnArgs &a, const Item &it, int tile_rows, int row0, int lane) {
+  Row r;
+  r.len = attn_len(a.lens, it.b, a.nk);
+  r.start = attn_start(a.starts, it.b, a.nq, a.nk);
+  const int row = it.rt * tile_rows + row0 + (lane & 31);
+  r.tok = it.qb * a.q_block + row / a.group;
+  r.head = it.h * a.group + row % a.group;
+  r.real = row < a.rows && r.tok < a.nq;
+  r.pos = r.start + r.tok;
+  r.live = r.real && r.pos >= 0 && r.pos < r.len;
+  const int last_row = min(a.rows, (it.rt + 1) * tile_rows) - 1;
+  const int last_tok = min(a.nq - 1, it.qb * a.q_block + last_row / a.group);
+  r.last_key = a.tree ? r.len - 1 : min(r.len - 1, r.start + last_tok);
+  int32_t open = r.live ? (a.tree ? min(r.start, r.len) : r.pos + 1) : INT32_MAX;
+#pragma unroll
+  for (int m = 1; m < 32; m *= 2) open = min(open, __shfl_xor(open, m));
+  r.open = __builtin_amdgcn_readfirstlane(open);
+  r.bits = a.tree && r.real ? a.tree[static_cast<int64_t>(it.b) * a.nq + r.tok] : 0;
+  return r;
+}
+
+template <int D>
+__device__ __forceinline__ void load_q(const AttnArgs &a, const Item &it, const Row &r, int lane, u32x4 *q) {
+  const char *p = a.q.p + (r.real ? it.b * a.q.sb + r.tok * a.q.st + r.head * a.q.sh : 0) + 16 * (lane >> 5);
+#pragma unroll
+  for (int s = 0; s < D / 16; ++s) q[s] = *reinterpret_cast<const u32x4 *>(p + 32 * s);
+}
+
+// The entries [e0, e1) of the item's list that a range takes.
+struct Range {
+  const int32_t *list, *table_row;
+  int32_t e0, e1;
+};
+__device__ __forceinline__ Range range_of(const AttnArgs &a, const Item &it, const Row &r) {
+  Range x;
+  x.list = a.lists ? a.lists + ((static_cast<int64_t>(it.b) * a.hk + it.h) * a.nqb + it.qb) * a.max_blocks : nullptr;
+  x.table_row = a.table ? a.table + static_cast<int64_t>(it.b) * a.nkb : nullptr;
+  x.e0 = it.split * a.per_split;
+  x.e1 = min(a.entries, x.e0 + a.per_split);
+  if (!x.list) x.e1 = min(x.e1, r.last_key < 0 ? 0 : r.last_key / kAttnPage + 1);
+  return x;
+}
+
+// `kept` keys from key `first` of a block on, as a buffer.  Rows past them
+// read as zeros: what stands there may be anything, and a weight of zero does
+// not make a NaN harmless.
+template <int D>
+__device__ __forceinline__ i32x4 keys_of(const AttnArgs &a, const AttnView &x, const Item &it, int id, int page,
+                                         int32_t first, int32_t kept) {
+  const char *p = x.p + it.h * x.sh;
+  if (a.table)
+    p += page * x.sb + first * x.st;
+  else
+    p += it.b * x.sb + (static_cast<int64_t>(id) * kAttnPage + first) * x.st;
+  return buffer(p, kept > 0 ? static_cast<int32_t>((kept - 1) * x.st + D * 2) : 0);
+}
+
+// A row's softmax statistics, base 2; l is this lane's half of the keys.
+struct Stats {
+  float m = -INFINITY, l = 0.0f;
+};
+
+// The scores s of N * 32 keys from key0 on become weights, and o, m and l move
+// with the maximum.
+template <int D, int N>
+__device__ __forceinline__ void softmax(const AttnArgs &a, const Row &r, int32_t key0, int lane, float c, f32x16 *s,
+                                        Stats &st, f32x16 *o) {
+  const int h2 = lane >> 5;
+  if (key0 + 32 * N > r.open) {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int32_t key = key0 + 32 * n + 8 * (e >> 2) + 4 * h2 + (e & 3);
+        bool sees;
+        if (a.tree) {
+          const int32_t draft = key - r.start;
+          sees = key < r.len && (draft < 0 || (draft < 64 && ((r.bits >> (draft & 63)) & 1)));
+        } else {
+          sees = key <= r.pos && key < r.len;
+        }
+        s[n][e] = sees ? s[n][e] : -INFINITY;
+      }
+  }
+  float top = s[0][0];
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) top = fmaxf(top, s[n][e]);
+  top = max_halves(top) * c;
+  if (__any(top > st.m + kSlack)) {
+    const float next = fmaxf(st.m, top);
+    const float f = next == -INFINITY ? 1.0f : exp2_(st.m - next);
+    st.l *= f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[i][e] *= f;
+    st.m = next;
+  }
+  const float from = st.m == -INFINITY ? 0.0f : st.m;
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      s[n][e] = exp2_(__builtin_fmaf(s[n][e], c, -from));
+      st.l += s[n][e];
+    }
+}
+
+// The sums of key groups 1 .. KW - 1 (RW waves each), joined by the first in
+// group order through LDS that nothing else uses by then.
+template <int D, int RW, int KW>
+__device__ __forceinline__ void join_groups(char *lds, int wave, int lane, Stats &st, f32x16 *o) {
+  constexpr int kRowsF = D / 2;  // floats of o a lane holds
+  float *buf = reinterpret_cast<float *>(lds);
+  const int rw = wave % RW;
+  barrier();
+  if (wave >= RW) {
+    float *p = buf + (wave - RW) * (kRowsF + 2) * 64 + lane;
+#pragma unroll
+    for (int i = 0; i < kRowsF; ++i) p[i * 64] = o[i / 16][i % 16];
+    p[kRowsF * 64] = st.m;
+    p[(kRowsF + 1) * 64] = st.l;
+  }
+  __syncthreads();
+  if (wave >= RW) return;
+#pragma unroll
+  for (int g = 1; g < KW; ++g) {
+    const float *p = buf + (g * RW + rw - RW) * (kRowsF + 2) * 64 + lane;
+    const float m2 = p[kRowsF * 64], l2 = p[(kRowsF + 1) * 64];
+    const float next = fmaxf(st.m, m2);
+    const float f1 = st.m == -INFINITY ? 0.0f : exp2_(st.m - next);
+    const float f2 = m2 == -INFINITY ? 0.0f : exp2_(m2 - next);
+#pragma unroll
+    for (int i = 0; i < kRowsF; ++i) o[i / 16][i % 16] = o[i / 16][i % 16] * f1 + p[i * 64] * f2;
+    st.l = st.l * f1 + l2 * f2;
+    st.m = next;
+  }
+}
+
+// o and lse of a row, or its part of them where a list is cut into ranges.
+template <class T, int D>
+__device__ __forceinline__ void store(const AttnArgs &a, const Item &it, const Row &r, int lane, float m, float l,
+                                      const f32x16 *o) {
+  if (!r.real) return;
+  const int h2 = lane >> 5;
+  const int64_t rid = (static_cast<int64_t>(it.b) * a.hq + r.head) * a.nq + r.tok;
+  if (a.nsplit > 1) {
+    const int64_t at = it.split * (static_cast<int64_t>(a.b) * a.hq * a.nq) + rid;
+    if (h2 == 0) {
+      a.part_ml[2 * at] = m;
+      a.part_ml[2 * at + 1] = l;
+    }
+    if (m == -INFINITY && l == 0.0f) return;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        *reinterpret_cast<f32x4 *>(a.part_o + at * D + 32 * i + 8 * g + 4 * h2) =
+            f32x4{o[i][4 * g], o[i][4 * g + 1], o[i][4 * g + 2], o[i][4 * g + 3]};
+    return;
+  }
+  const bool none = l == 0.0f;
+  const float inv = none ? 0.0f : 1.0f / l;
+  char *op = a.o.p + it.b * a.o.sb + r.tok * a.o.st + r.head * a.o.sh;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      u32x2 w;
+      w[0] = none ? 0 : pack2<T>(o[i][4 * g] * inv, o[i][4 * g + 1] * inv);
+      w[1] = none ? 0 : pack2<T>(o[i][4 * g + 2] * inv, o[i][4 * g + 3] * inv);
+      *reinterpret_cast<u32x2 *>(op + (32 * i + 8 * g + 4 * h2) * 2) = w;
+    }
+  if (h2 == 0) a.lse[rid] = none ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// Many rows to a list: RW waves of 32 rows share each staged tile of KT keys;
+// KW groups of them take the tiles in turn.  Two stages: the next tile loads
+// while this one is multiplied.
 template <class T, int D, int RW, int KW, int KT>
-__global__ __launch_bounds__(64 * RW * KW) void attn_forward(const AttnArgs a) {
+__global__ __launch_bounds__(64 * RW * KW, 2) void attn_forward(const AttnArgs a) {
   using L = Tile<D>;
   constexpr int kHalf = KT * L::kRowBytes;  // K or V of a stage
   constexpr int kLoads = kHalf / 1024 / RW;  // direct loads of K, and of V, of a wave
   static_assert(kLoads >= 1 && kLoads * RW * 1024 == kHalf, "loads of a stage");
+  static_assert((KW - 1) * RW * (D / 2 + 2) * 256 <= KW * 4 * kHalf, "the groups' sums fit the stages");
   constexpr int kSubs = kAttnPage / KT;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rw = wave % RW, kw = wave / RW;
-  const int h2 = lane >> 5;
-
-  // heads run fastest: with 8 key heads each XCD keeps to one of them
-  int64_t item = blockIdx.x;
-  const int h = item % a.hk;
-  item /= a.hk;
-  const int rt = item % a.rtiles;
-  item /= a.rtiles;
-  const int split = item % a.nsplit;
-  item /= a.nsplit;
-  const int qb = item % a.nqb;
-  const int b = static_cast<int>(item / a.nqb);
-
-  const int32_t len = attn_len(a.lens, b, a.nk);
-  const int32_t start = attn_start(a.starts, b, a.nq, a.nk);
-
-  // this lane's row
-  const int row = rt * (32 * RW) + rw * 32 + (lane & 31);
-  const int tok = qb * a.q_block + row / a.group;
-  const int head = h * a.group + row % a.group;
-  const bool real = row < a.rows && tok < a.nq;
-  const int32_t pos = start + tok;
-  const bool live = real && pos >= 0 && pos < len;
-  // the last key any row of the workgroup sees
-  const int last_row = min(a.rows, (rt + 1) * (32 * RW)) - 1;
-  const int last_tok = min(a.nq - 1, qb * a.q_block + last_row / a.group);
-  const int32_t last_key = a.tree ? len - 1 : min(len - 1, start + last_tok);
-  // keys below `open` are seen by every live row of the wave
-  int32_t open = live ? (a.tree ? min(start, len) : pos + 1) : INT32_MAX;
-#pragma unroll
-  for (int m = 1; m < 32; m *= 2) open = min(open, __shfl_xor(open, m));
-  open = __builtin_amdgcn_readfirstlane(open);
-  const uint64_t bits = a.tree && real ? a.tree[static_cast<int64_t>(b) * a.nq + tok] : 0;
-
+  const Item it = item_of(a);
+  const Row row = row_of(a, it, 32 * RW, 32 * rw, lane);
+  const Range range = range_of(a, it, row);
   u32x4 q[D / 16];
-  {
-    const int64_t at = real ? b * a.q.sb + tok * a.q.st + head * a.q.sh : 0;
-    const char *p = a.q.p + at + 16 * h2;
-#pragma unroll
-    for (int s = 0; s < D / 16; ++s) q[s] = *reinterpret_cast<const u32x4 *>(p + 32 * s);
-  }
+  load_q<D>(a, it, row, lane, q);
 
   const uint32_t stage0 = lds_addr(lds) + kw * 4 * kHalf;
   const char *stage_p = lds + kw * 4 * kHalf;
@@ -91,58 +265,39 @@ __global__ __launch_bounds__(64 * RW * KW) void attn_forward(const AttnArgs a) {
   f32x16 o[D / 32];
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) o[i] = zero16();
-  float m = -INFINITY, l = 0.0f;
+  Stats st;
   const float c = a.scale * kLog2e;
 
-  const int32_t *list =
-      a.lists ? a.lists + ((static_cast<int64_t>(b) * a.hk + h) * a.nqb + qb) * a.max_blocks : nullptr;
-  const int32_t *table_row = a.table ? a.table + static_cast<int64_t>(b) * a.nkb : nullptr;
-  int32_t e_end = min(a.entries, (split + 1) * a.per_split);
-  if (!list) e_end = min(e_end, last_key < 0 ? 0 : last_key / kAttnPage + 1);
-
-  for (int32_t e = split * a.per_split; e < e_end; e += 64) {
-    const Named blocks = named_blocks(list, table_row, a.pages, e, e_end, last_key, lane);
+  for (int32_t e = range.e0; e < range.e1; e += 64) {
+    const Named blocks = named_blocks(range.list, range.table_row, a.pages, e, range.e1, row.last_key, lane);
     const int tiles = blocks.n * kSubs;
-    // rounds are alike for all key groups where they meet at barriers
-    const int rounds = (tiles - (RW > 1 ? 0 : kw) + KW - 1) / KW;
+    const int rounds = (tiles + KW - 1) / KW;
     auto issue = [&](int round) {
       const int t = round * KW + kw;
       const int at = t < tiles ? t / kSubs : 0;
       const int id = __builtin_amdgcn_readlane(blocks.id, at);
       const int page = __builtin_amdgcn_readlane(blocks.page, at);
-      const int32_t first = (t % kSubs) * KT;  // key of the block the tile starts at
-      const int32_t kept = t < tiles ? min(KT, len - id * kAttnPage - first) : 0;
-      const char *kp, *vp;
-      if (a.table) {
-        kp = a.k.p + page * a.k.sb + first * a.k.st;
-        vp = a.v.p + page * a.v.sb + first * a.v.st;
-      } else {
-        kp = a.k.p + b * a.k.sb + (static_cast<int64_t>(id) * kAttnPage + first) * a.k.st;
-        vp = a.v.p + b * a.v.sb + (static_cast<int64_t>(id) * kAttnPage + first) * a.v.st;
-      }
-      // rows past the length are zeros: what stands there may be anything,
-      // and a weight of zero does not make a NaN harmless
-      const i32x4 kbuf = buffer(kp + h * a.k.sh, kept > 0 ? static_cast<int32_t>((kept - 1) * a.k.st + D * 2) : 0);
-      const i32x4 vbuf = buffer(vp + h * a.v.sh, kept > 0 ? static_cast<int32_t>((kept - 1) * a.v.st + D * 2) : 0);
-      const uint32_t st = stage0 + (round & 1) * 2 * kHalf;
+      const int32_t first = (t % kSubs) * KT;
+      const int32_t kept = t < tiles ? min(KT, row.len - id * kAttnPage - first) : 0;
+      const i32x4 kbuf = keys_of<D>(a, a.k, it, id, page, first, kept);
+      const i32x4 vbuf = keys_of<D>(a, a.v, it, id, page, first, kept);
+      const uint32_t at_lds = stage0 + (round & 1) * 2 * kHalf;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i)
-        load_lds16(__builtin_amdgcn_readfirstlane(st + (rw * kLoads + i) * 1024), kbuf, koff[i]);
+        load_lds16(__builtin_amdgcn_readfirstlane(at_lds + (rw * kLoads + i) * 1024), kbuf, koff[i]);
 #pragma unroll
       for (int i = 0; i < kLoads; ++i)
-        load_lds16(__builtin_amdgcn_readfirstlane(st + kHalf + (rw * kLoads + i) * 1024), vbuf, voff[i]);
+        load_lds16(__builtin_amdgcn_readfirstlane(at_lds + kHalf + (rw * kLoads + i) * 1024), vbuf, voff[i]);
     };
     if (rounds > 0) issue(0);
     for (int round = 0; round < rounds; ++round) {
       wait_vm<0>();
-      if constexpr (RW > 1) barrier();
-      else wait_lds();
+      barrier();
       if (round + 1 < rounds) issue(round + 1);
       const char *kt = stage_p + (round & 1) * 2 * kHalf, *vt = kt + kHalf;
       const int t = round * KW + kw;
       if (t >= tiles) continue;
       const int32_t key0 = __builtin_amdgcn_readlane(blocks.id, t / kSubs) * kAttnPage + (t % kSubs) * KT;
-
       f32x16 s[KT / 32];
 #pragma unroll
       for (int n = 0; n < KT / 32; ++n) {
@@ -150,46 +305,7 @@ __global__ __launch_bounds__(64 * RW * KW) void attn_forward(const AttnArgs a) {
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) s[n] = T::mma(L::operand(kt, 32 * n, x, lane), q[x], s[n]);
       }
-      if (key0 + KT > open) {
-#pragma unroll
-        for (int n = 0; n < KT / 32; ++n)
-#pragma unroll
-          for (int e2 = 0; e2 < 16; ++e2) {
-            const int32_t key = key0 + 32 * n + 8 * (e2 >> 2) + 4 * h2 + (e2 & 3);
-            bool sees;
-            if (a.tree) {
-              const int32_t draft = key - start;
-              sees = key < len && (draft < 0 || (draft < 64 && ((bits >> (draft & 63)) & 1)));
-            } else {
-              sees = key <= pos && key < len;
-            }
-            s[n][e2] = sees ? s[n][e2] : -INFINITY;
-          }
-      }
-      float top = s[0][0];
-#pragma unroll
-      for (int n = 0; n < KT / 32; ++n)
-#pragma unroll
-        for (int e2 = 0; e2 < 16; ++e2) top = fmaxf(top, s[n][e2]);
-      top = max_halves(top) * c;
-      if (__any(top > m + kSlack)) {
-        const float next = fmaxf(m, top);
-        const float f = next == -INFINITY ? 1.0f : exp2_(m - next);
-        l *= f;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-          for (int e2 = 0; e2 < 16; ++e2) o[i][e2] *= f;
-        m = next;
-      }
-      const float from = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-      for (int n = 0; n < KT / 32; ++n)
-#pragma unroll
-        for (int e2 = 0; e2 < 16; ++e2) {
-          s[n][e2] = exp2_(__builtin_fmaf(s[n][e2], c, -from));
-          l += s[n][e2];
-        }
+      softmax<D, KT / 32>(a, row, key0, lane, c, s, st, o);
 #pragma unroll
       for (int n = 0; n < KT / 32; ++n)
 #pragma unroll
@@ -200,72 +316,104 @@ __global__ __launch_bounds__(64 * RW * KW) void attn_forward(const AttnArgs a) {
         }
     }
     // the next entries' first tiles go where the last ones may still be read
-    if constexpr (RW > 1) barrier();
-    else wait_lds();
+    barrier();
   }
 
-  l = add_halves(l);
-  if (!live) {
-    m = -INFINITY;
-    l = 0.0f;
-  }
+  st.l = add_halves(st.l);
+  if (!row.live) st = Stats();
   if constexpr (KW > 1) {
-    // the key groups' sums, joined by the first of them in group order
-    constexpr int kRowsF = D / 2;  // floats of o a lane holds
-    float *buf = reinterpret_cast<float *>(lds);
-    barrier();
-    if (kw > 0) {
-      float *p = buf + (wave - RW) * (kRowsF + 2) * 64 + lane;
-#pragma unroll
-      for (int i = 0; i < kRowsF; ++i) p[i * 64] = o[i / 16][i % 16];
-      p[kRowsF * 64] = m;
-      p[(kRowsF + 1) * 64] = l;
-    }
-    __syncthreads();
+    join_groups<D, RW, KW>(lds, wave, lane, st, o);
     if (kw > 0) return;
-#pragma unroll
-    for (int g = 1; g < KW; ++g) {
-      const float *p = buf + (g * RW + rw - RW) * (kRowsF + 2) * 64 + lane;
-      const float m2 = p[kRowsF * 64], l2 = p[(kRowsF + 1) * 64];
-      const float next = fmaxf(m, m2);
-      const float f1 = m == -INFINITY ? 0.0f : exp2_(m - next);
-      const float f2 = m2 == -INFINITY ? 0.0f : exp2_(m2 - next);
-#pragma unroll
-      for (int i = 0; i < kRowsF; ++i) o[i / 16][i % 16] = o[i / 16][i % 16] * f1 + p[i * 64] * f2;
-      l = l * f1 + l2 * f2;
-      m = next;
-    }
   }
-  if (!real) return;
-  const int64_t rid = (static_cast<int64_t>(b) * a.hq + head) * a.nq + tok;
-  if (a.nsplit > 1) {
-    const int64_t at = split * (static_cast<int64_t>(a.b) * a.hq * a.nq) + rid;
-    if (h2 == 0) {
-      a.part_ml[2 * at] = m;
-      a.part_ml[2 * at + 1] = l;
-    }
-    if (m == -INFINITY && !(l != l)) return;
+  store<T, D>(a, it, row, lane, st.m, st.l, o);
+}
+
+// Up to 32 rows to a list: each wave streams tiles of 32 keys through LDS of
+// its own, without barriers, K and V in one buffer each: the next K loads
+// during the softmax and the product with V, the next V during the scores.
+// Small buffers put 8 waves on a CU (registers allow no more), which covers
+// each wave's waits.  KW waves share a list's tiles and join their sums; with
+// KW = 1 a list is a wave's own.
+template <class T, int D, int KW>
+__global__ __launch_bounds__(64 * KW, 2) void attn_stream(const AttnArgs a) {
+  using L = Tile<D>;
+  constexpr int KT = 32, kSubs = kAttnPage / KT;
+  constexpr int kHalf = KT * L::kRowBytes;
+  constexpr int kLoads = kHalf / 1024;
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Item it = item_of(a);
+  const Row row = row_of(a, it, 32, 0, lane);
+  const Range range = range_of(a, it, row);
+  u32x4 q[D / 16];
+  load_q<D>(a, it, row, lane, q);
+
+  const char *kt = lds + wave * 2 * kHalf, *vt = kt + kHalf;
+  const uint32_t lds_k = __builtin_amdgcn_readfirstlane(lds_addr(kt));
+  uint32_t koff[kLoads], voff[kLoads];
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-      for (int g = 0; g < 4; ++g)
-        *reinterpret_cast<f32x4 *>(a.part_o + at * D + 32 * i + 8 * g + 4 * h2) =
-            f32x4{o[i][4 * g], o[i][4 * g + 1], o[i][4 * g + 2], o[i][4 * g + 3]};
-    return;
+  for (int i = 0; i < kLoads; ++i) {
+    const int r = L::load_row(i, lane), c = L::load_byte(i, lane);
+    koff[i] = static_cast<uint32_t>(r * a.k.st + c);
+    voff[i] = static_cast<uint32_t>(r * a.v.st + c);
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  char *op = a.o.p + b * a.o.sb + tok * a.o.st + head * a.o.sh;
+  f32x16 o[D / 32];
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i)
+  for (int i = 0; i < D / 32; ++i) o[i] = zero16();
+  Stats st;
+  const float c = a.scale * kLog2e;
+
+  for (int32_t e = range.e0; e < range.e1; e += 64) {
+    const Named blocks = named_blocks(range.list, range.table_row, a.pages, e, range.e1, row.last_key, lane);
+    const int tiles = blocks.n * kSubs;
+    // past the last tile the loads are of no bytes, so that the waits below
+    // always count the same loads
+    auto issue = [&](int t, bool values) {
+      const int at = t < tiles ? t / kSubs : 0;
+      const int id = __builtin_amdgcn_readlane(blocks.id, at);
+      const int page = __builtin_amdgcn_readlane(blocks.page, at);
+      const int32_t first = (t % kSubs) * KT;
+      const int32_t kept = t < tiles ? min(KT, row.len - id * kAttnPage - first) : 0;
+      const i32x4 buf = keys_of<D>(a, values ? a.v : a.k, it, id, page, first, kept);
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const bool none = l == 0.0f;
-      u32x2 w;
-      w[0] = none ? 0 : pack2<T>(o[i][4 * g] * inv, o[i][4 * g + 1] * inv);
-      w[1] = none ? 0 : pack2<T>(o[i][4 * g + 2] * inv, o[i][4 * g + 3] * inv);
-      *reinterpret_cast<u32x2 *>(op + (32 * i + 8 * g + 4 * h2) * 2) = w;
+      for (int i = 0; i < kLoads; ++i)
+        load_lds16(lds_k + (values ? kHalf : 0) + i * 1024, buf, values ? voff[i] : koff[i]);
+    };
+    if (wave < tiles) {
+      issue(wave, false);
+      issue(wave, true);
     }
-  if (h2 == 0) a.lse[rid] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+    for (int t = wave; t < tiles; t += KW) {
+      const int32_t key0 = __builtin_amdgcn_readlane(blocks.id, t / kSubs) * kAttnPage + (t % kSubs) * KT;
+      wait_vm<kLoads>();
+      f32x16 s = zero16();
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x) s = T::mma(L::operand(kt, 0, x, lane), q[x], s);
+      wait_lds();
+      issue(t + KW, false);
+      softmax<D, 1>(a, row, key0, lane, c, &s, st, o);
+      wait_vm<kLoads>();
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const u32x4 p = pack8<T>(s, x);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) o[i] = T::mma(L::operand_t(vt, 16 * x, i, lane), p, o[i]);
+      }
+      wait_lds();
+      issue(t + KW, true);
+    }
+    wait_vm<0>();  // the loads of no bytes
+  }
+
+  st.l = add_halves(st.l);
+  if (!row.live) st = Stats();
+  if constexpr (KW > 1) {
+    join_groups<D, 1, KW>(lds, wave, lane, st, o);
+    if (wave > 0) return;
+  }
+  store<T, D>(a, it, row, lane, st.m, st.l, o);
 }
 
 // The sums m, l, o joined with others of the same row.
@@ -321,24 +469,40 @@ __global__ __launch_bounds__(256) void attn_merge(const AttnArgs a, int per_row)
   if (lane == 0) a.lse[rid] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
+int64_t grid_of(const AttnArgs &a) {
+  return static_cast<int64_t>(a.b) * a.hk * a.nqb * a.rtiles * a.nsplit;
+}
+
 template <class T, int D, int RW, int KW, int KT>
 hipError_t run(const AttnArgs &a, hipStream_t s) {
   constexpr size_t kLds = static_cast<size_t>(KW) * 4 * KT * D * 2;
-  const int64_t grid = static_cast<int64_t>(a.b) * a.hk * a.nqb * a.rtiles * a.nsplit;
-  if (grid == 0) return hipSuccess;
-  if (grid > 0x7fffffff) return hipErrorInvalidValue;
   hipError_t e = allow_dynamic_lds(reinterpret_cast<const void *>(&attn_forward<T, D, RW, KW, KT>), kLds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((attn_forward<T, D, RW, KW, KT>), dim3(static_cast<unsigned>(grid)), dim3(64 * RW * KW), kLds,
-                     s, a);
+  hipLaunchKernelGGL((attn_forward<T, D, RW, KW, KT>), dim3(static_cast<unsigned>(grid_of(a))), dim3(64 * RW * KW),
+                     kLds, s, a);
+  return hipGetLastError();
+}
+
+template <class T, int D, int KW>
+hipError_t run_stream(const AttnArgs &a, hipStream_t s) {
+  constexpr size_t kTiles = static_cast<size_t>(KW) * 2 * 32 * D * 2;
+  constexpr size_t kSums = static_cast<size_t>(KW - 1) * (D / 2 + 2) * 256;
+  constexpr size_t kLds = kTiles > kSums ? kTiles : kSums;
+  hipError_t e = allow_dynamic_lds(reinterpret_cast<const void *>(&attn_stream<T, D, KW>), kLds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((attn_stream<T, D, KW>), dim3(static_cast<unsigned>(grid_of(a))), dim3(64 * KW), kLds, s, a);
   return hipGetLastError();
 }
 
 template <class T, int D>
 hipError_t run_tile(const AttnArgs &a, hipStream_t s) {
+  if (grid_of(a) == 0) return hipSuccess;
+  if (grid_of(a) > 0x7fffffff) return hipErrorInvalidValue;
   hipError_t e;
   switch (attn_tile(a.rows).row_waves) {
-    case 1: e = run<T, D, 1, 4, 32>(a, s); break;
+    // a wave a list where there are enough lists to fill the chip (8 waves a
+    // CU) twice over
+    case 1: e = grid_of(a) >= 4096 && a.nsplit == 1 ? run_stream<T, D, 1>(a, s) : run_stream<T, D, 4>(a, s); break;
     case 2: e = run<T, D, 2, 2, 32>(a, s); break;
     case 4: e = run<T, D, 4, 1, 64>(a, s); break;
     default: e = run<T, D, 8, 1, 64>(a, s); break;
