@@ -301,14 +301,12 @@ __global__ __launch_bounds__(64 * RW * KW) void attn_dq(const AttnArgs a) {
 // dv^T += dO^T P and dk^T += Q^T dS from registers, with dO and Q read
 // transposed from LDS.
 template <class T, int D, int RG>
-__global__ __launch_bounds__(128 * RG, 2) void attn_dkv(const AttnArgs a) {
+__global__ __launch_bounds__(128 * RG) void attn_dkv(const AttnArgs a) {
   using L = Tile<D>;
   constexpr int kRows = 32 * RG;
   constexpr int kHalf = kRows * L::kRowBytes;     // Q or dO of a stage
   constexpr int kLoads = kHalf / 1024 / (2 * RG);  // direct loads of each, of a wave
   static_assert(kLoads >= 1 && kLoads * 2 * RG * 1024 == kHalf, "loads of a stage");
-  constexpr int kRowsF = D / 2;
-  static_assert(kRowsF * 2 * 64 * 4 * 2 * (RG - 1) <= 4 * kHalf, "sums of the row groups fit the stages");
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   struct Rows {
     uint32_t qoff[kRows], goff[kRows];
@@ -318,7 +316,7 @@ __global__ __launch_bounds__(128 * RG, 2) void attn_dkv(const AttnArgs a) {
     int32_t lim[kRows];
     int32_t open[4];  // 1: every row sees the whole key block
   };
-  Rows *rows = reinterpret_cast<Rows *>(lds + 4 * kHalf);      // [2]
+  Rows *rows = reinterpret_cast<Rows *>(lds + 4 * kHalf + kAttnPage * L::kRowBytes);  // [2]
   Stats *stats = reinterpret_cast<Stats *>(rows + 2);          // [2]
   int32_t *ids = reinterpret_cast<int32_t *>(stats + 2);       // [chunk]
 
@@ -344,15 +342,28 @@ __global__ __launch_bounds__(128 * RG, 2) void attn_dkv(const AttnArgs a) {
     for (int i = threadIdx.x; i < count; i += 128 * RG) ids[i] = from[i];
   }
   const int32_t key = kb * kAttnPage + 32 * kh + (lane & 31);
-  u32x4 kf[D / 16], vf[D / 16];
+  u32x4 kf[D / 16];
 #pragma unroll
   for (int x = 0; x < D / 16; ++x) {
-    kf[x] = vf[x] = u32x4{0, 0, 0, 0};
-    if (key < len) {
+    kf[x] = u32x4{0, 0, 0, 0};
+    if (key < len)
       kf[x] = *reinterpret_cast<const u32x4 *>(a.k.p + b * a.k.sb + key * a.k.st + h * a.k.sh + 32 * x + 16 * h2);
-      vf[x] = *reinterpret_cast<const u32x4 *>(a.v.p + b * a.v.sb + key * a.v.st + h * a.v.sh + 32 * x + 16 * h2);
+  }
+  const char *vt = lds + 4 * kHalf;  // the block's V
+  {
+    constexpr int kVLoads = kAttnPage * L::kRowBytes / 1024 / (2 * RG);
+    static_assert(kVLoads * 2 * RG * 1024 == kAttnPage * L::kRowBytes, "loads of V");
+    const int32_t kept = min(kAttnPage, len - kb * kAttnPage);
+    const i32x4 vbuf = buffer(a.v.p + b * a.v.sb + static_cast<int64_t>(kb) * kAttnPage * a.v.st + h * a.v.sh,
+                              kept > 0 ? static_cast<int32_t>((kept - 1) * a.v.st + D * 2) : 0);
+#pragma unroll
+    for (int i = 0; i < kVLoads; ++i) {
+      const int n = wave * kVLoads + i;
+      load_lds16(__builtin_amdgcn_readfirstlane(lds_addr(vt) + n * 1024), vbuf,
+                 static_cast<uint32_t>(L::load_row(n, lane) * a.v.st + L::load_byte(n, lane)));
     }
   }
+  wait_vm<0>();
   __syncthreads();
 
   const i32x4 qbuf = buffer(a.q.p + b * a.q.sb,
@@ -450,21 +461,26 @@ __global__ __launch_bounds__(128 * RG, 2) void attn_dkv(const AttnArgs a) {
 #pragma unroll
     for (int x = 0; x < D / 16; ++x) {
       s = T::mma(L::operand(qt, 32 * rg, x, lane), kf[x], s);
-      dp = T::mma(L::operand(gt, 32 * rg, x, lane), vf[x], dp);
+      dp = T::mma(L::operand(gt, 32 * rg, x, lane), L::operand(vt, 32 * kh, x, lane), dp);
     }
     const bool masked = st.open[rg / 2] == 0;
+    if (masked) {
+#pragma unroll
+      for (int g4 = 0; g4 < 4; ++g4) {
+        const i32x4 m4 = *reinterpret_cast<const i32x4 *>(&st.lim[32 * rg + 8 * g4 + 4 * h2]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[4 * g4 + i] = key <= m4[i] ? s[4 * g4 + i] : -INFINITY;
+      }
+    }
 #pragma unroll
     for (int g4 = 0; g4 < 4; ++g4) {
       const int r0 = 32 * rg + 8 * g4 + 4 * h2;
       const f32x4 l4 = *reinterpret_cast<const f32x4 *>(&st.lse2[r0]);
       const f32x4 d4 = *reinterpret_cast<const f32x4 *>(&st.delta[r0]);
-      const i32x4 m4 = *reinterpret_cast<const i32x4 *>(&st.lim[r0]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float p = exp2_(__builtin_fmaf(s[4 * g4 + i], c, -l4[i]));
-        if (masked) p = key <= m4[i] ? p : 0.0f;
-        s[4 * g4 + i] = p;
-        dp[4 * g4 + i] = p * (dp[4 * g4 + i] - d4[i]);
+        s[4 * g4 + i] = exp2_(__builtin_fmaf(s[4 * g4 + i], c, -l4[i]));
+        dp[4 * g4 + i] = s[4 * g4 + i] * (dp[4 * g4 + i] - d4[i]);
       }
     }
 #pragma unroll
@@ -477,56 +493,51 @@ __global__ __launch_bounds__(128 * RG, 2) void attn_dkv(const AttnArgs a) {
       }
     }
   }
-  // the row groups' sums, added by the first of them in group order
+  // the row groups' sums, each group adding a share of them in group order
+  constexpr int kTiles = D / 32;
   float *buf = reinterpret_cast<float *>(lds);
-  barrier();
-  if (rg > 0) {
-    float *p = buf + (wave - 2) * 2 * kRowsF * 64 + lane;
 #pragma unroll
-    for (int i = 0; i < kRowsF; ++i) {
-      p[i * 64] = dk[i / 16][i % 16];
-      p[(kRowsF + i) * 64] = dv[i / 16][i % 16];
+  for (int which = 0; which < 2; ++which) {
+    barrier();
+    {
+      float *p = buf + wave * kTiles * 16 * 64 + lane;
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) p[(i * 16 + e) * 64] = which ? dv[i][e] : dk[i][e];
     }
-  }
-  __syncthreads();
-  if (rg > 0) return;
+    __syncthreads();
+    for (int i = rg; i < kTiles; i += RG) {
+      const float *p = buf + (kh * kTiles + i) * 16 * 64 + lane;
+      f32x16 sum;
 #pragma unroll
-  for (int g = 1; g < RG; ++g) {
-    const float *p = buf + (2 * (g - 1) + kh) * 2 * kRowsF * 64 + lane;
+      for (int e = 0; e < 16; ++e) {
+        float x = p[e * 64];
 #pragma unroll
-    for (int i = 0; i < kRowsF; ++i) {
-      dk[i / 16][i % 16] += p[i * 64];
-      dv[i / 16][i % 16] += p[(kRowsF + i) * 64];
-    }
-  }
-  if (same > a.chunk) {
-    float *p = a.part_kv + (bh * a.slots + slot) * 2 * kAttnPage * D + (32 * kh + (lane & 31)) * D + 4 * h2;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-      for (int g4 = 0; g4 < 4; ++g4) {
-        *reinterpret_cast<f32x4 *>(p + 32 * i + 8 * g4) =
-            f32x4{dk[i][4 * g4], dk[i][4 * g4 + 1], dk[i][4 * g4 + 2], dk[i][4 * g4 + 3]};
-        *reinterpret_cast<f32x4 *>(p + kAttnPage * D + 32 * i + 8 * g4) =
-            f32x4{dv[i][4 * g4], dv[i][4 * g4 + 1], dv[i][4 * g4 + 2], dv[i][4 * g4 + 3]};
+        for (int g = 1; g < RG; ++g) x += p[(2 * g * kTiles * 16 + e) * 64];
+        sum[e] = x;
       }
-    return;
-  }
-  if (key >= a.nk) return;
-  char *kp = a.dk.p + b * a.dk.sb + key * a.dk.st + h * a.dk.sh + 8 * h2;
-  char *vp = a.dv.p + b * a.dv.sb + key * a.dv.st + h * a.dv.sh + 8 * h2;
+      if (same > a.chunk) {
+        float *out = a.part_kv + (bh * a.slots + slot) * 2 * kAttnPage * D + which * kAttnPage * D +
+                     (32 * kh + (lane & 31)) * D + 32 * i + 4 * h2;
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i)
+        for (int g4 = 0; g4 < 4; ++g4)
+          *reinterpret_cast<f32x4 *>(out + 8 * g4) =
+              f32x4{sum[4 * g4], sum[4 * g4 + 1], sum[4 * g4 + 2], sum[4 * g4 + 3]};
+      } else if (key < a.nk) {
+        const AttnView &o = which ? a.dv : a.dk;
+        const float f = which ? 1.0f : a.scale;
+        char *out = o.p + b * o.sb + key * o.st + h * o.sh + 64 * i + 8 * h2;
 #pragma unroll
-    for (int g4 = 0; g4 < 4; ++g4) {
-      u32x2 w;
-      w[0] = pack2<T>(dk[i][4 * g4] * a.scale, dk[i][4 * g4 + 1] * a.scale);
-      w[1] = pack2<T>(dk[i][4 * g4 + 2] * a.scale, dk[i][4 * g4 + 3] * a.scale);
-      *reinterpret_cast<u32x2 *>(kp + (32 * i + 8 * g4) * 2) = w;
-      w[0] = pack2<T>(dv[i][4 * g4], dv[i][4 * g4 + 1]);
-      w[1] = pack2<T>(dv[i][4 * g4 + 2], dv[i][4 * g4 + 3]);
-      *reinterpret_cast<u32x2 *>(vp + (32 * i + 8 * g4) * 2) = w;
+        for (int g4 = 0; g4 < 4; ++g4) {
+          u32x2 w;
+          w[0] = pack2<T>(sum[4 * g4] * f, sum[4 * g4 + 1] * f);
+          w[1] = pack2<T>(sum[4 * g4 + 2] * f, sum[4 * g4 + 3] * f);
+          *reinterpret_cast<u32x2 *>(out + 16 * g4) = w;
+        }
+      }
     }
+  }
 }
 
 // dk and dv of the key blocks that were cut into items: their partial sums in
@@ -580,8 +591,8 @@ hipError_t run_backward(const AttnArgs &a, hipStream_t s) {
     default: e = run_dq<T, D, 8, 1, 64>(a, s); break;
   }
   if (e != hipSuccess || a.nkb == 0) return e;
-  constexpr int kRG = 2;
-  const size_t lds = 4 * 32 * kRG * D * 2 + 2 * (2 * 32 * kRG * 4) + 2 * (3 * 32 * kRG * 4 + 16) +
+  constexpr int kRG = 4;
+  const size_t lds = 4 * 32 * kRG * D * 2 + kAttnPage * D * 2 + 2 * (2 * 32 * kRG * 4) + 2 * (3 * 32 * kRG * 4 + 16) +
                      static_cast<size_t>(a.chunk) * 4;
   const int64_t grid = static_cast<int64_t>(a.b) * a.hk * a.slots;
   const int64_t merge = static_cast<int64_t>(a.b) * a.hk * a.nkb * (2 * kAttnPage * D / 4 / 256);
