@@ -189,6 +189,37 @@ struct Tile {
   }
 };
 
+// N products whose LDS operands are read AHEAD products before their use (the
+// compiler reads each right before it and waits the whole latency out; only
+// scalar and vector arithmetic may move across pin()).  begin() reads the
+// first ones, which may stand before other work.
+__device__ __forceinline__ void pin() { __builtin_amdgcn_sched_barrier(0x406); }
+template <int N, int AHEAD, class R>
+struct Operands {
+  R read;
+  u32x4 buf[N];
+  __device__ __forceinline__ Operands(R r) : read(r) {}
+  __device__ __forceinline__ void begin() {
+#pragma unroll
+    for (int i = 0; i < AHEAD && i < N; ++i) buf[i] = read(i);
+    pin();
+  }
+  template <class M>
+  __device__ __forceinline__ void run(M mul) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (i + AHEAD < N) buf[i + AHEAD] = read(i + AHEAD);
+      pin();
+      mul(i, buf[i]);
+      pin();
+    }
+  }
+};
+template <int N, int AHEAD, class R>
+__device__ __forceinline__ Operands<N, AHEAD, R> operands(R read) {
+  return Operands<N, AHEAD, R>(read);
+}
+
 // Up to 64 entries e0 .. e1 of a list, one a lane: the blocks they name with
 // a key at or below last_key whose page exists, in order in the first n lanes.
 struct Named {

@@ -21,6 +21,7 @@ namespace attn {
 namespace {
 
 constexpr float kSlack = 8.0f;
+constexpr int kAhead = 4;  // operands read ahead of their product
 
 // One workgroup's part of the work.  Heads run fastest: with 8 key heads each
 // XCD keeps to one of them.
@@ -121,20 +122,25 @@ __device__ __forceinline__ void softmax(const AttnArgs &a, const Row &r, int32_t
                                         Stats &st, f32x16 *o) {
   const int h2 = lane >> 5;
   if (key0 + 32 * N > r.open) {
+    if (a.tree) {
+      // the bits of the drafted tokens among the lane's keys, from its first on
+      const int32_t before = r.start - (key0 + 4 * h2);  // keys of the text
 #pragma unroll
-    for (int n = 0; n < N; ++n)
+      for (int n = 0; n < N; ++n)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int32_t key = key0 + 32 * n + 8 * (e >> 2) + 4 * h2 + (e & 3);
-        bool sees;
-        if (a.tree) {
-          const int32_t draft = key - r.start;
-          sees = key < r.len && (draft < 0 || (draft < 64 && ((r.bits >> (draft & 63)) & 1)));
-        } else {
-          sees = key <= r.pos && key < r.len;
+        for (int e = 0; e < 16; ++e) {
+          const int32_t draft = 32 * n + 8 * (e >> 2) + (e & 3) - before;
+          const uint64_t bit = draft < 64 ? r.bits >> (draft & 63) : 0;
+          s[n][e] = (draft < 0 || (bit & 1)) && draft < r.len - r.start ? s[n][e] : -INFINITY;
         }
-        s[n][e] = sees ? s[n][e] : -INFINITY;
-      }
+    } else {
+      const int32_t last = min(r.pos, r.len - 1) - (key0 + 4 * h2);
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          s[n][e] = 32 * n + 8 * (e >> 2) + (e & 3) <= last ? s[n][e] : -INFINITY;
+    }
   }
   float top = s[0][0];
 #pragma unroll
@@ -300,20 +306,18 @@ __global__ __launch_bounds__(64 * RW * KW, 2) void attn_forward(const AttnArgs a
       const int32_t key0 = __builtin_amdgcn_readlane(blocks.id, t / kSubs) * kAttnPage + (t % kSubs) * KT;
       f32x16 s[KT / 32];
 #pragma unroll
-      for (int n = 0; n < KT / 32; ++n) {
-        s[n] = zero16();
-#pragma unroll
-        for (int x = 0; x < D / 16; ++x) s[n] = T::mma(L::operand(kt, 32 * n, x, lane), q[x], s[n]);
-      }
+      for (int n = 0; n < KT / 32; ++n) s[n] = zero16();
+      constexpr int kX = D / 16, kI = D / 32;
+      auto ks = operands<KT / 32 * kX, kAhead>([&](int i) { return L::operand(kt, 32 * (i / kX), i % kX, lane); });
+      ks.begin();
+      ks.run([&](int i, u32x4 k) { s[i / kX] = T::mma(k, q[i % kX], s[i / kX]); });
+      auto vs = operands<KT / 16 * kI, kAhead>([&](int i) { return L::operand_t(vt, 16 * (i / kI), i % kI, lane); });
+      vs.begin();
       softmax<D, KT / 32>(a, row, key0, lane, c, s, st, o);
+      u32x4 p[KT / 16];
 #pragma unroll
-      for (int n = 0; n < KT / 32; ++n)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const u32x4 p = pack8<T>(s[n], x);
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) o[i] = T::mma(L::operand_t(vt, 32 * n + 16 * x, i, lane), p, o[i]);
-        }
+      for (int x = 0; x < KT / 16; ++x) p[x] = pack8<T>(s[x / 2], x % 2);
+      vs.run([&](int i, u32x4 v) { o[i % kI] = T::mma(v, p[i / kI], o[i % kI]); });
     }
     // the next entries' first tiles go where the last ones may still be read
     barrier();
@@ -389,18 +393,18 @@ __global__ __launch_bounds__(64 * KW, 2) void attn_stream(const AttnArgs a) {
       const int32_t key0 = __builtin_amdgcn_readlane(blocks.id, t / kSubs) * kAttnPage + (t % kSubs) * KT;
       wait_vm<kLoads>();
       f32x16 s = zero16();
-#pragma unroll
-      for (int x = 0; x < D / 16; ++x) s = T::mma(L::operand(kt, 0, x, lane), q[x], s);
+      auto ks = operands<D / 16, D / 16>([&](int x) { return L::operand(kt, 0, x, lane); });
+      ks.begin();
+      ks.run([&](int x, u32x4 k) { s = T::mma(k, q[x], s); });
       wait_lds();
       issue(t + KW, false);
       softmax<D, 1>(a, row, key0, lane, c, &s, st, o);
       wait_vm<kLoads>();
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const u32x4 p = pack8<T>(s, x);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) o[i] = T::mma(L::operand_t(vt, 16 * x, i, lane), p, o[i]);
-      }
+      constexpr int kI = D / 32;
+      auto vs = operands<2 * kI, kI>([&](int i) { return L::operand_t(vt, 16 * (i / kI), i % kI, lane); });
+      vs.begin();
+      const u32x4 p[2] = {pack8<T>(s, 0), pack8<T>(s, 1)};
+      vs.run([&](int i, u32x4 v) { o[i % kI] = T::mma(v, p[i / kI], o[i % kI]); });
       wait_lds();
       issue(t + KW, true);
     }
