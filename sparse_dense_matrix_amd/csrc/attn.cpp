@@ -187,12 +187,14 @@ spmm_status_t plan_attn(spmm_plan_s *p) {
   a.part_ml = static_cast<float *>(ptr);
   if (!d.backward) return SPMM_OK;
   const int64_t heads = static_cast<int64_t>(a.b) * a.hk;
-  ATTN_TRY(plan_workspace(p, static_cast<size_t>(rows * 4), &ptr));
-  a.delta = static_cast<float *>(ptr);
+  ATTN_TRY(plan_workspace(p, static_cast<size_t>((rows + 1) * 8), &ptr));
+  a.stats = static_cast<float *>(ptr);
   ATTN_TRY(plan_workspace(p, static_cast<size_t>(heads * a.nqb * a.max_blocks * 4), &ptr));
   a.inv_ids = static_cast<int32_t *>(ptr);
   ATTN_TRY(plan_workspace(p, static_cast<size_t>(heads * a.nkb * 8), &ptr));
   a.inv_ptr = static_cast<int32_t *>(ptr);
+  ATTN_TRY(plan_workspace(p, 8 * 4, &ptr));
+  a.queue = static_cast<int32_t *>(ptr);
   ATTN_TRY(plan_workspace(p, static_cast<size_t>(heads * a.slots * 8), &ptr));
   a.items = static_cast<int32_t *>(ptr);
   if (a.slots > a.nkb) {

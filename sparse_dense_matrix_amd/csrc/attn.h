@@ -29,7 +29,7 @@ struct AttnArgs {
   AttnView q, k, v, o;
   AttnView g, dq, dk, dv;      // gradients (backward)
   float *lse;                  // [b][hq][nq]
-  float *delta;                // [b][hq][nq] workspace: rows' do . o
+  float *stats;                // [b * hq * nq + 1][2] workspace: rows' lse (base 2) and do . o; last: no row's
   const int32_t *lists;        // [b][hk][nqb][max_blocks], or null: every block
   const int32_t *table;        // [b][nkb] pages of the cache, or null
   const uint64_t *tree;        // [b][nq] rows of the drafted tokens' mask, or null
@@ -46,6 +46,7 @@ struct AttnArgs {
   int32_t *inv_ids;            // [b * hk][nqb * max_blocks] query blocks of each key block, key block major
   int32_t *inv_ptr;            // [b * hk][nkb][2] first entry and count of each key block
   int32_t *items;              // [b * hk][slots] key block | chunk pairs, key block -1: none
+  int32_t *queue;              // [8] items taken of each queue of the dk, dv kernel
   int32_t chunk, slots;        // entries of an item; items of a head at most
   float *part_kv;              // [b * hk][slots][2][64][d] partial dk, dv of split key blocks
 };

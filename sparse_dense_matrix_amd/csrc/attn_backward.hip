@@ -23,6 +23,8 @@ namespace sdm {
 namespace attn {
 namespace {
 
+constexpr int kAhead = 4;               // operands read ahead of their product
+constexpr int kCus = 256;
 constexpr int kMaxChunk = 1024;         // query blocks of an item
 constexpr uint32_t kDeadRow = 0xffffff00u;  // offset past every buffer: a direct load gives zeros
 
@@ -132,6 +134,11 @@ __global__ __launch_bounds__(64 * RW * KW) void attn_dq(const AttnArgs a) {
   int64_t item = blockIdx.x;
   const int64_t inverts = static_cast<int64_t>(a.b) * a.hk * a.nkb;
   if (item < inverts) {
+    // the first items of the dk, dv kernel's queues are its workgroups' own
+    if (item == 0 && threadIdx.x < 8) a.queue[threadIdx.x] = kCus / 8;
+    // the statistics of a row that is not there
+    if (item == 0 && threadIdx.x == 0)
+      *reinterpret_cast<f32x2 *>(a.stats + 2 * static_cast<int64_t>(a.b) * a.hq * a.nq) = f32x2{INFINITY, 0.0f};
     invert(a, item, lds);
     return;
   }
@@ -187,7 +194,7 @@ __global__ __launch_bounds__(64 * RW * KW) void attn_dq(const AttnArgs a) {
       if (x != -INFINITY) lse2 = x * kLog2e;
     }
     if (lse2 == INFINITY) delta = 0.0f;
-    if (real && kw == 0 && h2 == 0) a.delta[rid] = delta;
+    if (real && kw == 0 && h2 == 0) *reinterpret_cast<f32x2 *>(a.stats + 2 * rid) = f32x2{lse2, delta};
   }
 
   const uint32_t stage0 = lds_addr(lds) + kw * 4 * kHalf;
@@ -240,23 +247,23 @@ __global__ __launch_bounds__(64 * RW * KW) void attn_dq(const AttnArgs a) {
 #pragma unroll
       for (int n = 0; n < KT / 32; ++n) {
         f32x16 s = zero16(), dp = zero16();
-#pragma unroll
-        for (int x = 0; x < D / 16; ++x) {
-          s = T::mma(L::operand(kt, 32 * n, x, lane), q[x], s);
-          dp = T::mma(L::operand(vt, 32 * n, x, lane), g[x], dp);
-        }
+        auto kv = operands<D / 8, kAhead>([&](int i) { return L::operand(i % 2 ? vt : kt, 32 * n, i / 2, lane); });
+        kv.begin();
+        kv.run([&](int i, u32x4 x) {
+          if (i % 2) dp = T::mma(x, g[i / 2], dp);
+          else s = T::mma(x, q[i / 2], s);
+        });
+        constexpr int kI = D / 32;
+        auto ks = operands<2 * kI, kAhead>([&](int i) { return L::operand_t(kt, 32 * n + 16 * (i / kI), i % kI, lane); });
+        ks.begin();
 #pragma unroll
         for (int e2 = 0; e2 < 16; ++e2) {
           float p = exp2_(__builtin_fmaf(s[e2], c, -lse2));
           if (masked) p = key0 + 32 * n + 8 * (e2 >> 2) + 4 * h2 + (e2 & 3) <= min(pos, len - 1) ? p : 0.0f;
           s[e2] = p * (dp[e2] - delta);
         }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const u32x4 ds = pack8<T>(s, x);
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) dq[i] = T::mma(L::operand_t(kt, 32 * n + 16 * x, i, lane), ds, dq[i]);
-        }
+        const u32x4 ds[2] = {pack8<T>(s, 0), pack8<T>(s, 1)};
+        ks.run([&](int i, u32x4 k) { dq[i % kI] = T::mma(k, ds[i / kI], dq[i % kI]); });
       }
     }
     if constexpr (RW > 1) barrier();
@@ -294,37 +301,61 @@ __global__ __launch_bounds__(64 * RW * KW) void attn_dq(const AttnArgs a) {
     }
 }
 
+// x / d for d > 0, with inv = 0xffffffff / d: the product is at most one below
+__device__ __forceinline__ uint32_t over(uint32_t x, uint32_t d, uint32_t inv) {
+  const uint32_t r = __umulhi(x, inv);
+  return x - r * d >= d ? r + 1 : r;
+}
+
+// The kernel's arguments, read again: what a loop's body needs of them would
+// otherwise be kept in scalar registers throughout, more than there are.
+__device__ __forceinline__ AttnArgs args_again() {
+  typedef const __attribute__((address_space(4))) uint32_t *Words;
+  Words p = (Words)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  struct {
+    uint32_t w[sizeof(AttnArgs) / 4];
+  } x;
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(AttnArgs) / 4; ++i) x.w[i] = p[i];
+  return __builtin_bit_cast(AttnArgs, x);
+}
+
 // dk and dv of one item: 64 keys, up to `chunk` query blocks of the inverse
-// list.  RG row groups of two waves; a wave owns 32 keys (K and V rows in
-// registers as B operands) and 32 of the 32 RG rows staged at a time, so that
-// S = Q K^T and dP = dO V^T come out with a key a lane, and P and dS feed
+// list.  RG row groups of two waves; a wave owns 32 keys (K rows in registers
+// as B operands, V rows in LDS) and 32 of the 32 RG rows staged at a time, so
+// that S = Q K^T and dP = dO V^T come out with a key a lane, and P and dS feed
 // dv^T += dO^T P and dk^T += Q^T dS from registers, with dO and Q read
-// transposed from LDS.
+// transposed from LDS.  dk and dv fill half of a wave's 256 registers, which
+// is why V stays in LDS: with V in registers too the kernel spills (1502 us
+// against 1022 us for 16k tokens, 32 heads over 8, 1024 keys a query).
+// 64 keys and 512 registers a wave halve the LDS reads, but one wave a SIMD
+// waits for each of them: 1218 us.
 template <class T, int D, int RG>
-__global__ __launch_bounds__(128 * RG) void attn_dkv(const AttnArgs a) {
+__device__ __forceinline__ void dkv_item(const AttnArgs &a, char *lds, int64_t at) {
   using L = Tile<D>;
   constexpr int kRows = 32 * RG;
   constexpr int kHalf = kRows * L::kRowBytes;     // Q or dO of a stage
   constexpr int kLoads = kHalf / 1024 / (2 * RG);  // direct loads of each, of a wave
   static_assert(kLoads >= 1 && kLoads * 2 * RG * 1024 == kHalf, "loads of a stage");
-  extern __shared__ __attribute__((aligned(1024))) char lds[];
   struct Rows {
     uint32_t qoff[kRows], goff[kRows];
   };
   struct Stats {
     float lse2[kRows], delta[kRows];
     int32_t lim[kRows];
-    int32_t open[4];  // 1: every row sees the whole key block
+    int32_t open[4];  // of 64 rows each, 1: every row sees the whole key block
   };
   Rows *rows = reinterpret_cast<Rows *>(lds + 4 * kHalf + kAttnPage * L::kRowBytes);  // [2]
-  Stats *stats = reinterpret_cast<Stats *>(rows + 2);          // [2]
-  int32_t *ids = reinterpret_cast<int32_t *>(stats + 2);       // [chunk]
+  Stats *stats = reinterpret_cast<Stats *>(rows + 2);     // [4]
+  int32_t *ids = reinterpret_cast<int32_t *>(stats + 4);  // [chunk]
 
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));  // nothing of an item's is kept for the next
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int kh = wave & 1, rg = wave >> 1;
   const int h2 = lane >> 5;
-  int64_t at = blockIdx.x;
   const int h = at % a.hk;
   at /= a.hk;
   const int slot = at % a.slots;
@@ -339,7 +370,7 @@ __global__ __launch_bounds__(128 * RG) void attn_dkv(const AttnArgs a) {
   const int32_t start = attn_start(a.starts, b, a.nq, a.nk);
   {
     const int32_t *from = a.inv_ids + bh * a.nqb * a.max_blocks + less + part * a.chunk;
-    for (int i = threadIdx.x; i < count; i += 128 * RG) ids[i] = from[i];
+    for (int i = tid; i < count; i += 128 * RG) ids[i] = from[i];
   }
   const int32_t key = kb * kAttnPage + 32 * kh + (lane & 31);
   u32x4 kf[D / 16];
@@ -363,6 +394,10 @@ __global__ __launch_bounds__(128 * RG) void attn_dkv(const AttnArgs a) {
                  static_cast<uint32_t>(L::load_row(n, lane) * a.v.st + L::load_byte(n, lane)));
     }
   }
+  // the compiler does not see the waits in asm: here it waits for K itself,
+  // and not again in each round, where that would wait for the round's loads
+#pragma unroll
+  for (int x = 0; x < D / 16; ++x) asm volatile("" : "+v"(kf[x]));
   wait_vm<0>();
   __syncthreads();
 
@@ -370,39 +405,41 @@ __global__ __launch_bounds__(128 * RG) void attn_dkv(const AttnArgs a) {
                             static_cast<int32_t>((a.nq - 1) * a.q.st + (a.hq - 1) * a.q.sh + D * 2));
   const i32x4 gbuf = buffer(a.g.p + b * a.g.sb,
                             static_cast<int32_t>((a.nq - 1) * a.g.st + (a.hq - 1) * a.g.sh + D * 2));
-  const int total = count * a.rows;
-  const int rounds = (total + kRows - 1) / kRows;
-  // the row that thread < kRows looks after in a round
-  struct RowOf {
-    int64_t rid;
-    int32_t lim;
-  };
+  const uint32_t total = static_cast<uint32_t>(count) * a.rows;
+  const int rounds = static_cast<int>((total + kRows - 1) / kRows);
+  const uint32_t per_list = 0xffffffffu / static_cast<uint32_t>(a.rows);
+  const uint32_t per_token = 0xffffffffu / static_cast<uint32_t>(a.group);
+  // Threads below kRows look after a row each, two rounds ahead: its offsets
+  // for the direct loads, its limit, and its statistics on their way to LDS.
+  // Rows that are not there read zeros, and statistics that make their weights 0.
   auto find = [&](int round) {
-    const int flat = round * kRows + threadIdx.x;
-    RowOf r{0, -1};
+    const uint32_t flat = static_cast<uint32_t>(round) * kRows + tid;
+    Stats &s = stats[round & 3];
     uint32_t qo = kDeadRow, go = kDeadRow;
+    int32_t lim = INT32_MAX;
+    int64_t rid = static_cast<int64_t>(a.b) * a.hq * a.nq;
     if (flat < total) {
-      const int e = flat / a.rows, row = flat - e * a.rows;
-      const int t = row / a.group, tok = ids[e] * a.q_block + t, head = h * a.group + row - t * a.group;
+      const uint32_t e = over(flat, a.rows, per_list), row = flat - e * a.rows;
+      const uint32_t t = over(row, a.group, per_token);
+      const int tok = ids[e] * a.q_block + static_cast<int>(t);
+      const int head = h * a.group + static_cast<int>(row - t * a.group);
       const int32_t pos = start + tok;
       if (tok < a.nq && pos >= 0 && pos < len) {
-        r.rid = (static_cast<int64_t>(b) * a.hq + head) * a.nq + tok;
-        r.lim = pos;
+        rid = (static_cast<int64_t>(b) * a.hq + head) * a.nq + tok;
+        lim = pos;
         qo = static_cast<uint32_t>(tok * a.q.st + head * a.q.sh);
         go = static_cast<uint32_t>(tok * a.g.st + head * a.g.sh);
       }
     }
-    rows[round & 1].qoff[threadIdx.x] = qo;
-    rows[round & 1].goff[threadIdx.x] = go;
-    return r;
+    rows[round & 1].qoff[tid] = qo;
+    rows[round & 1].goff[tid] = go;
+    s.lim[tid] = lim;
+    const bool all = __all(lim >= kb * kAttnPage + kAttnPage - 1);
+    if (lane == 0) s.open[wave] = all;
+    load_lds4(__builtin_amdgcn_readfirstlane(lds_addr(&s.lse2[64 * wave])), a.stats + 2 * rid);
+    load_lds4(__builtin_amdgcn_readfirstlane(lds_addr(&s.delta[64 * wave])), a.stats + 2 * rid + 1);
   };
-  const bool finder = threadIdx.x < kRows;
-  RowOf mine{0, -1}, later{0, -1};
-  float lse = -INFINITY, delta = 0.0f;
-  auto fetch = [&](const RowOf &r) {
-    lse = r.lim >= 0 ? a.lse[r.rid] : -INFINITY;
-    delta = r.lim >= 0 ? a.delta[r.rid] : 0.0f;
-  };
+  const bool finder = wave < kRows / 64;
   auto issue = [&](int round) {
     const uint32_t st = lds_addr(lds) + (round & 1) * 2 * kHalf;
     const Rows &r = rows[round & 1];
@@ -429,40 +466,41 @@ __global__ __launch_bounds__(128 * RG) void attn_dkv(const AttnArgs a) {
   const float c = a.scale * kLog2e;
   if (rounds > 0) {
     if (finder) {
-      mine = find(0);
-      fetch(mine);
-      later = find(1);
+      find(0);
+      find(1);
     }
     __syncthreads();
     issue(0);
   }
   for (int round = 0; round < rounds; ++round) {
     wait_vm<0>();
-    if (finder) {
-      Stats &s = stats[round & 1];
-      s.lse2[threadIdx.x] = lse == -INFINITY ? INFINITY : lse * kLog2e;
-      s.delta[threadIdx.x] = lse == -INFINITY ? 0.0f : delta;
-      s.lim[threadIdx.x] = mine.lim;
-      const bool all = __all(mine.lim < 0 || mine.lim >= kb * kAttnPage + kAttnPage - 1);
-      if (lane == 0) s.open[wave] = all;
-    }
     barrier();
-    if (round + 1 < rounds) {
-      issue(round + 1);
-      if (finder) {
-        mine = later;
-        fetch(mine);
-        later = find(round + 2);
-      }
-    }
+    if (round + 1 < rounds) issue(round + 1);
+    if (round + 2 < rounds && finder) find(round + 2);
     const char *qt = lds + (round & 1) * 2 * kHalf, *gt = qt + kHalf;
-    const Stats &st = stats[round & 1];
+    const Stats &st = stats[round & 3];
     f32x16 s = zero16(), dp = zero16();
+    constexpr int AQ = 1;
+    auto qs = operands<D / 16, AQ>([&](int x) { return L::operand(qt, 32 * rg, x, lane); });
+    auto gs = operands<D / 16, AQ>([&](int x) { return L::operand(gt, 32 * rg, x, lane); });
+    auto vs = operands<D / 16, AQ>([&](int x) { return L::operand(vt, 32 * kh, x, lane); });
+    qs.begin();
+    gs.begin();
+    vs.begin();
 #pragma unroll
     for (int x = 0; x < D / 16; ++x) {
-      s = T::mma(L::operand(qt, 32 * rg, x, lane), kf[x], s);
-      dp = T::mma(L::operand(gt, 32 * rg, x, lane), L::operand(vt, 32 * kh, x, lane), dp);
+      qs.next(x);
+      gs.next(x);
+      vs.next(x);
+      pin();
+      s = T::mma(qs.buf[x], kf[x], s);
+      dp = T::mma(gs.buf[x], vs.buf[x], dp);
+      pin();
     }
+    constexpr int kI = D / 32;
+    auto ts = operands<4 * kI, kAhead>([&](int i) {  // dO^T for P, then Q^T for dS
+      return L::operand_t(i < 2 * kI ? gt : qt, 32 * rg + 16 * (i / kI % 2), i % kI, lane);
+    });
     const bool masked = st.open[rg / 2] == 0;
     if (masked) {
 #pragma unroll
@@ -483,16 +521,15 @@ __global__ __launch_bounds__(128 * RG) void attn_dkv(const AttnArgs a) {
         dp[4 * g4 + i] = s[4 * g4 + i] * (dp[4 * g4 + i] - d4[i]);
       }
     }
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const u32x4 p = pack8<T>(s, x), ds = pack8<T>(dp, x);
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        dv[i] = T::mma(L::operand_t(gt, 32 * rg + 16 * x, i, lane), p, dv[i]);
-        dk[i] = T::mma(L::operand_t(qt, 32 * rg + 16 * x, i, lane), ds, dk[i]);
-      }
-    }
+    const u32x4 w[4] = {pack8<T>(s, 0), pack8<T>(s, 1), pack8<T>(dp, 0), pack8<T>(dp, 1)};
+    ts.begin();
+    ts.run([&](int i, u32x4 x) {
+      f32x16 &to = i < 2 * kI ? dv[i % kI] : dk[i % kI];
+      to = T::mma(x, w[i / kI], to);
+    });
   }
+  {
+  const AttnArgs a = args_again();
   // the row groups' sums, each group adding a share of them in group order
   constexpr int kTiles = D / 32;
   float *buf = reinterpret_cast<float *>(lds);
@@ -537,6 +574,41 @@ __global__ __launch_bounds__(128 * RG) void attn_dkv(const AttnArgs a) {
         }
       }
     }
+  }
+  }
+}
+
+// Each workgroup takes its own item, then further ones from queues: the
+// dispatcher leaves a CU idle for a fifth of the time where a workgroup fills
+// it and the items differ in length.  Queue x holds every eighth item, so that
+// with 8 key heads XCD x keeps to one of them; a workgroup whose queue is empty
+// goes on to the next one that is not.
+template <class T, int D, int RG>
+__global__ __launch_bounds__(128 * RG) void attn_dkv(const AttnArgs) {
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  __shared__ int32_t taken[2];  // queue, or -1: nothing is left; place in it
+  int64_t item = blockIdx.x;
+  for (;;) {
+    const AttnArgs a = args_again();
+    const int64_t items = static_cast<int64_t>(a.b) * a.slots * a.hk;
+    if (item < items) dkv_item<T, D, RG>(a, lds, item);
+    if (items <= gridDim.x) return;
+    __syncthreads();
+    if (threadIdx.x < 64) {
+      const int q = threadIdx.x & 7;
+      const int64_t at = __hip_atomic_load(a.queue + q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      const uint32_t some = __ballot(at * 8 + q < items) & 0xff, own = blockIdx.x & 7;
+      const uint32_t first = some & (0xffu << own) ? some & (0xffu << own) : some;
+      if (threadIdx.x == 0) {
+        const int x = some ? __builtin_ctz(first) : -1;
+        taken[0] = x;
+        if (some) taken[1] = atomicAdd(a.queue + x, 1);
+      }
+    }
+    __syncthreads();
+    const int q = __builtin_amdgcn_readfirstlane(taken[0]);
+    if (q < 0) return;
+    item = static_cast<int64_t>(__builtin_amdgcn_readfirstlane(taken[1])) * 8 + q;
   }
 }
 
@@ -592,14 +664,14 @@ hipError_t run_backward(const AttnArgs &a, hipStream_t s) {
   }
   if (e != hipSuccess || a.nkb == 0) return e;
   constexpr int kRG = 4;
-  const size_t lds = 4 * 32 * kRG * D * 2 + kAttnPage * D * 2 + 2 * (2 * 32 * kRG * 4) + 2 * (3 * 32 * kRG * 4 + 16) +
+  const size_t lds = 4 * 32 * kRG * D * 2 + kAttnPage * D * 2 + 2 * (2 * 32 * kRG * 4) + 4 * (3 * 32 * kRG * 4 + 16) +
                      static_cast<size_t>(a.chunk) * 4;
   const int64_t grid = static_cast<int64_t>(a.b) * a.hk * a.slots;
   const int64_t merge = static_cast<int64_t>(a.b) * a.hk * a.nkb * (2 * kAttnPage * D / 4 / 256);
   if (grid > 0x7fffffff || merge > 0x7fffffff) return hipErrorInvalidValue;
   e = allow_dynamic_lds(reinterpret_cast<const void *>(&attn_dkv<T, D, kRG>), lds + (kMaxChunk - a.chunk) * 4);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((attn_dkv<T, D, kRG>), dim3(static_cast<unsigned>(grid)), dim3(128 * kRG), lds, s, a);
+  hipLaunchKernelGGL((attn_dkv<T, D, kRG>), dim3(static_cast<unsigned>(std::min<int64_t>(grid, kCus))), dim3(128 * kRG), lds, s, a);
   e = hipGetLastError();
   if (e != hipSuccess || a.slots == a.nkb) return e;
   hipLaunchKernelGGL((attn_dkv_merge<T, D>), dim3(static_cast<unsigned>(merge)), dim3(256), 0, s, a);
@@ -613,7 +685,9 @@ void attn_chunks(int64_t heads, int64_t entries, int32_t rows, int32_t nkb, int3
   // about 2048 items (8 a CU), but at least 512 rows an item: its partial
   // sums cost as much traffic as 128 rows' q and do
   const int64_t most = heads * entries / 2048 + 1, least = (511 + rows) / rows;
-  const int64_t c = std::min<int64_t>(attn::kMaxChunk, std::max(most, least));
+  // (and at most 2^28, so that the kernel counts them in 32 bits)
+  const int64_t cap = std::max<int64_t>(1, std::min<int64_t>(attn::kMaxChunk, (int64_t(1) << 28) / rows));
+  const int64_t c = std::min(cap, std::max(most, least));
   *chunk = static_cast<int32_t>(c);
   // items of key block kb start at kb + (entries before it) / chunk
   *slots = static_cast<int32_t>(nkb + entries / c);

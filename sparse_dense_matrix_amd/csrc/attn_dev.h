@@ -22,6 +22,7 @@ namespace attn {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
@@ -146,6 +147,14 @@ __device__ __forceinline__ void load_lds16(uint32_t lds, const char *p) {
                : "memory", "m0");
 }
 
+// 4 bytes a lane: LDS[lds + 4 * lane] = *p.
+__device__ __forceinline__ void load_lds4(uint32_t lds, const float *p) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off"
+               :
+               : "s"(lds), "v"(p)
+               : "memory", "m0");
+}
+
 // A staged tile: rows of d elements in 16-byte pieces, piece c of row r at
 // piece c ^ f(r).  One f serves both kinds of reads without bank conflicts:
 // 16 consecutive rows at one piece land on 16 distinct pieces of the 256-byte
@@ -166,26 +175,28 @@ struct Tile {
     return ((lane % kPieces) ^ f(load_row(i, lane))) * 16;
   }
   // A operand over the row: lane l gives row row0 + l % 32, elements
-  // 16 step + 8 (l / 32) + 0..7.  row0 is a multiple of 32.
+  // 16 step + 8 (l / 32) + 0..7.  row0 is a multiple of 32, t of 256 bytes.
+  // The swizzle is an XOR, so steps differ by an XOR of the lane's address:
+  // one register serves all of them.
   __device__ static __forceinline__ u32x4 operand(const char *t, int row0, int step, int lane) {
     const int r = lane & 31;
-    return *reinterpret_cast<const u32x4 *>(t + row0 * kRowBytes + r * kRowBytes +
-                                            ((2 * step + (lane >> 5)) ^ f(r)) * 16);
+    const uint32_t at = lds_addr(t) + r * kRowBytes + (((lane >> 5) ^ f(r)) << 4);
+    return *(const __attribute__((address_space(3))) u32x4 *)((at ^ (step << 5)) + row0 * kRowBytes);
   }
   // A operand of the tile's transpose: lane l gives element 32 dt + l % 32 of
   // rows row0 + 4 (l / 32) + 0..3 and row0 + 8 + 4 (l / 32) + 0..3.  row0 is
-  // a multiple of 16.
+  // a multiple of 16.  f(r + 8) is f(r) ^ 2 for r < 8.
   __device__ static __forceinline__ u32x4 operand_t(const char *t, int row0, int dt, int lane) {
     const int r = ((lane >> 2) & 3) + 4 * (lane >> 5);
-    const int piece = 4 * dt + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-    const char *p = t + row0 * kRowBytes + (lane & 1) * 8;
-    const u32x2 lo = tr(p + r * kRowBytes + (piece ^ f(r)) * 16);
-    const u32x2 hi = tr(p + (r + 8) * kRowBytes + (piece ^ f(r + 8)) * 16);
+    const int piece = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+    const uint32_t at = lds_addr(t) + r * kRowBytes + ((piece ^ f(r)) << 4) + (lane & 1) * 8;
+    const u32x2 lo = tr((at ^ (dt << 6)) + row0 * kRowBytes);
+    const u32x2 hi = tr((at ^ (dt << 6 | 32)) + (row0 + 8) * kRowBytes);
     return u32x4{lo[0], lo[1], hi[0], hi[1]};
   }
-  __device__ static __forceinline__ u32x2 tr(const char *p) {
-    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                         (__attribute__((address_space(3))) s16x4 *)(p)));
+  __device__ static __forceinline__ u32x2 tr(uint32_t at) {
+    return __builtin_bit_cast(
+        u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(at)));
   }
 };
 
@@ -204,11 +215,14 @@ struct Operands {
     for (int i = 0; i < AHEAD && i < N; ++i) buf[i] = read(i);
     pin();
   }
+  __device__ __forceinline__ void next(int i) {
+    if (i + AHEAD < N) buf[i + AHEAD] = read(i + AHEAD);
+  }
   template <class M>
   __device__ __forceinline__ void run(M mul) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      if (i + AHEAD < N) buf[i + AHEAD] = read(i + AHEAD);
+      next(i);
       pin();
       mul(i, buf[i]);
       pin();
