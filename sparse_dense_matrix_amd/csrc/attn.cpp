@@ -158,7 +158,7 @@ spmm_status_t attn_shape(const spmm_attn_desc_t &d, spmm_plan_s *p) {
     if (entries > INT32_MAX)
       return fail(SPMM_ERR_UNSUPPORTED, "spmm_plan_attn: lists of a head hold more than 2^31 - 1 entries");
     attn_chunks(static_cast<int64_t>(a.b) * a.hk, entries, a.rows, a.nkb, &a.chunk, &a.slots);
-    if (static_cast<double>(a.b) * a.hk * (static_cast<double>(a.nqb) * a.rtiles + a.nkb) > 0x7fffffff ||
+    if (static_cast<double>(a.b) * a.hk * (static_cast<double>(a.nqb) * 2 * a.rtiles + a.nkb) > 0x7fffffff ||
         static_cast<double>(a.b) * a.hk * std::max<double>(a.slots, 16.0 * a.nkb) > 0x7fffffff)
       return fail(SPMM_ERR_UNSUPPORTED, "spmm_plan_attn: more workgroups than a launch holds");
   }

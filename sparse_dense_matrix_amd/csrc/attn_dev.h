@@ -68,6 +68,17 @@ __device__ __forceinline__ float elem(unsigned v, int i) {
   return static_cast<float>(__builtin_bit_cast(E2, v)[i]);
 }
 
+// the same, and what the rounding left out as a second operand
+template <class T>
+__device__ __forceinline__ void split8(const f32x16 &x, int s, u32x4 &hi, u32x4 &lo) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = x[8 * s + 2 * i], b = x[8 * s + 2 * i + 1];
+    hi[i] = pack2<T>(a, b);
+    lo[i] = pack2<T>(a - elem<T>(hi[i], 0), b - elem<T>(hi[i], 1));
+  }
+}
+
 __device__ __forceinline__ f32x16 zero16() {
   f32x16 z;
 #pragma unroll

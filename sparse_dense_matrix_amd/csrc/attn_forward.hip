@@ -96,7 +96,8 @@ __device__ __forceinline__ Range range_of(const AttnArgs &a, const Item &it, con
   return x;
 }
 
-// `kept` keys from key `first` of a block on, as a buffer.  Rows past them
+// `kept` keys from key `first` of a block on (those that some row sees), as a
+// buffer.  Rows past them
 // read as zeros: what stands there may be anything, and a weight of zero does
 // not make a NaN harmless.
 template <int D>
@@ -284,7 +285,7 @@ __global__ __launch_bounds__(64 * RW * KW, 2) void attn_forward(const AttnArgs a
       const int id = __builtin_amdgcn_readlane(blocks.id, at);
       const int page = __builtin_amdgcn_readlane(blocks.page, at);
       const int32_t first = (t % kSubs) * KT;
-      const int32_t kept = t < tiles ? min(KT, row.len - id * kAttnPage - first) : 0;
+      const int32_t kept = t < tiles ? min(KT, row.last_key + 1 - id * kAttnPage - first) : 0;
       const i32x4 kbuf = keys_of<D>(a, a.k, it, id, page, first, kept);
       const i32x4 vbuf = keys_of<D>(a, a.v, it, id, page, first, kept);
       const uint32_t at_lds = stage0 + (round & 1) * 2 * kHalf;
@@ -379,7 +380,7 @@ __global__ __launch_bounds__(64 * KW, 2) void attn_stream(const AttnArgs a) {
       const int id = __builtin_amdgcn_readlane(blocks.id, at);
       const int page = __builtin_amdgcn_readlane(blocks.page, at);
       const int32_t first = (t % kSubs) * KT;
-      const int32_t kept = t < tiles ? min(KT, row.len - id * kAttnPage - first) : 0;
+      const int32_t kept = t < tiles ? min(KT, row.last_key + 1 - id * kAttnPage - first) : 0;
       const i32x4 buf = keys_of<D>(a, values ? a.v : a.k, it, id, page, first, kept);
 #pragma unroll
       for (int i = 0; i < kLoads; ++i)
