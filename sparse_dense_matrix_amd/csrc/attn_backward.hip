@@ -609,12 +609,12 @@ __device__ __forceinline__ void dkv_item(const AttnArgs &a, char *lds, int64_t a
   const uint32_t per_token = 0xffffffffu / static_cast<uint32_t>(a.group);
   // Threads below kRows look after a row each, two rounds ahead: its offsets
   // for the direct loads, its limit, and its statistics on their way to LDS.
-  // Rows that are not there read zeros, and statistics that make their weights 0.
+  // Rows that are not there read zeros and see no key.
   auto find = [&](int round) {
     const uint32_t flat = static_cast<uint32_t>(round) * kRows + tid;
     Stats &s = stats[round & 3];
     uint32_t qo = kDeadRow, go = kDeadRow;
-    int32_t lim = INT32_MAX;
+    int32_t lim = -1;
     int64_t rid = static_cast<int64_t>(a.b) * a.hq * a.nq;
     if (flat < total) {
       const uint32_t e = over(flat, a.rows, per_list), row = flat - e * a.rows;

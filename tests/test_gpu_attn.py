@@ -533,3 +533,156 @@ def test_refusals_of_tensors(S):
         S.spmm_execute(P, q[0, :, 0], o[0, :, 0])
     with pytest.raises(S.SpmmError):
         S.spmm_execute_sddmm(P, q[0, :, 0], o[0, :, 0], lse)
+
+
+# ---- what stands where no query looks, far offsets, many items -------------
+
+def test_keys_that_no_query_sees_may_hold_anything(S):
+    """Keys below the length but past every query: NaN there changes nothing,
+    and their gradients are zero."""
+    for c in (case(nq=40, nk=256, hq=8, hk=2, d=128, q_block=64, blocks=4), case(nq=5, nk=256, hq=4, hk=4, q_block=1, blocks=4)):
+        q, k, v, grad, g = inputs(c, 40)
+        starts, lens = torch.tensor([70], dtype=torch.int32), torch.tensor([250], dtype=torch.int32)
+        end = 70 + c["nq"]
+        k[0, end:], v[0, end:] = float("nan"), float("inf")
+        lists = torch.tensor([0, 1, 2, 3], dtype=torch.int32).expand(1, c["hk"], -(-c["nq"] // c["q_block"]), 4).contiguous()
+        P = plan(S, c, backward=True)
+        o, lse = run_forward(S, c, q.cuda(), k.cuda(), v.cuda(), lists.cuda(), lens.cuda(), starts.cuda(), P)
+        dq, dk, dv = (torch.full_like(t, float("nan")).cuda() for t in (q, k, v))
+        S.spmm_execute_attn_backward(P, grad.cuda(), q.cuda(), k.cuda(), v.cuda(), lists.cuda(), o, lse, dq, dk, dv,
+                                     lens=lens.cuda(), starts=starts.cuda())
+        want = R.attention(c, q.double(), k.double(), v.double(), R.sees(c, lists, lens, starts, None), grad.double())
+        for name, got in (("o", o), ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv)):
+            R.check(name, got, *want[name])
+        assert (dk[:, end:] == 0).all() and (dv[:, end:] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("nq,q_block", [(1, 1), (14, 1), (100, 16), (128, 64)])
+def test_dq_of_few_keys_is_off_by_its_own_rounding(S, nq, q_block, dtype):
+    """Up to two blocks: the rounding of dq, and errors of 32-bit sums; neither
+    the rounding of o nor that of dS (kept to two steps) shows."""
+    c = case(b=2, nq=nq, hq=4, hk=2, d=64, q_block=q_block, blocks=2, dtype=dtype)
+    q, k, v, grad, g = inputs(c, 50 + nq)
+    lists = torch.tensor([0, 1], dtype=torch.int32).expand(2, 2, -(-nq // q_block), 2).contiguous()
+    P = plan(S, c, backward=True)
+    o, lse = run_forward(S, c, q.cuda(), k.cuda(), v.cuda(), lists.cuda(), None, None, P)
+    dq, dk, dv = (torch.full_like(t, float("nan")).cuda() for t in (q, k, v))
+    S.spmm_execute_attn_backward(P, grad.cuda(), q.cuda(), k.cuda(), v.cuda(), lists.cuda(), o, lse, dq, dk, dv)
+    q, k, v, grad = (t.double().permute(0, 2, 1, 3) for t in (q, k, v, grad))
+    k, v = k.repeat_interleave(2, 1), v.repeat_interleave(2, 1)
+    s = (q @ k.transpose(-1, -2) / 8).masked_fill(torch.ones(nq, nq).triu(1).bool(), -math.inf)
+    p = torch.softmax(s, -1)
+    dp = grad @ v.transpose(-1, -2)
+    delta = (p * dp).sum(-1, keepdim=True)
+    ds = p * (dp - delta)
+    want = ds @ k / 8
+    u, e32 = torch.finfo(dtype).eps / 2, 2.0 ** -24
+    tiny = torch.finfo(dtype).smallest_normal * u
+    # relative errors of a weight: its score's 66 terms, exponents, the rounded lse
+    ew = (2 * 66 * (q.abs() @ k.abs().transpose(-1, -2) / 8).amax(-1, keepdim=True) + 64) * e32
+    edp = 66 * e32 * (grad.abs() @ v.abs().transpose(-1, -2))
+    edelta = (p * (edp + (ew + 200 * e32) * dp.abs())).sum(-1, keepdim=True)
+    eds = 1.02 * ((u * u + ew) * ds.abs() + p * (edp + edelta + 4 * e32 * (dp.abs() + delta.abs()))) + tiny * (p > 0)
+    bound = (eds + 200 * e32 * ds.abs()) @ k.abs() / 8
+    bound = (u + 4 * e32) * (want.abs() + bound) + bound + tiny
+    R.check("dq", dq, want.permute(0, 2, 1, 3), bound.permute(0, 2, 1, 3))
+
+
+def test_offsets_past_4_gib(S):
+    """Pages, sequences and gradients that stand more than 2^32 bytes apart."""
+    c = case(b=2, nq=70, nk=70, hq=4, hk=2, d=64, q_block=16, blocks=2)
+    q, k, v, grad, g = inputs(c, 60)
+    lists = random_lists(c, g).cuda()
+    step = 2 ** 31 + 64  # elements
+    room = torch.empty(step + 2 ** 20, dtype=c["dtype"], device="cuda")
+    at = [0]
+
+    def far(x):
+        n = x[0].numel()
+        y = room.as_strided(x.shape, (step, *x.stride()[1:]), at[0])
+        at[0] += (n + 7) // 8 * 8
+        y.copy_(x)
+        return y
+
+    outs = []
+    for place in (lambda x: x, far):
+        q1, k1, v1, g1 = (place(t.cuda()) for t in (q, k, v, grad))
+        o, dq, dk, dv = (place(torch.zeros_like(t).cuda()) for t in (q, q, k, k))
+        lse = torch.zeros((2, 4, 70), device="cuda")
+        P = plan(S, c, backward=True)
+        S.spmm_execute_attn(P, q1, k1, v1, lists, o, lse)
+        S.spmm_execute_attn_backward(P, g1, q1, k1, v1, lists, o, lse, dq, dk, dv)
+        values = torch.zeros((4, 2, 64), dtype=torch.int8, device="cuda")
+        scale = torch.zeros((4, 2), device="cuda")
+        S.spmm_execute_attn_pool(P, k1, values, scale)
+        outs.append([t.contiguous() for t in (o, lse, dq, dk, dv, values, scale)])
+    assert all(torch.equal(x, y) for x, y in zip(*outs))
+    assert outs[0][0][1].abs().sum() > 0
+    # a cache whose second page stands past 2^32 bytes
+    c = case(b=1, nq=3, nk=128, hq=4, hk=2, d=64, blocks=2)
+    q, k, v, _, g = inputs(c, 61)
+    table = torch.tensor([[1, 0]], dtype=torch.int32)
+    pages = [x.reshape(2, PAGE, 2, 64).flip(0).contiguous().cuda() for x in (k, v)]
+    starts = torch.tensor([125], dtype=torch.int32)
+    at[0] = 0
+    a = run_cache(S, c, q, *pages, table=table, starts=starts)
+    b = run_cache(S, c, q, far(pages[0]), far(pages[1]), table=table, starts=starts)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    want = R.attention(c, q.double(), k.double(), v.double(), R.sees(c, None, [128], [125], None))
+    R.check("o", b[0], *want["o"])
+
+
+def test_cache_strides(S):
+    """Pages with their heads first, and K and V side by side in one page."""
+    c = case(b=2, nq=4, nk=320, hq=8, hk=2, d=128, blocks=3)
+    q, k, v, _, g = inputs(c, 62)
+    kp, vp, table = paged(c, k, v, g)
+    lens, starts = torch.tensor([320, 77], dtype=torch.int32), torch.tensor([316, 73], dtype=torch.int32)
+    a = run_cache(S, c, q, kp, vp, table=table, lens=lens, starts=starts)
+    both = torch.stack([kp, vp], 3).cuda()  # [pages, 64, heads, 2, dim]
+    views = [(kp.cuda().transpose(1, 2).contiguous().transpose(1, 2), vp.cuda().transpose(1, 2).contiguous().transpose(1, 2)),
+             (both[:, :, :, 0], both[:, :, :, 1])]
+    for k1, v1 in views:
+        assert not k1.is_contiguous()
+        b = run_cache(S, c, q, k1, v1, table=table, lens=lens, starts=starts)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_backward_many_items(S):
+    """More items than workgroups: the same bits as sequence by sequence."""
+    c = case(b=8, nq=700, hq=16, hk=8, d=128, q_block=16, blocks=3)
+    q, k, v, grad, g = inputs(c, 63)
+    lists = random_lists(c, g, empty=0.1).cuda()
+    lens = torch.tensor([700, 1, 650, 64, 65, 300, 700, 699], dtype=torch.int32).cuda()
+    q, k, v, grad = (t.cuda() for t in (q, k, v, grad))
+
+    def run(c, part):
+        P = plan(S, c, backward=True)
+        x = [t[part].contiguous() for t in (q, k, v, grad, lists, lens)]
+        o, lse = run_forward(S, c, *x[:3], x[4], x[5], None, P)
+        out = [torch.full_like(t, float("nan")) for t in x[:3]]
+        for _ in range(2):  # the queues start anew
+            S.spmm_execute_attn_backward(P, x[3], *x[:3], x[4], o, lse, *out, lens=x[5])
+        return out
+
+    whole = run(c, slice(0, 8))
+    for i in range(8):
+        for x, y in zip(whole, run(dict(c, b=1), slice(i, i + 1))):
+            assert torch.equal(x[i:i + 1], y), i
+
+
+def test_plan_out_of_memory(S, monkeypatch):
+    """Every allocation of a plan that fails: OUT_OF_MEMORY, and the next plan works."""
+    n = 1
+    while True:
+        monkeypatch.setenv("SPMM_TEST_FAIL_ALLOC", str(n))
+        try:
+            plan(S, case(b=1, nq=2, nk=4096, hq=4, hk=2, q_block=1, blocks=64), backward=True)
+            break
+        except S.SpmmError as e:
+            assert e.name == "SPMM_ERR_OUT_OF_MEMORY"
+        n += 1
+    assert n > 6
+    monkeypatch.delenv("SPMM_TEST_FAIL_ALLOC")
+    plan(S, case(), backward=True)
