@@ -102,8 +102,8 @@ struct AttnTile {
   int32_t row_waves, key_waves, key_tile, rows;
 };
 AttnTile attn_tile(int32_t rows);
-// Ranges a list is cut into, and entries of each, for `tiles` row tiles of
-// tile_rows rows in all.
+// Ranges a list is cut into, and entries of each, for `tiles` row tiles in
+// all with tile_rows rows each.
 void attn_split(int64_t tiles, int32_t tile_rows, int32_t entries, int32_t *nsplit, int32_t *per_split);
 // Query blocks that one item of the dk, dv kernel takes, and items of a head.
 void attn_chunks(int64_t heads, int64_t entries, int32_t rows, int32_t nkb, int32_t *chunk, int32_t *slots);
