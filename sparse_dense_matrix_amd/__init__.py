@@ -474,65 +474,67 @@ def _attn_expect(d: AttnDesc, device: int) -> dict:
         "q": ((b, nq, hq, dim), t), "k": ((b, nk, hk, dim), t), "page": ((64, hk, dim), t),
         "lse": ((b, hq, nq), torch.float32), "lists": ((b, hk, nqb, d.max_blocks), torch.int32),
         "table": ((b, nkb), torch.int32), "seq": ((b,), torch.int32), "tree": ((b, nq), torch.int64),
-        "slots": b * nkb}}
+        "slots": b * nkb, "int8": torch.int8}}
 
 
 _pack_tensor = struct.Struct("=4q").pack
+_raw_stream = None
+
+# Marshalling of the attention calls: each tensor is checked against the plan
+# (a few attribute reads, no objects made: the smallest calls take as long as
+# their marshalling), then goes as a pointer, a tensor of heads with strides.
 
 
-class _AttnCall:
-    """Marshals one call: every tensor against the plan, then pointers."""
+def _attn_want(plan: Plan) -> dict:
+    want = plan.expect.get("attn")
+    if want is None:
+        raise ValueError("not a plan of spmm_plan_attn")
+    return want
 
-    def __init__(self, plan: Plan):
-        self.want = plan.expect.get("attn")
-        if self.want is None:
-            raise ValueError("not a plan of spmm_plan_attn")
-        self.device = plan.expect["device"]
 
-    def _check(self, name: str, t, shape, dtype):
-        if t.dtype is not dtype:
-            raise ValueError(f"{name} is {t.dtype}; the plan takes {dtype}")
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}; the plan takes {shape}")
-        if t.get_device() != self.device:
-            raise ValueError(f"{name} must be on cuda:{self.device}")
+def _refuse(name: str, t, shape, dtype, device):
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} is {t.dtype}; the plan takes {dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; the plan takes {shape}")
+    raise ValueError(f"{name} must be on cuda:{device}")
 
-    def heads(self, name: str, t, like: str, paged: bool = False):
-        """A tensor of heads: its strides go along."""
-        shape, dtype = self.want[like]
-        if paged:
-            shape, dtype = self.want["page"]
-            shape = (t.shape[0],) + shape
-        self._check(name, t, shape, dtype)
-        sb, st, sh, sd = t.stride()
-        if sd != 1 and t.numel():
-            raise ValueError(f"{name}: the elements of a head must be consecutive")
-        return _pack_tensor(t.data_ptr(), sb, st, sh)
 
-    def whole(self, name: str, t, like: str, optional: bool = False):
-        """A contiguous tensor of the plan's shape."""
-        if t is None and optional:
-            return None
-        shape, dtype = self.want[like]
-        return self.flat(name, t, shape, dtype)
+def _heads(name: str, t, want, device):
+    """A tensor of heads: its strides go along."""
+    shape, dtype = want
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
+        _refuse(name, t, shape, dtype, device)
+    sb, st, sh, sd = t.stride()
+    if sd != 1 and t.numel():
+        raise ValueError(f"{name}: the elements of a head must be consecutive")
+    return _pack_tensor(t.data_ptr(), sb, st, sh)
 
-    def flat(self, name: str, t, shape, dtype):
-        self._check(name, t, shape, dtype)
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        return t.data_ptr()
 
-    def pooled(self, pooled, scale, slots: int):
-        import torch
-        _, hk, dim = self.want["page"][0]
-        return (self.flat("pooled", pooled, (slots, hk, dim), torch.int8),
-                self.flat("pooled_scale", scale, (slots, hk), torch.float32))
+def _flat(name: str, t, want, device):
+    """A contiguous tensor."""
+    shape, dtype = want
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
+        _refuse(name, t, shape, dtype, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
-    def stream(self, stream):
-        if stream is None:
-            import torch
-            stream = torch.cuda.current_stream(self.device)
+
+def _opt(name: str, t, want, device):
+    return None if t is None else _flat(name, t, want, device)
+
+
+def _stream_of(stream, device):
+    if stream is not None:
         return getattr(stream, "cuda_stream", stream)
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        # the handle alone where this torch has it: a Stream object takes 2 us
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _raw_stream(device)
 
 
 def spmm_execute_attn_pool(plan: Plan, k, pooled, pooled_scale, lens=None, table=None, first=None,
@@ -541,52 +543,64 @@ def spmm_execute_attn_pool(plan: Plan, k, pooled, pooled_scale, lens=None, table
     with pooled_scale [slots, heads_kv] float32.  k is [batch, keys, heads_kv,
     dim] (slots = batch * blocks), or with a table [pages, 64, heads_kv, dim]
     (slots = pages).  first [batch]: only the blocks from that key on."""
-    c = _AttnCall(plan)
-    kp = c.heads("k", k, "k", table is not None)
-    pages = k.shape[0] if table is not None else 0
-    pp, sp = c.pooled(pooled, pooled_scale, pages if table is not None else c.want["slots"])
-    _check(_lib.spmm_execute_attn_pool(
-        plan.handle, kp, pages, pp, sp, c.whole("table", table, "table", True),
-        c.whole("lens", lens, "seq", True), c.whole("first", first, "seq", True), c.stream(stream)),
-        "spmm_execute_attn_pool")
+    w, d = _attn_want(plan), plan.expect["device"]
+    pages, slots, kw = 0, w["slots"], w["k"]
+    if table is not None:
+        pages = slots = k.shape[0]
+        kw = ((pages,) + w["page"][0], w["page"][1])
+    _, hk, dim = w["page"][0]
+    st = _lib.spmm_execute_attn_pool(
+        plan.handle, _heads("k", k, kw, d), pages, _flat("pooled", pooled, ((slots, hk, dim), w["int8"]), d),
+        _flat("pooled_scale", pooled_scale, ((slots, hk), w["lse"][1]), d), _opt("table", table, w["table"], d),
+        _opt("lens", lens, w["seq"], d), _opt("first", first, w["seq"], d), _stream_of(stream, d))
+    if st:
+        _check(st, "spmm_execute_attn_pool")
 
 
 def spmm_execute_attn_select(plan: Plan, q, pooled, pooled_scale, lists, lens=None, starts=None,
                              table=None, stream=None):
     """lists [batch, heads_kv, query blocks, max_blocks] int32: the blocks of
     the highest scores, ascending, filled up with -1."""
-    c = _AttnCall(plan)
-    slots = pooled.shape[0] if table is not None else c.want["slots"]
-    pp, sp = c.pooled(pooled, pooled_scale, slots)
-    _check(_lib.spmm_execute_attn_select(
-        plan.handle, c.heads("q", q, "q"), pp, sp, slots if table is not None else 0,
-        c.whole("lists", lists, "lists"), c.whole("table", table, "table", True),
-        c.whole("lens", lens, "seq", True), c.whole("starts", starts, "seq", True), c.stream(stream)),
-        "spmm_execute_attn_select")
+    w, d = _attn_want(plan), plan.expect["device"]
+    pages, slots = 0, w["slots"]
+    if table is not None:
+        pages = slots = pooled.shape[0]
+    _, hk, dim = w["page"][0]
+    st = _lib.spmm_execute_attn_select(
+        plan.handle, _heads("q", q, w["q"], d), _flat("pooled", pooled, ((slots, hk, dim), w["int8"]), d),
+        _flat("pooled_scale", pooled_scale, ((slots, hk), w["lse"][1]), d), pages,
+        _flat("lists", lists, w["lists"], d), _opt("table", table, w["table"], d), _opt("lens", lens, w["seq"], d),
+        _opt("starts", starts, w["seq"], d), _stream_of(stream, d))
+    if st:
+        _check(st, "spmm_execute_attn_select")
 
 
 def spmm_execute_attn(plan: Plan, q, k, v, lists, o, lse, lens=None, starts=None, stream=None):
     """o (as q) and lse [batch, heads_q, queries] float32 of attention over
     the listed blocks.  Query t stands at position starts + t."""
-    c = _AttnCall(plan)
-    _check(_lib.spmm_execute_attn(
-        plan.handle, c.heads("q", q, "q"), c.heads("k", k, "k"), c.heads("v", v, "k"),
-        c.whole("lists", lists, "lists"), c.heads("o", o, "q"), c.whole("lse", lse, "lse"),
-        c.whole("lens", lens, "seq", True), c.whole("starts", starts, "seq", True), c.stream(stream)),
-        "spmm_execute_attn")
+    w, d = _attn_want(plan), plan.expect["device"]
+    qw, kw = w["q"], w["k"]
+    st = _lib.spmm_execute_attn(
+        plan.handle, _heads("q", q, qw, d), _heads("k", k, kw, d), _heads("v", v, kw, d),
+        _flat("lists", lists, w["lists"], d), _heads("o", o, qw, d), _flat("lse", lse, w["lse"], d),
+        _opt("lens", lens, w["seq"], d), _opt("starts", starts, w["seq"], d), _stream_of(stream, d))
+    if st:
+        _check(st, "spmm_execute_attn")
 
 
 def spmm_execute_attn_backward(plan: Plan, grad, q, k, v, lists, o, lse, dq, dk, dv, lens=None,
                                starts=None, stream=None):
     """dq, dk and dv from grad, the gradient of o; o and lse are the forward
     call's.  The plan must have been made with backward=True."""
-    c = _AttnCall(plan)
-    _check(_lib.spmm_execute_attn_backward(
-        plan.handle, c.heads("grad", grad, "q"), c.heads("q", q, "q"), c.heads("k", k, "k"),
-        c.heads("v", v, "k"), c.whole("lists", lists, "lists"), c.heads("o", o, "q"),
-        c.whole("lse", lse, "lse"), c.heads("dq", dq, "q"), c.heads("dk", dk, "k"),
-        c.heads("dv", dv, "k"), c.whole("lens", lens, "seq", True),
-        c.whole("starts", starts, "seq", True), c.stream(stream)), "spmm_execute_attn_backward")
+    w, d = _attn_want(plan), plan.expect["device"]
+    qw, kw = w["q"], w["k"]
+    st = _lib.spmm_execute_attn_backward(
+        plan.handle, _heads("grad", grad, qw, d), _heads("q", q, qw, d), _heads("k", k, kw, d),
+        _heads("v", v, kw, d), _flat("lists", lists, w["lists"], d), _heads("o", o, qw, d),
+        _flat("lse", lse, w["lse"], d), _heads("dq", dq, qw, d), _heads("dk", dk, kw, d), _heads("dv", dv, kw, d),
+        _opt("lens", lens, w["seq"], d), _opt("starts", starts, w["seq"], d), _stream_of(stream, d))
+    if st:
+        _check(st, "spmm_execute_attn_backward")
 
 
 def spmm_execute_attn_cache(plan: Plan, q, k, v, o, lse, table=None, lists=None, tree=None, lens=None,
@@ -595,13 +609,17 @@ def spmm_execute_attn_cache(plan: Plan, q, k, v, o, lse, table=None, lists=None,
     heads_kv, dim] with a table [batch, blocks], else [batch, keys, heads_kv,
     dim]; every block, or the lists'.  tree [batch, queries] int64: bit u of a
     drafted token's word is set where it sees drafted token u."""
-    c = _AttnCall(plan)
-    paged = table is not None
-    if paged and k.shape[0] != v.shape[0]:
-        raise ValueError("k and v must have the same pages")
-    _check(_lib.spmm_execute_attn_cache(
-        plan.handle, c.heads("q", q, "q"), c.heads("k", k, "k", paged), c.heads("v", v, "k", paged),
-        k.shape[0] if paged else 0, c.heads("o", o, "q"), c.whole("lse", lse, "lse"),
-        c.whole("table", table, "table", True), c.whole("lists", lists, "lists", True),
-        c.whole("tree", tree, "tree", True), c.whole("lens", lens, "seq", True),
-        c.whole("starts", starts, "seq", True), c.stream(stream)), "spmm_execute_attn_cache")
+    w, d = _attn_want(plan), plan.expect["device"]
+    pages, qw, kw = 0, w["q"], w["k"]
+    if table is not None:
+        pages = k.shape[0]
+        if pages != v.shape[0]:
+            raise ValueError("k and v must have the same pages")
+        kw = ((pages,) + w["page"][0], w["page"][1])
+    st = _lib.spmm_execute_attn_cache(
+        plan.handle, _heads("q", q, qw, d), _heads("k", k, kw, d), _heads("v", v, kw, d), pages,
+        _heads("o", o, qw, d), _flat("lse", lse, w["lse"], d), _opt("table", table, w["table"], d),
+        _opt("lists", lists, w["lists"], d), _opt("tree", tree, w["tree"], d), _opt("lens", lens, w["seq"], d),
+        _opt("starts", starts, w["seq"], d), _stream_of(stream, d))
+    if st:
+        _check(st, "spmm_execute_attn_cache")
