@@ -100,12 +100,21 @@ void attn_log(const spmm_plan_s *p) {
 
 }  // namespace
 
-void attn_split(int64_t tiles, int32_t tile_rows, int32_t entries, int32_t *nsplit, int32_t *per_split) {
+void attn_split(int64_t tiles, int32_t tile_rows, int32_t entries, int32_t max_entries, int32_t *nsplit,
+                int32_t *per_split) {
   // 4096 workgroups to fill the chip and even out ragged lengths, but no more
   // than 48k rows of partial sums (24 drafted tokens over 16 sequences of up to
   // 8k: 4 ranges 113 us, 8 127 us, 16 146 us), and at least eight blocks a
   // range (64 lists of 32 blocks: 108 us, with four blocks 120 us), or four
-  // where that leaves CUs without work.
+  // where that leaves CUs without work.  What a merge costs (4 us) is more than
+  // the 0.35 us a block that ranges save where four waves share 32 rows' list
+  // of 16 blocks, or 1 us a block where rows fill the tile and there are 6.
+  if (entries <= (tile_rows <= 32 ? 16 : 6)) {
+    *nsplit = 1;
+    *per_split = std::max(1, max_entries);
+    return;
+  }
+  entries = max_entries;
   tiles = std::max<int64_t>(1, tiles);
   const int64_t want = std::max<int64_t>(1, std::min<int64_t>(4096 / tiles, 49152 / (tiles * tile_rows)));
   int64_t per = std::max<int64_t>(4, (entries + want - 1) / want);
@@ -156,13 +165,13 @@ spmm_status_t attn_shape(const spmm_attn_desc_t &d, spmm_plan_s *p) {
     return fail(SPMM_ERR_UNSUPPORTED, "spmm_plan_attn: more workgroups than a launch holds");
   const int64_t n = static_cast<int64_t>(tiles);
   const int32_t rows = std::min(a.rows, t.rows);
-  attn_split(n, rows, a.max_blocks, &p->attn_split_listed[0], &p->attn_split_listed[1]);
-  attn_split(n, rows, a.nkb, &p->attn_split_all[0], &p->attn_split_all[1]);
+  attn_split(n, rows, std::min(a.max_blocks, a.nkb), a.max_blocks, &p->attn_split_listed[0], &p->attn_split_listed[1]);
+  attn_split(n, rows, a.nkb, a.nkb, &p->attn_split_all[0], &p->attn_split_all[1]);
   if (d.backward) {
     const int64_t entries = static_cast<int64_t>(a.nqb) * a.max_blocks;
     if (entries > INT32_MAX)
       return fail(SPMM_ERR_UNSUPPORTED, "spmm_plan_attn: lists of a head hold more than 2^31 - 1 entries");
-    attn_chunks(static_cast<int64_t>(a.b) * a.hk, entries, a.rows, a.nkb, &a.chunk, &a.slots);
+    attn_chunks(static_cast<int64_t>(a.b) * a.hk, entries, a.nqb, a.rows, a.nkb, &a.chunk, &a.slots);
     if (static_cast<double>(a.b) * a.hk * (static_cast<double>(a.nqb) * 2 * a.rtiles + a.nkb) > 0x7fffffff ||
         static_cast<double>(a.b) * a.hk * std::max<double>(a.slots, 16.0 * a.nkb) > 0x7fffffff)
       return fail(SPMM_ERR_UNSUPPORTED, "spmm_plan_attn: more workgroups than a launch holds");

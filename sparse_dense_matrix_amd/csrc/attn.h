@@ -103,10 +103,13 @@ struct AttnTile {
 };
 AttnTile attn_tile(int32_t rows);
 // Ranges a list is cut into, and entries of each, for `tiles` row tiles in
-// all with tile_rows rows each.
-void attn_split(int64_t tiles, int32_t tile_rows, int32_t entries, int32_t *nsplit, int32_t *per_split);
-// Query blocks that one item of the dk, dv kernel takes, and items of a head.
-void attn_chunks(int64_t heads, int64_t entries, int32_t rows, int32_t nkb, int32_t *chunk, int32_t *slots);
+// all with tile_rows rows each; lists name about `entries` blocks at most, in
+// max_entries places.
+void attn_split(int64_t tiles, int32_t tile_rows, int32_t entries, int32_t max_entries, int32_t *nsplit,
+                int32_t *per_split);
+// Query blocks that one item of the dk, dv kernel takes, and items of a head,
+// for nqb lists of a head with `entries` entries in all.
+void attn_chunks(int64_t heads, int64_t entries, int32_t nqb, int32_t rows, int32_t nkb, int32_t *chunk, int32_t *slots);
 
 hipError_t launch_attn_forward(const AttnArgs &a, spmm_dtype_t t, int d, hipStream_t s);
 hipError_t launch_attn_backward(const AttnArgs &a, spmm_dtype_t t, int d, hipStream_t s);

@@ -906,14 +906,17 @@ hipError_t run_backward(const AttnArgs &a, hipStream_t s) {
 }  // namespace
 }  // namespace attn
 
-void attn_chunks(int64_t heads, int64_t entries, int32_t rows, int32_t nkb, int32_t *chunk, int32_t *slots) {
+void attn_chunks(int64_t heads, int64_t entries, int32_t nqb, int32_t rows, int32_t nkb, int32_t *chunk, int32_t *slots) {
   // about 512 items more than one a key block: two a CU, taken from queues
   // (16k tokens: 1502 us the step, with four times as many 1567), but at least
   // 512 rows an item: its partial sums cost as much traffic as 128 rows' q and do
   const int64_t most = heads * entries / 512 + 1, least = (511 + rows) / rows;
   // (and at most 2^28, so that the kernel counts them in 32 bits)
   const int64_t cap = std::max<int64_t>(1, std::min<int64_t>(attn::kMaxChunk, (int64_t(1) << 28) / rows));
-  const int64_t c = std::min(cap, std::max(most, least));
+  int64_t c = std::min(cap, std::max(most, least));
+  // no key block is cut, not even one that lists name more than once: without
+  // partial sums there is no launch to merge them (4 us)
+  if (nqb <= c && entries < cap) c = entries + 1;
   *chunk = static_cast<int32_t>(c);
   // items of key block kb start at kb + (entries before it) / chunk
   *slots = static_cast<int32_t>(nkb + entries / c);
