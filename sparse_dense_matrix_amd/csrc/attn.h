@@ -35,6 +35,8 @@ struct AttnArgs {
   const uint64_t *tree;        // [b][nq] rows of the drafted tokens' mask, or null
   const int32_t *lens, *starts;  // [b], or null: nk, 0
   int32_t b, nq, nk, hq, hk, group, q_block, nqb, nkb, max_blocks, pages;
+  int32_t pack, list_nqb;      // lists that share a row tile (0: one), and lists of a head: q_block, nqb and
+                               // rows are then those of `pack` query blocks
   int32_t rows;                // rows of a query block: min(q_block, nq) * group
   int32_t rtiles;              // row tiles of a query block
   int32_t nsplit, per_split;   // ranges of a list and entries of each
@@ -102,6 +104,10 @@ struct AttnTile {
   int32_t row_waves, key_waves, key_tile, rows;
 };
 AttnTile attn_tile(int32_t rows);
+// Lists that share a row tile of 32 rows (a power of two), for `lists` lists in
+// all with `rows` rows and max_blocks entries each; 0: one list a tile.
+int32_t attn_pack(int64_t lists, int32_t rows, int32_t max_blocks);
+AttnArgs attn_packed(AttnArgs a, int32_t pack);
 // Ranges a list is cut into, and entries of each, for `tiles` row tiles in
 // all with tile_rows rows each; lists name about `entries` blocks at most, in
 // max_entries places.

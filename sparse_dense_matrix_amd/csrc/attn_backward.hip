@@ -31,8 +31,8 @@ constexpr uint32_t kDeadRow = 0xffffff00u;  // offset past every buffer: a direc
 
 // Sequence length, position of the first query, and last key that query block
 // qb sees.
-__device__ __forceinline__ int32_t last_key_of(const AttnArgs &a, int qb, int32_t len, int32_t start) {
-  return min(len - 1, start + min(a.nq - 1, qb * a.q_block + a.q_block - 1));
+__device__ __forceinline__ int32_t last_key_of(const AttnArgs &a, int q_block, int qb, int32_t len, int32_t start) {
+  return min(len - 1, start + min(a.nq - 1, qb * q_block + q_block - 1));
 }
 
 // x / d for d > 0, with inv = 0xffffffff / d: the product is at most one below
@@ -49,7 +49,8 @@ __device__ void invert(const AttnArgs &a, int64_t which, char *lds) {
   const int64_t bh = which / a.nkb;
   const int b = bh / a.hk;
   const int32_t len = attn_len(a.lens, b, a.nk), start = attn_start(a.starts, b, a.nq, a.nk);
-  const uint32_t entries = static_cast<uint32_t>(a.nqb) * a.max_blocks;  // below 2^31
+  const int nqb = a.pack ? a.list_nqb : a.nqb, q_block = a.pack ? a.q_block / a.pack : a.q_block;  // of one list
+  const uint32_t entries = static_cast<uint32_t>(nqb) * a.max_blocks;  // below 2^31
   const int32_t *lists = a.lists + bh * static_cast<int64_t>(entries);
   int *sums = reinterpret_cast<int *>(lds);  // [waves][2]
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 63, wave = tid >> 6, waves = nt >> 6;
@@ -59,7 +60,7 @@ __device__ void invert(const AttnArgs &a, int64_t which, char *lds) {
   // the block that entry e names, or -1
   auto named = [&](uint32_t e) {
     const int32_t id = e < e1 ? lists[e] : -1;
-    return id >= 0 && attn_names(id, last_key_of(a, over(e, a.max_blocks, inv), len, start)) ? id : -1;
+    return id >= 0 && attn_names(id, last_key_of(a, q_block, over(e, a.max_blocks, inv), len, start)) ? id : -1;
   };
 
   int less = 0, same = 0;
@@ -396,14 +397,16 @@ __global__ __launch_bounds__(64 * RW * KW, 2) void attn_dq(const AttnArgs a) {
 // dq where a list has up to 32 rows: each wave streams tiles of 32 keys
 // through LDS of its own, without barriers, V in one buffer and K in another:
 // the next V loads during the scores and dS, the next K during do . v.  The
-// four waves share a list, or with OWN have one each.
-template <class T, int D, bool OWN>
+// four waves share a list, or with OWN have one each; with PACK the lists of
+// neighbouring query blocks share a wave's 32 rows as in the forward kernel.
+template <class T, int D, bool OWN, bool PACK>
 __global__ __launch_bounds__(256, 2) void attn_dq_stream(const AttnArgs a) {
   using L = Tile<D>;
   constexpr int KT = 32, kSubs = kAttnPage / KT;
   constexpr int kHalf = KT * L::kRowBytes;
   constexpr int kLoads = kHalf / 1024;
   constexpr int kX = D / 16, kI = D / 32;
+  static_assert(!PACK || OWN, "packed lists are a wave's own");
   static_assert(3 * (D / 2 + 1) * 256 <= 8 * kHalf, "the waves' sums fit the tiles");
   extern __shared__ __attribute__((aligned(1024))) char lds[];
 
@@ -439,17 +442,29 @@ __global__ __launch_bounds__(256, 2) void attn_dq_stream(const AttnArgs a) {
   for (int i = 0; i < kI; ++i) dq[i] = zero16();
   float sum = 0.0f;
   const float c = a.scale * kLog2e;
-  const int32_t *list = a.lists + ((static_cast<int64_t>(b) * a.hk + h) * a.nqb + qb) * a.max_blocks;
+  const int64_t head0 = (static_cast<int64_t>(b) * a.hk + h) * (PACK ? a.list_nqb : a.nqb);
+  const int32_t *list = a.lists + (head0 + static_cast<int64_t>(qb) * (PACK ? a.pack : 1)) * a.max_blocks;
+  const int lists = PACK ? min(a.pack, a.list_nqb - qb * a.pack) : 1;  // of the tile
+  const int mine = PACK ? (lane & 31) / (a.rows / a.pack) : 0;         // the row's among them
+  const int32_t entries = lists * a.max_blocks;
   constexpr int kStep = OWN ? 1 : 4;
   const int first = OWN ? 0 : wave;
 
+  // for delta if the list is short; all lists together; then if need be one by one
 #pragma unroll 1
-  for (int walk = 0; walk < 2; ++walk) {
+  for (int pass = -2; pass < (PACK ? lists : 0); ++pass) {
+    const uint32_t take = pass < 0 ? ~0u : 1u << pass;
     int named = 0;
-    for (int32_t e = 0; e < a.max_blocks; e += 64) {
-      const Named blocks = named_blocks(list, nullptr, 0, e, a.max_blocks, row.last_key, lane);
+    for (int32_t e = 0; e < entries; e += 64) {
+      Shared blocks;
+      if constexpr (PACK) {
+        blocks = shared_blocks(list, entries, a.max_blocks, nullptr, 0, take, row.last_key, lane);
+      } else {
+        const Named n = named_blocks(list, nullptr, 0, e, entries, row.last_key, lane);
+        blocks = Shared{n.id, n.page, 1, n.n};
+      }
       named += blocks.n;
-      if (walk == 0 && named > kFew) break;
+      if (pass == -2 && named > kFew) break;
       const int tiles = blocks.n * kSubs;
       // past the last tile the loads are of no bytes, so that the waits below
       // always count the same loads
@@ -482,6 +497,17 @@ __global__ __launch_bounds__(256, 2) void attn_dq_stream(const AttnArgs a) {
         ks.begin();
         ks.run([&](int x, u32x4 k) { s = T::mma(k, row.q[x], s); });
         auto ts = operands<2 * kI, kAhead>([&](int i) { return L::operand_t(kt, 16 * (i / kI), i % kI, lane); });
+        if constexpr (PACK) {
+          const int members = __builtin_amdgcn_readlane(blocks.members, t / kSubs);
+          if (members != (1 << lists) - 1) {
+            const bool in = members >> mine & 1;
+#pragma unroll
+            for (int e2 = 0; e2 < 16; ++e2) {
+              s[e2] = in ? s[e2] : -INFINITY;
+              dp[e2] = in ? dp[e2] : 0.0f;
+            }
+          }
+        }
         row.ds(s, dp, key0, c, lane, sum);
         ts.begin();
         add_dq<T, D>(s, ts, dq);
@@ -490,19 +516,30 @@ __global__ __launch_bounds__(256, 2) void attn_dq_stream(const AttnArgs a) {
       }
       wait_vm<0>();  // the loads of no bytes
     }
-    if (walk == 0) {
+    if (pass == -2) {
       if (named <= kFew) row.delta += sum_groups<1, OWN ? 1 : 4>(lds, wave, lane, add_halves(sum));
-      sum = 0.0f;
+    } else {
+      sum = add_halves(sum);
+      if constexpr (!OWN) {
+        join_dq<D, 1, 4>(lds, wave, lane, dq, sum);
+        if (wave > 0) return;
+      }
+      if (!PACK || (take >> mine & 1)) row.store(a, lane, dq, sum);
+      if constexpr (PACK) {
+        if (pass < 0) {
+          float x = 0.0f;  // NaN where anything is not finite
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) dq[i] = zero16();
+          for (int i = 0; i < kI; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x = __builtin_fmaf(dq[i][e], 0.0f, x);
+          if (!__any(row.lse2 != INFINITY && x != x)) return;
+        }
+      }
     }
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kI; ++i) dq[i] = zero16();
   }
-  sum = add_halves(sum);
-  if constexpr (!OWN) {
-    join_dq<D, 1, 4>(lds, wave, lane, dq, sum);
-    if (wave > 0) return;
-  }
-  row.store(a, lane, dq, sum);
 }
 
 // The kernel's arguments, read again: what a loop's body needs of them would
@@ -854,16 +891,16 @@ hipError_t run_dq(const AttnArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <class T, int D, bool OWN>
+template <class T, int D, bool OWN, bool PACK>
 hipError_t run_dq_stream(const AttnArgs &a, hipStream_t s) {
   constexpr size_t kLds = 4 * 2 * 32 * D * 2;
   const int64_t lists = static_cast<int64_t>(a.b) * a.nqb;
   const int64_t grid = static_cast<int64_t>(a.hk) * ((OWN ? (lists + 3) / 4 : lists) + static_cast<int64_t>(a.b) * a.nkb);
   if (grid == 0) return hipSuccess;
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
-  hipError_t e = allow_dynamic_lds(reinterpret_cast<const void *>(&attn_dq_stream<T, D, OWN>), kLds);
+  hipError_t e = allow_dynamic_lds(reinterpret_cast<const void *>(&attn_dq_stream<T, D, OWN, PACK>), kLds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((attn_dq_stream<T, D, OWN>), dim3(static_cast<unsigned>(grid)), dim3(256), kLds, s, a);
+  hipLaunchKernelGGL((attn_dq_stream<T, D, OWN, PACK>), dim3(static_cast<unsigned>(grid)), dim3(256), kLds, s, a);
   return hipGetLastError();
 }
 
@@ -874,8 +911,12 @@ hipError_t run_backward(const AttnArgs &a, hipStream_t s) {
     // a wave a list where there are enough lists to fill the chip (8 waves a
     // CU) twice over
     case 1:
-      e = static_cast<int64_t>(a.b) * a.hk * a.nqb >= 4096 ? run_dq_stream<T, D, true>(a, s)
-                                                            : run_dq_stream<T, D, false>(a, s);
+      if (const int64_t lists = static_cast<int64_t>(a.b) * a.hk * a.nqb; lists >= 4096) {
+        const int32_t pack = a.nqb > 1 ? attn_pack(lists, a.rows, a.max_blocks) : 0;
+        e = pack ? run_dq_stream<T, D, true, true>(attn_packed(a, pack), s) : run_dq_stream<T, D, true, false>(a, s);
+      } else {
+        e = run_dq_stream<T, D, false, false>(a, s);
+      }
       break;
     case 2: e = run_dq<T, D, 2, 2, 32>(a, s); break;
     // two workgroups of four waves a CU rather than one of eight: one reads

@@ -268,5 +268,48 @@ __device__ __forceinline__ Named named_blocks(const int32_t *list, const int32_t
   return r;
 }
 
+// The blocks that consecutive lists of per_list entries name (those lists
+// whose bit is set in `take`), each once, in the first n lanes; members has
+// the bits of the lists that name it.  At most 64 entries in all, one a lane.
+// A block that a list names twice stands twice.
+struct Shared {
+  int id, page, members, n;
+};
+__device__ __forceinline__ Shared shared_blocks(const int32_t *lists, int entries, int per_list,
+                                                const int32_t *table_row, int32_t pages, uint32_t take,
+                                                int32_t last_key, int lane) {
+  int id = lane < entries ? lists[lane] : -1;
+  const int list = lane / per_list;
+  if (!attn_names(id, last_key) || !(take >> (list & 31) & 1)) id = -1;
+  const int page = id >= 0 ? attn_page(table_row, id, pages) : -1;
+  if (page < 0) id = -1;
+  const uint64_t below = (uint64_t(1) << lane) - 1;
+  const uint64_t one = per_list >= 64 ? ~uint64_t(0) : (uint64_t(1) << per_list) - 1;
+  auto equal = [&](int key) {  // the lanes whose key is this lane's
+    unsigned lo = 0, hi = 0;
+    for (int l = 0; l < entries; ++l) {
+      const uint64_t m = __ballot(key == __builtin_amdgcn_readlane(key, l));
+      lo = lane == l ? static_cast<unsigned>(m) : lo;
+      hi = lane == l ? static_cast<unsigned>(m >> 32) : hi;
+    }
+    return uint64_t(hi) << 32 | lo;
+  };
+  uint64_t same = equal(id);
+  const int again = __builtin_popcountll(same & (one << (list * per_list & 63)) & below);
+  if (__any(id >= 0 && again > 0)) same = equal(id * 64 + again);  // id < 2^25
+  int members = 0;
+  for (int l = 0; l * per_list < entries; ++l) members |= ((same & (one << (l * per_list))) != 0) << l;
+  const bool leads = id >= 0 && (same & below) == 0;
+  const uint64_t ok = __ballot(leads);
+  const int before = __builtin_popcountll(ok & below), n = __builtin_popcountll(ok);
+  const int to = leads ? before : n + lane - before;  // every lane has a place of its own
+  Shared r;
+  r.id = __builtin_amdgcn_ds_permute(4 * to, id);
+  r.page = __builtin_amdgcn_ds_permute(4 * to, page);
+  r.members = __builtin_amdgcn_ds_permute(4 * to, members);
+  r.n = __builtin_amdgcn_readfirstlane(n);
+  return r;
+}
+
 }  // namespace attn
 }  // namespace sdm

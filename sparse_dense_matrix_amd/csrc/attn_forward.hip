@@ -339,19 +339,38 @@ __global__ __launch_bounds__(64 * RW * KW, 2) void attn_forward(const AttnArgs a
 // Small buffers put 8 waves on a CU (registers allow no more), which covers
 // each wave's waits.  KW waves share a list's tiles and join their sums; with
 // KW = 1 a list is a wave's own.
-template <class T, int D, int KW>
+//
+// With PACK the lists of neighbouring query blocks share a wave's 32 rows: a
+// block that several of them name is read once, and rows whose list does not
+// name it have weights of zero there.  What each list alone would read and
+// multiply (its tile has 32 rows, used or not) is never less.  A weight of
+// zero does not make an infinite or NaN value harmless, so where a row comes
+// out as neither finite the lists are gone through again one by one.
+template <class T, int D, int KW, bool PACK>
 __global__ __launch_bounds__(64 * KW, 2) void attn_stream(const AttnArgs a) {
   using L = Tile<D>;
   constexpr int KT = 32, kSubs = kAttnPage / KT;
   constexpr int kHalf = KT * L::kRowBytes;
   constexpr int kLoads = kHalf / 1024;
+  static_assert(!PACK || KW == 1, "packed lists are a wave's own");
   extern __shared__ __attribute__((aligned(1024))) char lds[];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Item it = item_of(a);
   const Row row = row_of(a, it, 32, 0, lane);
-  const Range range = range_of(a, it, row);
+  Range range;
+  int lists = 1, list = 0;  // lists of the tile; the row's among them
+  if constexpr (PACK) {
+    lists = min(a.pack, a.list_nqb - it.qb * a.pack);
+    list = (lane & 31) / (a.rows / a.pack);
+    range.list = a.lists + ((static_cast<int64_t>(it.b) * a.hk + it.h) * a.list_nqb + static_cast<int64_t>(it.qb) * a.pack) * a.max_blocks;
+    range.table_row = a.table ? a.table + static_cast<int64_t>(it.b) * a.nkb : nullptr;
+    range.e0 = 0;
+    range.e1 = lists * a.max_blocks;  // at most 64
+  } else {
+    range = range_of(a, it, row);
+  }
   u32x4 q[D / 16];
   load_q<D>(a, it, row, lane, q);
 
@@ -364,61 +383,89 @@ __global__ __launch_bounds__(64 * KW, 2) void attn_stream(const AttnArgs a) {
     koff[i] = static_cast<uint32_t>(r * a.k.st + c);
     voff[i] = static_cast<uint32_t>(r * a.v.st + c);
   }
-  f32x16 o[D / 32];
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) o[i] = zero16();
-  Stats st;
   const float c = a.scale * kLog2e;
 
-  for (int32_t e = range.e0; e < range.e1; e += 64) {
-    const Named blocks = named_blocks(range.list, range.table_row, a.pages, e, range.e1, row.last_key, lane);
-    const int tiles = blocks.n * kSubs;
-    // past the last tile the loads are of no bytes, so that the waits below
-    // always count the same loads
-    auto issue = [&](int t, bool values) {
-      const int at = t < tiles ? t / kSubs : 0;
-      const int id = __builtin_amdgcn_readlane(blocks.id, at);
-      const int page = __builtin_amdgcn_readlane(blocks.page, at);
-      const int32_t first = (t % kSubs) * KT;
-      const int32_t kept = t < tiles ? min(KT, row.last_key + 1 - id * kAttnPage - first) : 0;
-      const i32x4 buf = keys_of<D>(a, values ? a.v : a.k, it, id, page, first, kept);
+#pragma unroll 1
+  for (int pass = -1; pass < (PACK ? lists : 0); ++pass) {  // all lists together, then if need be one by one
+    const uint32_t take = pass < 0 ? ~0u : 1u << pass;
+    f32x16 o[D / 32];
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i)
-        load_lds16(lds_k + (values ? kHalf : 0) + i * 1024, buf, values ? voff[i] : koff[i]);
-    };
-    if (wave < tiles) {
-      issue(wave, false);
-      issue(wave, true);
+    for (int i = 0; i < D / 32; ++i) o[i] = zero16();
+    Stats st;
+    for (int32_t e = range.e0; e < range.e1; e += 64) {
+      Shared blocks;
+      if constexpr (PACK) {
+        blocks = shared_blocks(range.list, range.e1, a.max_blocks, range.table_row, a.pages, take, row.last_key, lane);
+      } else {
+        const Named b = named_blocks(range.list, range.table_row, a.pages, e, range.e1, row.last_key, lane);
+        blocks = Shared{b.id, b.page, 1, b.n};
+      }
+      const int tiles = blocks.n * kSubs;
+      // past the last tile the loads are of no bytes, so that the waits below
+      // always count the same loads
+      auto issue = [&](int t, bool values) {
+        const int at = t < tiles ? t / kSubs : 0;
+        const int id = __builtin_amdgcn_readlane(blocks.id, at);
+        const int page = __builtin_amdgcn_readlane(blocks.page, at);
+        const int32_t first = (t % kSubs) * KT;
+        const int32_t kept = t < tiles ? min(KT, row.last_key + 1 - id * kAttnPage - first) : 0;
+        const i32x4 buf = keys_of<D>(a, values ? a.v : a.k, it, id, page, first, kept);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+          load_lds16(lds_k + (values ? kHalf : 0) + i * 1024, buf, values ? voff[i] : koff[i]);
+      };
+      if (wave < tiles) {
+        issue(wave, false);
+        issue(wave, true);
+      }
+      for (int t = wave; t < tiles; t += KW) {
+        const int32_t key0 = __builtin_amdgcn_readlane(blocks.id, t / kSubs) * kAttnPage + (t % kSubs) * KT;
+        wait_vm<kLoads>();
+        f32x16 s = zero16();
+        auto ks = operands<D / 16, D / 16>([&](int x) { return L::operand(kt, 0, x, lane); });
+        ks.begin();
+        ks.run([&](int x, u32x4 k) { s = T::mma(k, q[x], s); });
+        wait_lds();
+        issue(t + KW, false);
+        if constexpr (PACK) {
+          const int members = __builtin_amdgcn_readlane(blocks.members, t / kSubs);
+          if (members != (1 << lists) - 1) {
+            const bool in = members >> list & 1;
+#pragma unroll
+            for (int e2 = 0; e2 < 16; ++e2) s[e2] = in ? s[e2] : -INFINITY;
+          }
+        }
+        softmax<D, 1>(a, row, key0, lane, c, &s, st, o);
+        wait_vm<kLoads>();
+        constexpr int kI = D / 32;
+        auto vs = operands<2 * kI, kI>([&](int i) { return L::operand_t(vt, 16 * (i / kI), i % kI, lane); });
+        vs.begin();
+        const u32x4 p[2] = {pack8<T>(s, 0), pack8<T>(s, 1)};
+        vs.run([&](int i, u32x4 v) { o[i % kI] = T::mma(v, p[i / kI], o[i % kI]); });
+        wait_lds();
+        issue(t + KW, true);
+      }
+      wait_vm<0>();  // the loads of no bytes
     }
-    for (int t = wave; t < tiles; t += KW) {
-      const int32_t key0 = __builtin_amdgcn_readlane(blocks.id, t / kSubs) * kAttnPage + (t % kSubs) * KT;
-      wait_vm<kLoads>();
-      f32x16 s = zero16();
-      auto ks = operands<D / 16, D / 16>([&](int x) { return L::operand(kt, 0, x, lane); });
-      ks.begin();
-      ks.run([&](int x, u32x4 k) { s = T::mma(k, q[x], s); });
-      wait_lds();
-      issue(t + KW, false);
-      softmax<D, 1>(a, row, key0, lane, c, &s, st, o);
-      wait_vm<kLoads>();
-      constexpr int kI = D / 32;
-      auto vs = operands<2 * kI, kI>([&](int i) { return L::operand_t(vt, 16 * (i / kI), i % kI, lane); });
-      vs.begin();
-      const u32x4 p[2] = {pack8<T>(s, 0), pack8<T>(s, 1)};
-      vs.run([&](int i, u32x4 v) { o[i % kI] = T::mma(v, p[i / kI], o[i % kI]); });
-      wait_lds();
-      issue(t + KW, true);
-    }
-    wait_vm<0>();  // the loads of no bytes
-  }
 
-  st.l = add_halves(st.l);
-  if (!row.live) st = Stats();
-  if constexpr (KW > 1) {
-    join_groups<D, 1, KW>(lds, wave, lane, st, o);
-    if (wave > 0) return;
+    st.l = add_halves(st.l);
+    if (!row.live) st = Stats();
+    if constexpr (KW > 1) {
+      join_groups<D, 1, KW>(lds, wave, lane, st, o);
+      if (wave > 0) return;
+    }
+    if (!PACK || (take >> list & 1)) store<T, D>(a, it, row, lane, st.m, st.l, o);
+    if constexpr (PACK) {
+      if (pass < 0) {
+        float x = 0.0f;  // NaN where anything is not finite
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x = __builtin_fmaf(o[i][e], 0.0f, x);
+        if (!__any(row.live && x != x)) return;
+      }
+    }
   }
-  store<T, D>(a, it, row, lane, st.m, st.l, o);
 }
 
 // The sums m, l, o joined with others of the same row.
@@ -488,14 +535,14 @@ hipError_t run(const AttnArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <class T, int D, int KW>
+template <class T, int D, int KW, bool PACK>
 hipError_t run_stream(const AttnArgs &a, hipStream_t s) {
   constexpr size_t kTiles = static_cast<size_t>(KW) * 2 * 32 * D * 2;
   constexpr size_t kSums = static_cast<size_t>(KW - 1) * (D / 2 + 2) * 256;
   constexpr size_t kLds = kTiles > kSums ? kTiles : kSums;
-  hipError_t e = allow_dynamic_lds(reinterpret_cast<const void *>(&attn_stream<T, D, KW>), kLds);
+  hipError_t e = allow_dynamic_lds(reinterpret_cast<const void *>(&attn_stream<T, D, KW, PACK>), kLds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((attn_stream<T, D, KW>), dim3(static_cast<unsigned>(grid_of(a))), dim3(64 * KW), kLds, s, a);
+  hipLaunchKernelGGL((attn_stream<T, D, KW, PACK>), dim3(static_cast<unsigned>(grid_of(a))), dim3(64 * KW), kLds, s, a);
   return hipGetLastError();
 }
 
@@ -507,7 +554,14 @@ hipError_t run_tile(const AttnArgs &a, hipStream_t s) {
   switch (attn_tile(a.rows).row_waves) {
     // a wave a list where there are enough lists to fill the chip (8 waves a
     // CU) twice over
-    case 1: e = grid_of(a) >= 4096 && a.nsplit == 1 ? run_stream<T, D, 1>(a, s) : run_stream<T, D, 4>(a, s); break;
+    case 1:
+      if (grid_of(a) >= 4096 && a.nsplit == 1) {
+        const int32_t pack = a.lists && a.nqb > 1 ? attn_pack(grid_of(a), a.rows, a.max_blocks) : 0;
+        e = pack ? run_stream<T, D, 1, true>(attn_packed(a, pack), s) : run_stream<T, D, 1, false>(a, s);
+      } else {
+        e = run_stream<T, D, 4, false>(a, s);
+      }
+      break;
     case 2: e = run<T, D, 2, 2, 32>(a, s); break;
     case 4: e = run<T, D, 4, 1, 64>(a, s); break;
     default: e = run<T, D, 8, 1, 64>(a, s); break;
@@ -541,6 +595,23 @@ AttnTile attn_tile(int32_t rows) {
   t.key_tile = best <= 2 ? 32 : 64;
   t.rows = 32 * best;
   return t;
+}
+
+int32_t attn_pack(int64_t lists, int32_t rows, int32_t max_blocks) {
+  // as many as fill a tile and a wave's lanes, while a wave is left for each
+  // of the 8 places of a CU
+  int32_t n = 1;
+  while (n < 16 && 2 * n * rows <= 32 && 2 * n * max_blocks <= 64 && lists / (2 * n) >= 2048) n *= 2;
+  return n > 1 ? n : 0;
+}
+
+AttnArgs attn_packed(AttnArgs a, int32_t pack) {
+  a.pack = pack;
+  a.list_nqb = a.nqb;
+  a.rows *= pack;
+  a.q_block *= pack;
+  a.nqb = (a.nqb + pack - 1) / pack;
+  return a;
 }
 
 hipError_t launch_attn_forward(const AttnArgs &a, spmm_dtype_t t, int d, hipStream_t s) {

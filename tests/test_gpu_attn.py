@@ -686,3 +686,69 @@ def test_plan_out_of_memory(S, monkeypatch):
     assert n > 6
     monkeypatch.delenv("SPMM_TEST_FAIL_ALLOC")
     plan(S, case(), backward=True)
+
+
+# ---- lists that share a row tile -------------------------------------------
+
+PACKED = [
+    case(b=2, nq=1100, hq=32, hk=2, d=128, q_block=1, blocks=5),
+    case(b=1, nq=1050, hq=12, hk=4, d=64, q_block=1, blocks=3, dtype=torch.float16),
+    case(b=1, nq=2100, hq=8, hk=4, d=64, q_block=1, blocks=4),
+    case(b=1, nq=2060, nk=500, hq=4, hk=4, d=128, q_block=2, blocks=7, dtype=torch.float16),
+]
+
+
+def packed_lists(c, g):
+    """Lists of neighbours that share blocks, with gaps, some empty, some
+    naming a block twice, some past the end."""
+    lists = random_lists(c, g, empty=0.1)
+    lists[:, :, 1::3] = lists[:, :, :-1:3][:, :, :lists[:, :, 1::3].shape[2]]
+    lists[:, :, ::5, 1] = lists[:, :, ::5, 0]
+    lists[:, :, ::7, -1] = 2 ** 31 - 1
+    lists[:, :, ::11, 0] = -1
+    return lists
+
+
+@pytest.mark.parametrize("n", range(len(PACKED)))
+def test_lists_that_share_a_tile(S, n):
+    c = PACKED[n]
+    assert c["b"] * c["hk"] * -(-c["nq"] // c["q_block"]) >= 4096
+    q, k, v, grad, g = inputs(c, 900 + n)
+    lists = packed_lists(c, g)
+    nk = c["nk"]
+    lens = torch.tensor([nk, nk - 77][:c["b"]], dtype=torch.int32)
+    starts = torch.tensor([nk - c["nq"], -5][:c["b"]], dtype=torch.int32).clamp(max=20)
+    P = plan(S, c, backward=True)
+    o, lse = run_forward(S, c, q.cuda(), k.cuda(), v.cuda(), lists.cuda(), lens.cuda(), starts.cuda(), P)
+    dq, dk, dv = (torch.full_like(t, float("nan")).cuda() for t in (q, k, v))
+    S.spmm_execute_attn_backward(P, grad.cuda(), q.cuda(), k.cuda(), v.cuda(), lists.cuda(), o, lse, dq, dk, dv,
+                                 lens=lens.cuda(), starts=starts.cuda())
+    want = R.attention(c, q.double(), k.double(), v.double(), R.sees(c, lists, lens, starts, None), grad.double())
+    for name, got in (("o", o), ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv)):
+        R.check(name, got, *want[name])
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_neighbours_list_does_not_spoil_a_row(S, bad):
+    """A block with values that are no numbers, named by one list of a tile:
+    the other lists' rows come out as without it."""
+    c = case(b=2, nq=1100, hq=32, hk=2, d=128, q_block=1, blocks=2)
+    q, k, v, grad, g = inputs(c, 950)
+    starts = torch.tensor([0, 0], dtype=torch.int32)
+    lists = torch.zeros((2, 2, 1100, 2), dtype=torch.int32)
+    lists[..., 1] = -1
+    lists[:, :, 901::9, 1] = 3
+    clean = [t.clone() for t in (k, v)]
+    k[:, 200], v[:, 210] = bad, bad  # in block 3
+    sees3 = (lists[..., 1] == 3).repeat_interleave(16, 1)  # [b, hq, nq]
+    outs = []
+    for k1, v1 in ((k, v), clean):
+        P = plan(S, c, backward=True)
+        o, lse = run_forward(S, c, q.cuda(), k1.cuda(), v1.cuda(), lists.cuda(), None, starts.cuda(), P)
+        dq, dk, dv = (torch.full_like(t, float("nan")).cuda() for t in (q, k, v))
+        S.spmm_execute_attn_backward(P, grad.cuda(), q.cuda(), k1.cuda(), v1.cuda(), lists.cuda(), o, lse, dq, dk, dv)
+        outs.append([o.cpu().transpose(1, 2), lse.cpu(), dq.cpu().transpose(1, 2)])
+    for x, y in zip(*outs):
+        assert torch.isfinite(y).all()
+        assert torch.equal(x[~sees3], y[~sees3])
+    assert not torch.isfinite(outs[0][0][sees3]).all()
