@@ -44,7 +44,8 @@ __device__ __forceinline__ u32x2 round8(const double *sum, double top) {
 __device__ __forceinline__ double top_of(double x, double y) { return y > x || y != y ? y : x; }
 
 // A wave pools one block of one head: 16 bytes a lane, rows over the other
-// lanes.  Bound by reading the keys once.
+// lanes.  Bound by reading the keys once: 32k tokens of 8 key heads 15.5 us,
+// 4.3 TB/s.
 template <class T, int D>
 __global__ __launch_bounds__(256) void attn_pool(const AttnPoolArgs a) {
   constexpr int kPieces = D / 8, kStep = 64 / kPieces;
@@ -110,7 +111,11 @@ constexpr int kSelThreads = 256;
 // One workgroup a list.  The queries' sum is bound by reading them; the
 // scores read the pooled keys of the visible blocks from L2.  The threshold
 // (the blocks-th highest score) is found bit by bit by one wave with the
-// scores in LDS, stopping as soon as the count fits.
+// scores in LDS, stopping as soon as the count fits.  32k tokens, 32 heads over
+// 8: 69 us, 3.9 TB/s of queries; one token of 32 sequences 10.5 us, which is the
+// chain of its loads and steps.  Loading the first pooled keys before the
+// queries' sum takes 0.4 us off that, but costs the prompt 17 us: its registers
+// leave half as many lists on a CU.
 template <class T, int D>
 __global__ __launch_bounds__(kSelThreads) void attn_select(const AttnSelectArgs a) {
   constexpr int kPieces = D / 8, kStep = kSelThreads / kPieces, kWaves = kSelThreads / 64;
