@@ -25,6 +25,7 @@ namespace {
 
 constexpr int kAhead = 4;               // operands read ahead of their product
 constexpr int kCus = 256;
+constexpr int kShort = 128;             // queries of a short sequence
 constexpr int kFew = 2;                 // blocks of a short list
 constexpr int kMaxChunk = 1024;         // query blocks of an item
 constexpr uint32_t kDeadRow = 0xffffff00u;  // offset past every buffer: a direct load gives zeros
@@ -573,7 +574,12 @@ __device__ __forceinline__ AttnArgs args_again() {
 // queues 640 us, 0.83 PFLOP/s: the matrix cores are busy for 37% of it, and the
 // rows come from beyond L2 in half of all loads (each is read once for every
 // key block that its list names).
-template <class T, int D, int RG>
+// FINE is for sequences of up to kShort queries: P and dS enter their products
+// as two operands as dS does for dq.  With few rows to a key the rounding of a
+// single dS may be all of dk's error, up to twice that of rounding dk; past
+// 128 queries it is 1.4 times, and the second operands would cost a quarter more
+// products.
+template <class T, int D, int RG, bool FINE>
 __device__ __forceinline__ void dkv_item(const AttnArgs &a, char *lds, int64_t at) {
   using L = Tile<D>;
   constexpr int kRows = 32 * RG;
@@ -766,11 +772,17 @@ __device__ __forceinline__ void dkv_item(const AttnArgs &a, char *lds, int64_t a
         dp[4 * g4 + i] = s[4 * g4 + i] * (dp[4 * g4 + i] - d4[i]);
       }
     }
-    const u32x4 w[4] = {pack8<T>(s, 0), pack8<T>(s, 1), pack8<T>(dp, 0), pack8<T>(dp, 1)};
+    u32x4 w[4], low[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if constexpr (FINE) split8<T>(x < 2 ? s : dp, x % 2, w[x], low[x]);
+      else w[x] = pack8<T>(x < 2 ? s : dp, x % 2);
+    }
     ts.begin();
     ts.run([&](int i, u32x4 x) {
       f32x16 &to = i < 2 * kI ? dv[i % kI] : dk[i % kI];
       to = T::mma(x, w[i / kI], to);
+      if constexpr (FINE) to = T::mma(x, low[i / kI], to);
     });
   }
   {
@@ -828,7 +840,7 @@ __device__ __forceinline__ void dkv_item(const AttnArgs &a, char *lds, int64_t a
 // it and the items differ in length.  Queue x holds every eighth item, so that
 // with 8 key heads XCD x keeps to one of them; a workgroup whose queue is empty
 // goes on to the next one that is not.
-template <class T, int D, int RG>
+template <class T, int D, int RG, bool FINE>
 __global__ __launch_bounds__(128 * RG) void attn_dkv(const AttnArgs) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   __shared__ int32_t taken[2];  // queue, or -1: nothing is left; place in it
@@ -836,7 +848,7 @@ __global__ __launch_bounds__(128 * RG) void attn_dkv(const AttnArgs) {
   for (;;) {
     const AttnArgs a = args_again();
     const int64_t items = static_cast<int64_t>(a.b) * a.slots * a.hk;
-    if (item < items) dkv_item<T, D, RG>(a, lds, item);
+    if (item < items) dkv_item<T, D, RG, FINE>(a, lds, item);
     if (items <= gridDim.x) return;
     __syncthreads();
     if (threadIdx.x < 64) {
@@ -911,6 +923,19 @@ hipError_t run_dq_stream(const AttnArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <class T, int D, bool FINE>
+hipError_t run_dkv(const AttnArgs &a, hipStream_t s) {
+  constexpr int kRG = 4;
+  const size_t lds = 4 * 32 * kRG * D * 2 + kAttnPage * D * 2 + 2 * (2 * 32 * kRG * 4) + 4 * (3 * 32 * kRG * 4 + 16) +
+                     static_cast<size_t>(a.chunk) * 4;
+  const int64_t grid = static_cast<int64_t>(a.b) * a.hk * a.slots;
+  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  hipError_t e = allow_dynamic_lds(reinterpret_cast<const void *>(&attn_dkv<T, D, kRG, FINE>), lds + (kMaxChunk - a.chunk) * 4);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((attn_dkv<T, D, kRG, FINE>), dim3(static_cast<unsigned>(std::min<int64_t>(grid, kCus))), dim3(128 * kRG), lds, s, a);
+  return hipGetLastError();
+}
+
 template <class T, int D>
 hipError_t run_backward(const AttnArgs &a, hipStream_t s) {
   hipError_t e;
@@ -936,17 +961,10 @@ hipError_t run_backward(const AttnArgs &a, hipStream_t s) {
     }
   }
   if (e != hipSuccess || a.nkb == 0) return e;
-  constexpr int kRG = 4;
-  const size_t lds = 4 * 32 * kRG * D * 2 + kAttnPage * D * 2 + 2 * (2 * 32 * kRG * 4) + 4 * (3 * 32 * kRG * 4 + 16) +
-                     static_cast<size_t>(a.chunk) * 4;
-  const int64_t grid = static_cast<int64_t>(a.b) * a.hk * a.slots;
-  const int64_t merge = static_cast<int64_t>(a.b) * a.hk * a.nkb * (2 * kAttnPage * D / 4 / 256);
-  if (grid > 0x7fffffff || merge > 0x7fffffff) return hipErrorInvalidValue;
-  e = allow_dynamic_lds(reinterpret_cast<const void *>(&attn_dkv<T, D, kRG>), lds + (kMaxChunk - a.chunk) * 4);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((attn_dkv<T, D, kRG>), dim3(static_cast<unsigned>(std::min<int64_t>(grid, kCus))), dim3(128 * kRG), lds, s, a);
-  e = hipGetLastError();
+  e = a.nq <= kShort ? run_dkv<T, D, true>(a, s) : run_dkv<T, D, false>(a, s);
   if (e != hipSuccess || a.slots == a.nkb) return e;
+  const int64_t merge = static_cast<int64_t>(a.b) * a.hk * a.nkb * (2 * kAttnPage * D / 4 / 256);
+  if (merge > 0x7fffffff) return hipErrorInvalidValue;
   hipLaunchKernelGGL((attn_dkv_merge<T, D>), dim3(static_cast<unsigned>(merge)), dim3(256), 0, s, a);
   return hipGetLastError();
 }

@@ -752,3 +752,42 @@ def test_a_neighbours_list_does_not_spoil_a_row(S, bad):
         assert torch.isfinite(y).all()
         assert torch.equal(x[~sees3], y[~sees3])
     assert not torch.isfinite(outs[0][0][sees3]).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("nq,q_block,hk", [(1, 1, 4), (2, 64, 1), (6, 16, 2), (100, 4, 4), (128, 64, 2)])
+def test_dk_dv_of_short_sequences_are_off_by_their_own_rounding(S, nq, q_block, hk, dtype):
+    """Up to 128 queries: the rounding of dk and dv, and errors of 32-bit sums."""
+    c = case(b=2, nq=nq, hq=4, hk=hk, d=128, q_block=q_block, blocks=2, dtype=dtype)
+    q, k, v, grad, g = inputs(c, 970 + nq)
+    lists = torch.tensor([0, 1], dtype=torch.int32).expand(2, hk, -(-nq // q_block), 2).contiguous()
+    P = plan(S, c, backward=True)
+    o, lse = run_forward(S, c, q.cuda(), k.cuda(), v.cuda(), lists.cuda(), None, None, P)
+    dq, dk, dv = (torch.full_like(t, float("nan")).cuda() for t in (q, k, v))
+    S.spmm_execute_attn_backward(P, grad.cuda(), q.cuda(), k.cuda(), v.cuda(), lists.cuda(), o, lse, dq, dk, dv)
+    q, k, v, grad = (t.double().permute(0, 2, 1, 3) for t in (q, k, v, grad))
+    k, v = k.repeat_interleave(4 // hk, 1), v.repeat_interleave(4 // hk, 1)
+    scale = 1.0 / math.sqrt(128)
+    s = (scale * (q @ k.transpose(-1, -2))).masked_fill(torch.ones(nq, nq).triu(1).bool(), -math.inf)
+    p = torch.softmax(s, -1)
+    dp = grad @ v.transpose(-1, -2)
+    delta = (p * dp).sum(-1, keepdim=True)
+    ds = p * (dp - delta)
+    u, e32 = torch.finfo(dtype).eps / 2, 2.0 ** -24
+    tiny = torch.finfo(dtype).smallest_normal * u
+    # as for dq: a weight's score of 130 terms, exponents, the rounded lse
+    ew = (2 * 130 * scale * (q.abs() @ k.abs().transpose(-1, -2)).amax(-1, keepdim=True) + 64) * e32
+    edp = 130 * e32 * (grad.abs() @ v.abs().transpose(-1, -2))
+    edelta = (p * (edp + (ew + 400 * e32) * dp.abs())).sum(-1, keepdim=True)
+    on = (p > 0).double()
+    eds = 1.02 * ((u * u + ew) * ds.abs() + p * (edp + edelta + 4 * e32 * (dp.abs() + delta.abs()))) + tiny * on
+    ep = 1.02 * (u * u + ew) * p + tiny * on
+    rows = 4 // hk * nq
+
+    def per_key(x):
+        return x.reshape(2, hk, 4 // hk, nq, 128).sum(2).permute(0, 2, 1, 3)
+
+    for name, got, w, e, x, f in (("dk", dk, ds, eds, q, scale), ("dv", dv, p, ep, grad, 1.0)):
+        want = per_key(f * (w.transpose(-1, -2) @ x))
+        off = per_key(f * ((e + rows * e32 * w.abs()).transpose(-1, -2) @ x.abs()))
+        R.check(name, got, want, (u + 4 * e32) * (want.abs() + off) + off + tiny)
