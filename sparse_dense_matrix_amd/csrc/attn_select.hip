@@ -112,7 +112,8 @@ constexpr int kSelThreads = 256;
 // scores read the pooled keys of the visible blocks from L2.  The threshold
 // (the blocks-th highest score) is found bit by bit by one wave with the
 // scores in LDS, stopping as soon as the count fits.  32k tokens, 32 heads over
-// 8: 69 us, 3.9 TB/s of queries; one token of 32 sequences 10.5 us, which is the
+// 8: 60 us, 4.5 TB/s of queries (four rows of a lane in flight; with eight 69 us,
+// as fewer lists fit on a CU); one token of 32 sequences 10.5 us, which is the
 // chain of its loads and steps.  Loading the first pooled keys before the
 // queries' sum takes 0.4 us off that, but costs the prompt 17 us: its registers
 // leave half as many lists on a CU.
@@ -146,7 +147,7 @@ __global__ __launch_bounds__(kSelThreads) void attn_select(const AttnSelectArgs 
     double sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     const int rows = (t1 - t0) * a.group;
     const char *p = a.q.p + b * a.q.sb + static_cast<int64_t>(h) * a.group * a.q.sh + (tid % kPieces) * 16;
-#pragma unroll 8
+#pragma unroll 4
     for (int r = tid / kPieces; r < rows; r += kStep) {
       const int t = r / a.group;
       add8<T>(sum, *reinterpret_cast<const u32x4 *>(p + (t0 + t) * a.q.st + (r - t * a.group) * a.q.sh));
@@ -179,7 +180,7 @@ __global__ __launch_bounds__(kSelThreads) void attn_select(const AttnSelectArgs 
   }
   // scores: D / 16 lanes a block, 16 bytes each, kBatch blocks of a lane in
   // flight at once (page, then keys and scale)
-  constexpr int kLanes = D / 16, kStride = kSelThreads / kLanes, kBatch = 8;
+  constexpr int kLanes = D / 16, kStride = kSelThreads / kLanes, kBatch = 4;
   const i32x4 mine = *reinterpret_cast<const i32x4 *>(q8 + 4 * (tid % kLanes));
   const int32_t *table_row = a.table ? a.table + b * a.nkb : nullptr;
   for (int j0 = 0; j0 < count; j0 += kBatch * kStride) {
