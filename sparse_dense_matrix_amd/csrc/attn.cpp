@@ -157,7 +157,7 @@ spmm_status_t attn_shape(const spmm_attn_desc_t &d, spmm_plan_s *p) {
   a.max_blocks = d.max_blocks;
   a.scale = d.scale > 0.0f ? d.scale : 1.0f / std::sqrt(static_cast<float>(d.dim));
   a.rows = std::min(a.q_block, std::max(a.nq, 1)) * a.group;
-  const AttnTile t = attn_tile(a.rows);
+  const AttnTile t = attn_tile(a.rows, a.nqb);
   a.rtiles = (a.rows + t.rows - 1) / t.rows;
   const double tiles = static_cast<double>(a.b) * a.hk * a.nqb * a.rtiles;
   if (tiles > 0x7fffffff || static_cast<double>(a.b) * a.hk * a.nkb > 0x7fffffff ||

@@ -103,7 +103,7 @@ __host__ __device__ inline bool attn_names(int32_t id, int32_t last_key) {
 struct AttnTile {
   int32_t row_waves, key_waves, key_tile, rows;
 };
-AttnTile attn_tile(int32_t rows);
+AttnTile attn_tile(int32_t rows, int32_t nqb);
 // Lists that share a row tile of 32 rows (a power of two), for `lists` lists in
 // all with `rows` rows and max_blocks entries each; 0: one list a tile.
 int32_t attn_pack(int64_t lists, int32_t rows, int32_t max_blocks);

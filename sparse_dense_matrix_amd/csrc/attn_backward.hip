@@ -939,7 +939,7 @@ hipError_t run_dkv(const AttnArgs &a, hipStream_t s) {
 template <class T, int D>
 hipError_t run_backward(const AttnArgs &a, hipStream_t s) {
   hipError_t e;
-  switch (attn_tile(a.rows).row_waves) {
+  switch (attn_tile(a.rows, a.nqb).row_waves) {
     // a wave a list where there are enough lists to fill the chip (8 waves a
     // CU) twice over
     case 1:

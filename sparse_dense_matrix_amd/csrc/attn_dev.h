@@ -211,8 +211,9 @@ struct Tile {
   }
 };
 
-// N products whose LDS operands are read AHEAD products before their use (the
-// compiler reads each right before it and waits the whole latency out; only
+// N products whose LDS operands are read AHEAD products before their use (left
+// to itself the compiler reads each right before it and waits the latency out:
+// a prompt of 32k tokens took 1177 us that way, 1101 us with reads ahead; only
 // scalar and vector arithmetic may move across pin()).  begin() reads the
 // first ones, which may stand before other work.
 __device__ __forceinline__ void pin() { __builtin_amdgcn_sched_barrier(0x406); }

@@ -21,7 +21,7 @@ namespace attn {
 namespace {
 
 constexpr float kSlack = 8.0f;
-constexpr int kAhead = 4;  // operands read ahead of their product
+constexpr int kAhead = 2;  // operands read ahead of their product
 
 // One workgroup's part of the work.  Heads run fastest: with 8 key heads each
 // XCD keeps to one of them.
@@ -239,10 +239,15 @@ __device__ __forceinline__ void store(const AttnArgs &a, const Item &it, const R
 // Many rows to a list: RW waves of 32 rows share each staged tile of KT keys;
 // KW groups of them take the tiles in turn.  Two stages: the next tile loads
 // while this one is multiplied.  32k tokens, 32 heads over 8, 2048 keys a
-// query: 1.10 ms, 0.95 PFLOP/s, 78% of the rate of a large matrix product; the
-// matrix cores are busy for 45% of it (LDS for 24%, waits 28% of the waves' time).
+// query: 1.09 ms, 0.96 PFLOP/s, 79% of the rate of a large matrix product.
+// Scores, softmax and the product with V follow one another in a wave, and ask
+// for LDS, vector units and matrix cores for about half of the time each, so
+// what counts is how many waves a SIMD holds: three (four waves of 32 rows a
+// workgroup, 32 keys a tile, 168 registers) are 4% faster than two (eight
+// waves, 64 keys, operands four ahead).  Two groups of waves half a tile apart
+// (1.18 ms) or exponentials laid between products (1.15 ms) gain nothing.
 template <class T, int D, int RW, int KW, int KT>
-__global__ __launch_bounds__(64 * RW * KW, 2) void attn_forward(const AttnArgs a) {
+__global__ __launch_bounds__(64 * RW * KW, RW == 4 ? 3 : 2) void attn_forward(const AttnArgs a) {
   using L = Tile<D>;
   constexpr int kHalf = KT * L::kRowBytes;  // K or V of a stage
   constexpr int kLoads = kHalf / 1024 / RW;  // direct loads of K, and of V, of a wave
@@ -557,7 +562,7 @@ hipError_t run_tile(const AttnArgs &a, hipStream_t s) {
   if (grid_of(a) == 0) return hipSuccess;
   if (grid_of(a) > 0x7fffffff) return hipErrorInvalidValue;
   hipError_t e;
-  switch (attn_tile(a.rows).row_waves) {
+  switch (attn_tile(a.rows, a.nqb).row_waves) {
     // a wave a list where there are enough lists to fill the chip (8 waves a
     // CU) twice over
     case 1:
@@ -569,7 +574,7 @@ hipError_t run_tile(const AttnArgs &a, hipStream_t s) {
       }
       break;
     case 2: e = run<T, D, 2, 2, 32>(a, s); break;
-    case 4: e = run<T, D, 4, 1, 64>(a, s); break;
+    case 4: e = run<T, D, 4, 1, 32>(a, s); break;
     default: e = run<T, D, 8, 1, 64>(a, s); break;
   }
   if (e != hipSuccess || a.nsplit == 1) return e;
@@ -586,19 +591,18 @@ hipError_t run_tile(const AttnArgs &a, hipStream_t s) {
 }  // namespace
 }  // namespace attn
 
-AttnTile attn_tile(int32_t rows) {
-  // one tile for all rows of a query block where that can be: rows in several
-  // tiles stage the same keys again.  Past 256 rows the tile that pads least.
-  int32_t best = 8;
-  if (rows <= 256) {
-    while (best > 1 && 32 * (best / 2) >= rows) best /= 2;
-  } else if ((rows + 127) / 128 % 2 == 1) {
-    best = 4;
-  }
+AttnTile attn_tile(int32_t rows, int32_t nqb) {
+  // The smallest tile that holds all rows of a query block, up to 128, or 256
+  // where it is a sequence's only one: rows in several tiles stage the same keys
+  // again, which then come from memory and not from L2 (24 drafted tokens with 8
+  // heads to a key head, 16 sequences of up to 8k: 172 us, in two tiles 226 us).
+  int32_t best = nqb == 1 ? 8 : 4;
+  while (best > 1 && 32 * (best / 2) >= rows) best /= 2;
+  if (best == 8 && rows > 256 && (rows + 127) / 128 % 2 == 1) best = 4;  // which pads least
   AttnTile t;
   t.row_waves = best;
   t.key_waves = best == 1 ? 4 : (best == 2 ? 2 : 1);
-  t.key_tile = best <= 2 ? 32 : 64;
+  t.key_tile = best == 8 ? 64 : 32;
   t.rows = 32 * best;
   return t;
 }
