@@ -24,7 +24,6 @@ namespace attn {
 namespace {
 
 constexpr int kAhead = 4;               // operands read ahead of their product
-constexpr int kCus = 256;
 constexpr int kShort = 128;             // queries of a short sequence
 constexpr int kFew = 2;                 // blocks of a short list
 constexpr int kMaxChunk = 1024;         // query blocks of an item

@@ -247,12 +247,11 @@ __device__ __forceinline__ void store(const AttnArgs &a, const Item &it, const R
 // waves, 64 keys, operands four ahead).  Two groups of waves half a tile apart
 // (1.18 ms) or exponentials laid between products (1.15 ms) gain nothing.
 template <class T, int D, int RW, int KW, int KT>
-__global__ __launch_bounds__(64 * RW * KW, RW == 4 ? 3 : 2) void attn_forward(const AttnArgs a) {
+__global__ __launch_bounds__(64 * RW * KW, RW == 4 && KW == 1 ? 3 : 2) void attn_forward(const AttnArgs a) {
   using L = Tile<D>;
   constexpr int kHalf = KT * L::kRowBytes;  // K or V of a stage
   constexpr int kLoads = kHalf / 1024 / RW;  // direct loads of K, and of V, of a wave
   static_assert(kLoads >= 1 && kLoads * RW * 1024 == kHalf, "loads of a stage");
-  static_assert((KW - 1) * RW * (D / 2 + 2) * 256 <= KW * 4 * kHalf, "the groups' sums fit the stages");
   constexpr int kSubs = kAttnPage / KT;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
 
@@ -351,7 +350,7 @@ __global__ __launch_bounds__(64 * RW * KW, RW == 4 ? 3 : 2) void attn_forward(co
 // block that several of them name is read once, and rows whose list does not
 // name it have weights of zero there.  What each list alone would read and
 // multiply (its tile has 32 rows, used or not) is never less.  8k queries with
-// a list each, 16 heads to a key head: 471 us against 726 us.  A weight of
+// a list each, 16 heads to a key head: 485 us against 726 us.  A weight of
 // zero does not make an infinite or NaN value harmless, so where a row comes
 // out as neither finite the lists are gone through again one by one.
 template <class T, int D, int KW, bool PACK>
@@ -538,7 +537,9 @@ int64_t grid_of(const AttnArgs &a) {
 
 template <class T, int D, int RW, int KW, int KT>
 hipError_t run(const AttnArgs &a, hipStream_t s) {
-  constexpr size_t kLds = static_cast<size_t>(KW) * 4 * KT * D * 2;
+  constexpr size_t kTiles = static_cast<size_t>(KW) * 4 * KT * D * 2;
+  constexpr size_t kSums = static_cast<size_t>(KW - 1) * RW * (D / 2 + 2) * 256;
+  constexpr size_t kLds = kTiles > kSums ? kTiles : kSums;
   hipError_t e = allow_dynamic_lds(reinterpret_cast<const void *>(&attn_forward<T, D, RW, KW, KT>), kLds);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((attn_forward<T, D, RW, KW, KT>), dim3(static_cast<unsigned>(grid_of(a))), dim3(64 * RW * KW),
@@ -574,7 +575,9 @@ hipError_t run_tile(const AttnArgs &a, hipStream_t s) {
       }
       break;
     case 2: e = run<T, D, 2, 2, 32>(a, s); break;
-    case 4: e = run<T, D, 4, 1, 32>(a, s); break;
+    // up to a workgroup a CU, two groups of waves share its list (2048 tokens, 16
+    // heads over 8, 16 blocks a query: 25.6 us against 31.0)
+    case 4: e = grid_of(a) <= kCus ? run<T, D, 4, 2, 32>(a, s) : run<T, D, 4, 1, 32>(a, s); break;
     default: e = run<T, D, 8, 1, 64>(a, s); break;
   }
   if (e != hipSuccess || a.nsplit == 1) return e;

@@ -791,3 +791,29 @@ def test_dk_dv_of_short_sequences_are_off_by_their_own_rounding(S, nq, q_block, 
         want = per_key(f * (w.transpose(-1, -2) @ x))
         off = per_key(f * ((e + rows * e32 * w.abs()).transpose(-1, -2) @ x.abs()))
         R.check(name, got, want, (u + 4 * e32) * (want.abs() + off) + off + tiny)
+
+
+MANY = [  # more tiles of 128 rows than CUs: a workgroup has no second group of waves for them
+    case(nq=521, hq=40, hk=8, q_block=16, blocks=5), case(b=4, nq=300, hq=28, hk=14, d=128, dtype=torch.float16),
+    case(b=4, nq=570, nk=600, hq=16, hk=2, blocks=3, dtype=torch.float16), case(b=2, nq=545, hq=24, hk=8, d=128, q_block=32),
+]
+
+
+@pytest.mark.parametrize("kind", ["full", "ragged", "odd"])
+@pytest.mark.parametrize("n", range(len(MANY)))
+def test_many_tiles_of_many_rows(S, n, kind):
+    c = MANY[n]
+    rows = c["q_block"] * (c["hq"] // c["hk"])
+    assert rows > 64 and c["b"] * c["hk"] * -(-c["nq"] // c["q_block"]) * -(-rows // 128) > 256
+    q, k, v, grad, g = inputs(c, 1100 + n)
+    lens, starts = lengths(c, g, kind)
+    lists = random_lists(c, g, empty=0.2)
+    P = plan(S, c, backward=True)
+    o, lse = run_forward(S, c, q.cuda(), k.cuda(), v.cuda(), lists.cuda(), lens.cuda(), starts.cuda(), P)
+    dq, dk, dv = (torch.full_like(t, float("nan")).cuda() for t in (q, k, v))
+    S.spmm_execute_attn_backward(P, grad.cuda(), q.cuda(), k.cuda(), v.cuda(), lists.cuda(), o, lse, dq, dk, dv,
+                                 lens=lens.cuda(), starts=starts.cuda())
+    w = R.sees(c, lists, lens, starts, None)
+    want = R.attention(c, q.double(), k.double(), v.double(), w, grad.double())
+    for name, got in (("o", o), ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv)):
+        R.check(name, got, *want[name])
