@@ -952,10 +952,15 @@ hipError_t run_backward(const AttnArgs &a, hipStream_t s) {
     case 2: e = run_dq<T, D, 2, 2, 32>(a, s); break;
     // two workgroups of four waves a CU rather than one of eight: one reads
     // its rows while the other multiplies (16k tokens: 605 us against 680)
+    // Tiles of 64 rows whose keys two groups of waves share where that leaves at
+    // most one workgroup a CU (1254 tokens, 8 heads over 2 of 64: 56 us the step
+    // against 63; two a CU, 2048 tokens, 16 heads over 8: 140.5 against 139.6).
     default: {
       AttnArgs x = a;
-      x.rtiles = (a.rows + 127) / 128;
-      e = run_dq<T, D, 4, 1, 64>(x, s);
+      x.rtiles = (a.rows + 63) / 64;
+      const bool small = static_cast<int64_t>(a.b) * a.hk * a.nqb * x.rtiles <= kCus;
+      if (!small) x.rtiles = (a.rows + 127) / 128;
+      e = small ? run_dq<T, D, 2, 2, 32>(x, s) : run_dq<T, D, 4, 1, 64>(x, s);
       break;
     }
   }
@@ -972,10 +977,11 @@ hipError_t run_backward(const AttnArgs &a, hipStream_t s) {
 }  // namespace attn
 
 void attn_chunks(int64_t heads, int64_t entries, int32_t nqb, int32_t rows, int32_t nkb, int32_t *chunk, int32_t *slots) {
-  // about 512 items more than one a key block: two a CU, taken from queues
-  // (16k tokens: 1502 us the step, with four times as many 1567), but at least
+  // about 256 items more than one a key block: one a CU, taken from queues (a
+  // step of 2048 tokens, 16 heads over 8: 117 us, with 512 140 us, with 128 135
+  // us; of 16k tokens, 32 heads over 8: 1.53, 1.53 and 1.99 ms), but at least
   // 512 rows an item: its partial sums cost as much traffic as 128 rows' q and do
-  const int64_t most = heads * entries / 512 + 1, least = (511 + rows) / rows;
+  const int64_t most = heads * entries / 256 + 1, least = (511 + rows) / rows;
   // (and at most 2^28, so that the kernel counts them in 32 bits)
   const int64_t cap = std::max<int64_t>(1, std::min<int64_t>(attn::kMaxChunk, (int64_t(1) << 28) / rows));
   int64_t c = std::min(cap, std::max(most, least));
