@@ -144,16 +144,18 @@ __device__ __forceinline__ i32x4 buffer(const char *base, int32_t bytes) {
 
 // Direct load of 16 bytes per lane: LDS[lds + 16 * lane] = buffer[voff].
 // Inline asm, so the compiler neither waits on it (the kernels count vmcnt
-// themselves) nor assumes later LDS reads depend on it.
+// themselves) nor assumes later LDS reads depend on it.  The load must come one
+// wait state after the write of M0 that gives its LDS address, which the
+// compiler does not see to inside asm.
 __device__ __forceinline__ void load_lds16(uint32_t lds, i32x4 buf, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :
                : "s"(lds), "v"(voff), "s"(buf)
                : "memory", "m0");
 }
 // The same from an address of the lane's own.
 __device__ __forceinline__ void load_lds16(uint32_t lds, const char *p) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                :
                : "s"(lds), "v"(p)
                : "memory", "m0");
@@ -161,7 +163,7 @@ __device__ __forceinline__ void load_lds16(uint32_t lds, const char *p) {
 
 // 4 bytes a lane: LDS[lds + 4 * lane] = *p.
 __device__ __forceinline__ void load_lds4(uint32_t lds, const float *p) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
                :
                : "s"(lds), "v"(p)
                : "memory", "m0");

@@ -99,9 +99,11 @@ __device__ __forceinline__ void wait_vm() {
 
 // Direct global->LDS load of 16 bytes per lane: LDS[lds + 16 * lane] =
 // global[base + voff].  Inline asm, so the compiler neither waits on it (the
-// kernel counts vmcnt itself) nor assumes later LDS reads depend on it.
+// kernel counts vmcnt itself) nor assumes later LDS reads depend on it.  The
+// load must come one wait state after the write of M0 that gives its LDS
+// address, which the compiler does not see to inside asm.
 __device__ __forceinline__ void load_lds16(uint32_t lds, const void *base, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                :
                : "s"(lds), "v"(voff), "s"(base)
                : "memory", "m0");
