@@ -132,14 +132,16 @@ __device__ __forceinline__ uint32_t lds_addr(const void *p) {
 }
 
 // A buffer of `bytes` bytes from base: direct loads past its end write zeros.
+// A load must come five wait states after a vector instruction that wrote one
+// of its scalar registers, as the reads of a first lane do.  The compiler does
+// not see to that in front of asm.
 __device__ __forceinline__ i32x4 buffer(const char *base, int32_t bytes) {
   const uint64_t a = reinterpret_cast<uint64_t>(base);
-  i32x4 r;
-  r[0] = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<uint32_t>(a)));
-  r[1] = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<uint32_t>(a >> 32) & 0xffffu));
-  r[2] = __builtin_amdgcn_readfirstlane(bytes);
-  r[3] = 0x00020000;
-  return r;
+  const int lo = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<uint32_t>(a)));
+  const int hi = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<uint32_t>(a >> 32) & 0xffffu));
+  int size = __builtin_amdgcn_readfirstlane(bytes);
+  asm("s_nop 4" : "+s"(size) : "s"(lo), "s"(hi));
+  return i32x4{lo, hi, size, 0x00020000};
 }
 
 // Direct load of 16 bytes per lane: LDS[lds + 16 * lane] = buffer[voff].

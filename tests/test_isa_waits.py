@@ -5,7 +5,8 @@ The compiler inserts the wait states that the hardware asks for between its
 own instructions, but not inside an inline asm string, and not in front of one
 for the registers it reads.  The direct loads to LDS are such strings.  They
 need one wait state between a write of M0 and the load that takes its LDS
-address from there."""
+address from there, and five between a vector instruction that writes a scalar
+register (v_readfirstlane and the like) and the load that reads it."""
 import collections
 import os
 import re
@@ -99,6 +100,15 @@ def m0_faults(insns):
     return [i for i, x in enumerate(insns) if is_lds_load(x) and too_close(insns, i, {"m0"}, lambda w: True, 1)]
 
 
+def is_memory(insn):
+    return insn.op.startswith(("global_", "buffer_", "flat_", "scratch_"))
+
+
+def scalar_faults(insns):
+    return [i for i, x in enumerate(insns)
+            if is_memory(x) and too_close(insns, i, scalars(x.args), lambda w: w.op.startswith("v_"), 5)]
+
+
 @pytest.fixture(scope="module")
 def kernels(tmp_path_factory):
     """[(name, instructions)] of every device function of the library."""
@@ -130,6 +140,28 @@ def test_the_check_itself():
     assert m0_faults(functions(LISTING % "")["k"]) == [1]
     good = functions(LISTING % nop)["k"]
     assert m0_faults(good) == [] and good[3].target == 2
+
+
+READ = """
+0000000000001000 <k>:
+\tv_readfirstlane_b32 s30, v7                                // 000000001000: 7E3C0507
+%s\tv_lshl_add_u32 v2, v3, 4, v2                               // 000000001010: D1FD0002 04090903
+\ts_mov_b32 m0, s4                                           // 000000001018: BEFC0004
+\tbuffer_load_dwordx4 v2, s[28:31], 0 offen lds              // 00000000101C: E05D1000 80070002
+\ts_endpgm                                                   // 000000001024: BF810000
+"""
+
+
+def test_the_check_of_scalar_operands():
+    for between, faults in (("", [3]), ("\ts_nop 1    // 000000001004: BF800001\n", [4]),
+                            ("\ts_nop 2    // 000000001004: BF800002\n", []),
+                            ("\ts_mov_b32 s30, 0    // 000000001004: BE9E0080\n", [])):
+        assert scalar_faults(functions(READ % between)["k"]) == faults, between
+
+
+def test_loads_wait_for_scalars_from_vector_instructions(kernels):
+    bad = {name: len(f) for name, insns in kernels if (f := scalar_faults(insns))}
+    assert not bad, bad
 
 
 def test_lds_loads_wait_for_m0(kernels):
