@@ -409,7 +409,7 @@ typedef struct {
   int32_t dim;                   /* 64 or 128 (else UNSUPPORTED)                    */
   int32_t dtype;                 /* SPMM_BF16 or SPMM_F16 (else UNSUPPORTED)        */
   int32_t q_block;               /* queries of a list: 1, 2, 4, .. 64               */
-  int32_t max_blocks;            /* entries of a list                               */
+  int32_t max_blocks;            /* entries of a list, at most 2^30 (else UNSUPPORTED) */
   int32_t sink_blocks;           /* first blocks that spmm_execute_attn_select keeps */
   int32_t local_blocks;          /* last blocks it keeps, at least 1 (the queries' own) */
   int32_t backward;              /* 1: with workspace for spmm_execute_attn_backward */

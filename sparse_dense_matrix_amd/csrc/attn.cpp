@@ -13,6 +13,7 @@ namespace sdm {
 namespace {
 
 constexpr int64_t kElem = 2;                      // bytes of bf16 and f16
+constexpr int32_t kMaxEntries = 1 << 30;          // of a list
 constexpr int64_t kMaxRowOffset = 0xffffff00ll;   // a sequence's last query byte in the backward kernels
 
 spmm_status_t bad(const char *fn, const std::string &what) {
@@ -153,6 +154,8 @@ spmm_status_t attn_shape(const spmm_attn_desc_t &d, spmm_plan_s *p) {
   if (d.dim != 64 && d.dim != 128) return fail(SPMM_ERR_UNSUPPORTED, "spmm_plan_attn: dim must be 64 or 128");
   if (!power_of_two(d.q_block) || d.q_block > 64)
     return fail(SPMM_ERR_UNSUPPORTED, "spmm_plan_attn: q_block must be 1, 2, 4, .. 64");
+  // the kernels step through lists by up to 256 entries in 32 bits
+  if (d.max_blocks > kMaxEntries) return fail(SPMM_ERR_UNSUPPORTED, "spmm_plan_attn: max_blocks above 2^30");
   if (d.heads_q > 65536) return fail(SPMM_ERR_UNSUPPORTED, "spmm_plan_attn: more than 65536 query heads");
 
   p->attn = true;

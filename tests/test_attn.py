@@ -151,3 +151,16 @@ def test_reference_gradients_against_differences():
             want_slope = (want[name][0] * to).sum().item()
             size = (want[name][0].norm() * to.norm()).item()
             assert abs(slope - want_slope) <= 1e-7 * size, (name, slope, want_slope)
+
+
+@pytest.mark.parametrize("blocks", [2 ** 30 + 1, 2 ** 31 - 1])
+def test_plan_refuses_lists_that_kernels_cannot_count(S, blocks):
+    """The kernels step through a list 64 or 256 entries at a time in 32 bits:
+    from 2^31 - 256 entries on a step would wrap and never end."""
+    with pytest.raises(S.SpmmError) as e:
+        S.spmm_plan_attn(1, 64, 64, 4, 2, 64, max_blocks=blocks)
+    assert e.value.name == "SPMM_ERR_UNSUPPORTED" and "max_blocks" in e.value.message
+
+
+def test_plan_takes_long_lists(ask):
+    assert ask(f"plan 1 64 640 4 2 64 64 {2 ** 30} 0")[0].split()[0] == "SPMM_OK"
