@@ -404,7 +404,8 @@ spmm_status_t spmm_execute_sddmm(spmm_plan_t p, const void *x_dev, int64_t ldx, 
  * not synchronise and can be captured into a graph.  A plan's workspace
  * allows one execute in flight at a time. */
 typedef struct {
-  int64_t batch, queries, keys;  /* sequences; queries and (at most) keys of each   */
+  int64_t batch, queries, keys;  /* sequences; queries and (at most) keys of each,
+                                    together at most 2^31 - 513 (else UNSUPPORTED) */
   int32_t heads_q, heads_kv;     /* heads_q a multiple of heads_kv                  */
   int32_t dim;                   /* 64 or 128 (else UNSUPPORTED)                    */
   int32_t dtype;                 /* SPMM_BF16 or SPMM_F16 (else UNSUPPORTED)        */

@@ -154,6 +154,9 @@ spmm_status_t attn_shape(const spmm_attn_desc_t &d, spmm_plan_s *p) {
   if (d.dim != 64 && d.dim != 128) return fail(SPMM_ERR_UNSUPPORTED, "spmm_plan_attn: dim must be 64 or 128");
   if (!power_of_two(d.q_block) || d.q_block > 64)
     return fail(SPMM_ERR_UNSUPPORTED, "spmm_plan_attn: q_block must be 1, 2, 4, .. 64");
+  // positions and the last key of a row tile are counted in 32 bits
+  if (d.queries + d.keys > INT32_MAX - 512)
+    return fail(SPMM_ERR_UNSUPPORTED, "spmm_plan_attn: queries + keys above 2^31 - 513");
   // the kernels step through lists by up to 256 entries in 32 bits
   if (d.max_blocks > kMaxEntries) return fail(SPMM_ERR_UNSUPPORTED, "spmm_plan_attn: max_blocks above 2^30");
   if (d.heads_q > 65536) return fail(SPMM_ERR_UNSUPPORTED, "spmm_plan_attn: more than 65536 query heads");

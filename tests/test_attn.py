@@ -164,3 +164,13 @@ def test_plan_refuses_lists_that_kernels_cannot_count(S, blocks):
 
 def test_plan_takes_long_lists(ask):
     assert ask(f"plan 1 64 640 4 2 64 64 {2 ** 30} 0")[0].split()[0] == "SPMM_OK"
+
+
+@pytest.mark.parametrize("queries,keys", [(64, 2 ** 31 - 257), (2 ** 30, 2 ** 30)])
+def test_plan_refuses_positions_past_32_bits(S, ask, queries, keys):
+    """starts + t reaches queries + keys, and a row tile 256 more: the last key
+    that a tile sees would wrap to a negative one, and its rows see nothing."""
+    with pytest.raises(S.SpmmError) as e:
+        S.spmm_plan_attn(1, queries, keys, 4, 2, 64)
+    assert e.value.name == "SPMM_ERR_UNSUPPORTED" and "queries + keys" in e.value.message
+    assert ask(f"plan 1 64 {2 ** 31 - 600} 4 2 64 64 16 0")[0].split()[0] == "SPMM_OK"
