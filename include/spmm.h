@@ -385,7 +385,8 @@ spmm_status_t spmm_execute_sddmm(spmm_plan_t p, const void *x_dev, int64_t ldx, 
  * Tensors of heads are [batch][tokens][heads][dim] (or [pages][64][heads][dim]
  * for a cache) with strides in elements, multiples of 8 and not negative, the
  * dim elements consecutive, 16-byte aligned.  Heads of an input may share
- * memory (stride_head = 0, a broadcast); a gradient is given per head.  Keys
+ * memory (stride_head = 0, a broadcast); a gradient is given per head.  Rows of
+ * a tensor that is written must not overlap (else INVALID_ARG).  Keys
  * past a sequence's length are never used, whatever stands there.
  * lens and starts are int32[batch] on the device; NULL means lens[i] = keys,
  * starts[i] = 0.  A length outside [0, keys] is taken as the nearer bound.

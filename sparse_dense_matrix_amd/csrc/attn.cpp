@@ -5,6 +5,7 @@
 #include <cstdio>
 #include <cstring>
 #include <new>
+#include <utility>
 
 #include "attn.h"
 #include "internal.h"
@@ -21,6 +22,33 @@ spmm_status_t bad(const char *fn, const std::string &what) {
 }
 
 bool power_of_two(int64_t x) { return x > 0 && (x & (x - 1)) == 0; }
+
+// Whether steps along the first k extents, each shorter than n[i] either way,
+// lead from r elements to less than dim away from 0, with a step somewhere
+// (`moved`: one was taken before).  Strides ascend, so that few steps of a
+// longer one are in reach of the shorter ones: one where the extents nest.
+// Strides that leave more than `tries` ways are taken to overlap.
+bool meets(const int64_t *n, const int64_t *s, int k, int64_t r, bool moved, int64_t dim, int *tries) {
+  if (k == 0) return moved && r > -dim && r < dim;
+  const int64_t last = n[k - 1] - 1, step = s[k - 1];
+  if (step == 0) return last > 0 || meets(n, s, k - 1, r, moved, dim, tries);
+  int64_t reach = dim - 1;
+  for (int i = 0; i < k - 1; ++i) reach += (n[i] - 1) * s[i];
+  const auto floor_div = [](int64_t x, int64_t d) { return x / d - (x % d < 0); };
+  const int64_t lo = std::max(-last, -floor_div(reach + r, step)), hi = std::min(last, floor_div(reach - r, step));
+  for (int64_t d = lo; d <= hi; ++d)
+    if (--*tries < 0 || meets(n, s, k - 1, r + d * step, moved || d != 0, dim, tries)) return true;
+  return false;
+}
+
+// Whether two rows of dim elements at i * sb + j * st + l * sh share memory.
+bool rows_overlap(int64_t outer, int64_t sb, int64_t tokens, int64_t st, int64_t heads, int64_t sh, int64_t dim) {
+  int64_t n[3] = {outer, tokens, heads}, s[3] = {outer > 1 ? sb : 0, tokens > 1 ? st : 0, heads > 1 ? sh : 0};
+  for (const auto &[i, j] : {std::pair{0, 1}, std::pair{1, 2}, std::pair{0, 1}})
+    if (s[i] > s[j]) std::swap(s[i], s[j]), std::swap(n[i], n[j]);
+  int tries = 1 << 16;
+  return meets(n, s, 3, 0, false, dim, &tries);
+}
 
 // A tensor [batch][tokens][heads][dim] as the kernels take it.  `outer` is the
 // number of sequences or pages.  Strides of an extent of one do not matter.
@@ -39,7 +67,7 @@ spmm_status_t view(const char *fn, const char *name, const spmm_attn_tensor_t *t
   if (sb > most / kElem / std::max<int64_t>(1, outer) || st > most / kElem / std::max<int64_t>(1, tokens) ||
       sh > most / kElem / std::max<int64_t>(1, heads))
     return bad(fn, std::string(name) + ": strides too large");
-  if (written && ((outer > 1 && sb < dim) || st < dim || (heads > 1 && sh < dim)))
+  if (written && rows_overlap(outer, sb, tokens, st, heads, sh, dim))
     return bad(fn, std::string(name) + " is written: its rows must not overlap");
   // the kernels bound a block's rows by their byte offset from its first one
   if (keys && (st < dim || st * kElem * kAttnPage >= (int64_t(1) << 31)))

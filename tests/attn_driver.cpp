@@ -7,6 +7,7 @@
 //   page <id pages p0 ..> -> page of block id of a table
 //   names <id last_key>   -> 0 or 1
 //   refuse <case>         -> "<status> <message>"
+//   written <b nq hq sb st sh>  -> message for an output of these extents and strides (lse is missing too)
 #include <cstdio>
 #include <cstring>
 #include <string>
@@ -146,6 +147,19 @@ int main() {
       if (std::scanf("%63s", what) != 1) return 2;
       const spmm_status_t s = refuse(what);
       std::printf("%s %s\n", spmm_status_str(s), s == SPMM_OK ? "" : spmm_last_error());
+    } else if (!std::strcmp(what, "written")) {
+      long long b, nq, sb, st, sh;
+      spmm_attn_desc_t d = shape(1, 1, 128);
+      if (std::scanf("%lld %lld %d %lld %lld %lld", &b, &nq, &d.heads_q, &sb, &st, &sh) != 6) return 2;
+      d.batch = b;
+      d.queries = nq;
+      d.heads_kv = 1;
+      spmm_plan_s p;
+      if (sdm::attn_shape(d, &p) != SPMM_OK) return 2;
+      const spmm_attn_tensor_t q = heads(nq, d.heads_q), k = heads(128, 1), o = {memory, sb, st, sh};
+      const spmm_status_t s = spmm_execute_attn(&p, &q, &k, &k, reinterpret_cast<int32_t *>(memory), &o, nullptr,
+                                                nullptr, nullptr, nullptr);
+      std::printf("%s\n", s == SPMM_OK ? "" : spmm_last_error());
     } else {
       return 2;
     }

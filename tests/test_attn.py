@@ -174,3 +174,27 @@ def test_plan_refuses_positions_past_32_bits(S, ask, queries, keys):
         S.spmm_plan_attn(1, queries, keys, 4, 2, 64)
     assert e.value.name == "SPMM_ERR_UNSUPPORTED" and "queries + keys" in e.value.message
     assert ask(f"plan 1 64 {2 ** 31 - 600} 4 2 64 64 16 0")[0].split()[0] == "SPMM_OK"
+
+
+def test_written_tensors_must_not_overlap(ask):
+    """Every small layout: refused where two rows share an element, and only there."""
+    r = np.random.default_rng(3)
+    lines, want = [], []
+    layouts = [(1, 4, 4, 0, 64, 64), (2, 3, 4, 256, 64, 128), (1, 2, 3, 0, 192, 128), (3, 2, 2, 64, 192, 384),
+               (2, 5, 1, 64, 128, 64), (4, 1, 1, 0, 64, 64), (1, 1, 1, 0, 0, 0), (2, 3, 4, 64, 512, 128)]
+    layouts += [(*r.integers(1, 5, 3).tolist(), *(8 * r.integers(0, 80, 3)).tolist()) for _ in range(600)]
+    layouts += [(*r.integers(1, 5, 3).tolist(), *(64 * r.integers(0, 20, 3)).tolist()) for _ in range(600)]
+    for b, nq, hq, sb, st, sh in layouts:
+        starts = np.sort((np.arange(b)[:, None, None] * sb + np.arange(nq)[:, None] * st + np.arange(hq) * sh).ravel())
+        want.append("o is written" if (np.diff(starts) < 64).any() else "lse is NULL")
+        lines.append(f"written {b} {nq} {hq} {sb} {st} {sh}")
+    # large ones: nested in any order, interleaved, and heads on top of tokens
+    for line, text in (("1000 100000 64 409600000 4096 64", "lse"), ("1000 100000 64 4096 4096000 64", "lse"),
+                       ("64 4096 32 64 131072 4096", "lse"), ("1 100000 64 0 64 64", "o is written"),
+                       ("2 100000 64 409599936 4096 64", "o is written")):
+        lines.append("written " + line)
+        want.append(text)
+    got = ask(*lines)
+    assert len(got) == len(want)
+    bad = [(x, y, z) for x, y, z in zip(lines, want, got) if y not in z]
+    assert not bad, bad[:5]
