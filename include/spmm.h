@@ -387,7 +387,9 @@ spmm_status_t spmm_execute_sddmm(spmm_plan_t p, const void *x_dev, int64_t ldx, 
  * dim elements consecutive, 16-byte aligned.  Heads of an input may share
  * memory (stride_head = 0, a broadcast); a gradient is given per head.  Rows of
  * a tensor that is written must not overlap (else INVALID_ARG).  Keys
- * past a sequence's length are never used, whatever stands there.
+ * past a sequence's length are never used, whatever stands there.  Else a NaN
+ * or an infinity spreads by whole blocks: from a key to the queries whose list
+ * names its block, from a query to the keys of the blocks that it sees keys of.
  * lens and starts are int32[batch] on the device; NULL means lens[i] = keys,
  * starts[i] = 0.  A length outside [0, keys] is taken as the nearer bound.
  *

@@ -658,7 +658,8 @@ __device__ __forceinline__ void dkv_item(const AttnArgs &a, char *lds, int64_t a
   const uint32_t per_token = 0xffffffffu / static_cast<uint32_t>(a.group);
   // Threads below kRows look after a row each, two rounds ahead: its offsets
   // for the direct loads, its limit, and its statistics on their way to LDS.
-  // Rows that are not there read zeros and see no key.
+  // Rows that are not there, or stand before the key block, read zeros and see
+  // no key: a weight of zero does not make a NaN in q or grad harmless.
   auto find = [&](int round) {
     const uint32_t flat = static_cast<uint32_t>(round) * kRows + tid;
     Stats &s = stats[round & 3];
@@ -671,7 +672,7 @@ __device__ __forceinline__ void dkv_item(const AttnArgs &a, char *lds, int64_t a
       const int tok = ids[e] * a.q_block + static_cast<int>(t);
       const int head = h * a.group + static_cast<int>(row - t * a.group);
       const int32_t pos = start + tok;
-      if (tok < a.nq && pos >= 0 && pos < len) {
+      if (tok < a.nq && pos >= kb * kAttnPage && pos < len) {
         rid = (static_cast<int64_t>(b) * a.hq + head) * a.nq + tok;
         lim = pos;
         qo = static_cast<uint32_t>(tok * a.q.st + head * a.q.sh);

@@ -817,3 +817,55 @@ def test_many_tiles_of_many_rows(S, n, kind):
     want = R.attention(c, q.double(), k.double(), v.double(), w, grad.double())
     for name, got in (("o", o), ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv)):
         R.check(name, got, *want[name])
+
+
+# ---- queries that see nothing of a block -----------------------------------
+
+QUIET = [
+    case(nq=64, nk=192, hq=4, hk=2, d=128, q_block=64, blocks=1), case(nq=48, nk=128, hq=3, hk=3, q_block=16, blocks=2),
+    case(nq=150, nk=256, hq=8, hk=1, d=64, q_block=4, blocks=1, dtype=torch.float16),
+]
+
+
+@pytest.mark.parametrize("n", range(len(QUIET)))
+def test_queries_without_keys_take_no_part(S, n):
+    """Lists that name the second block only: the queries before it see no key,
+    and what stands in their q and grad reaches no gradient."""
+    c = QUIET[n]
+    q, k, v, grad, g = inputs(c, 1200 + n)
+    starts, lens = torch.tensor([37], dtype=torch.int32), torch.tensor([c["nk"] - 3], dtype=torch.int32)
+    lists = torch.full((1, c["hk"], -(-c["nq"] // c["q_block"]), c["blocks"]), -1, dtype=torch.int32)
+    lists[..., 0] = 1
+    quiet = PAGE - 37
+    q[0, :quiet:2], q[0, 1:quiet:2] = float("nan"), float("inf")
+    grad[0, :quiet:2], grad[0, 1:quiet:2] = float("inf"), float("nan")
+    P = plan(S, c, backward=True)
+    o, lse = run_forward(S, c, q.cuda(), k.cuda(), v.cuda(), lists.cuda(), lens.cuda(), starts.cuda(), P)
+    dq, dk, dv = (torch.full_like(t, float("nan")).cuda() for t in (q, k, v))
+    S.spmm_execute_attn_backward(P, grad.cuda(), q.cuda(), k.cuda(), v.cuda(), lists.cuda(), o, lse, dq, dk, dv,
+                                 lens=lens.cuda(), starts=starts.cuda())
+    want = R.attention(c, q.double(), k.double(), v.double(), R.sees(c, lists, lens, starts, None), grad.double())
+    for name, got in (("o", o), ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv)):
+        R.check(name, got, *want[name])
+    assert (o[:, :quiet] == 0).all() and (dq[:, :quiet] == 0).all() and (dk[:, PAGE:] != 0).any()
+
+
+def test_queries_before_a_block_do_not_reach_it(S):
+    """Queries that see the first block alone, in one list with later ones: no
+    number of theirs reaches the gradients of the second block."""
+    c = case(nq=64, nk=128, hq=4, hk=2, d=128, q_block=64, blocks=2)
+    q, k, v, grad, g = inputs(c, 1210)
+    starts = torch.tensor([40], dtype=torch.int32, device="cuda")
+    lists = torch.tensor([0, 1], dtype=torch.int32).expand(1, 2, 1, 2).contiguous().cuda()
+    outs = []
+    for bad in (False, True):
+        if bad:
+            q[0, 3], grad[0, 20] = float("nan"), float("inf")
+        P = plan(S, c, backward=True)
+        x = [t.cuda() for t in (q, k, v, grad)]
+        o, lse = run_forward(S, c, *x[:3], lists, None, starts, P)
+        dq, dk, dv = (torch.full_like(t, float("nan")) for t in x[:3])
+        S.spmm_execute_attn_backward(P, x[3], *x[:3], lists, o, lse, dq, dk, dv, starts=starts)
+        outs.append((dk[:, PAGE:], dv[:, PAGE:]))
+    for x, y in zip(*outs):
+        assert torch.isfinite(x).all() and torch.equal(x, y)
