@@ -402,7 +402,9 @@ spmm_status_t spmm_execute_sddmm(spmm_plan_t p, const void *x_dev, int64_t ldx, 
  *
  * Products run on bf16 or f16 operands with fp32 sums; softmax statistics are
  * fp32; weights and their gradients are rounded to the element type (nearest
- * even) for the products that take them.  Same inputs, same bits.
+ * even) for the products that take them; gradients of f16 weights at a power
+ * of two of each row and key, so that they may pass the type's range where dq
+ * and dk do not.  Same inputs, same bits.
  * Every execute only launches kernels on `stream`: it allocates nothing, does
  * not synchronise and can be captured into a graph.  A plan's workspace
  * allows one execute in flight at a time. */

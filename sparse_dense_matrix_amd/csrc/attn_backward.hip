@@ -13,7 +13,10 @@
 // order: no atomics, so the same inputs give the same bits.
 //
 // p and ds are rounded to the element type for their products, at most half a
-// step each; sums, statistics and delta stay in 32 bits.
+// step each; sums, statistics and delta stay in 32 bits.  ds may be far larger
+// than the gradients it adds up to (heads of 128, unit normal inputs: 4 times
+// dq), so in f16 a row's ds, or a key's, are rounded at a power of two that
+// keeps the largest of them below 2^15 (Fit).
 #include <algorithm>
 
 #include "attn_dev.h"
@@ -125,6 +128,44 @@ __device__ __forceinline__ void prepare(const AttnArgs &a, int64_t item, char *l
     *reinterpret_cast<f32x2 *>(a.stats + 2 * static_cast<int64_t>(a.b) * a.hq * a.nq) = f32x2{INFINITY, 0.0f};
   invert(a, item, lds);
 }
+
+// The power of two at which dS enters its product where the type's range is
+// narrow: it starts out high and falls, with the sums so far, when a value of
+// the lane's row (or key) would pass 2^15.  A row's sums leave its wave at 2^0
+// again.  A training step in f16 takes 2 to 7% longer for it (16k tokens, 32
+// heads over 8, 1024 keys a query: 1.66 ms against 1.60).
+template <class T, int D>
+struct Fit {
+  int x = 100;
+  __device__ __forceinline__ void scale(f32x16 &ds, f32x16 *sum) {
+    if constexpr (T::kNarrow) {
+      float top = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(ds[e]));
+      top = max_halves(top);
+      const int n = __builtin_amdgcn_frexp_expf(top);  // top is in [2^(n - 1), 2^n)
+      const bool past = top > 0.0f && n + x > 15;
+      if (__any(past)) {
+        const int to = past ? 13 - n : x;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) sum[i][e] = __builtin_ldexpf(sum[i][e], to - x);
+        x = to;
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) ds[e] = __builtin_ldexpf(ds[e], x);
+    }
+  }
+  __device__ __forceinline__ void back(f32x16 *sum) {
+    if constexpr (T::kNarrow) {
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sum[i][e] = __builtin_ldexpf(sum[i][e], -x);
+    }
+  }
+};
 
 // A lane's row of a wave of the dq kernels.
 template <class T, int D>
@@ -324,6 +365,7 @@ __global__ __launch_bounds__(64 * RW * KW, 2) void attn_dq(const AttnArgs a) {
   f32x16 dq[D / 32];
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) dq[i] = zero16();
+  Fit<T, D> fit;
   float sum = 0.0f;
   const float c = a.scale * kLog2e;
   const int32_t *list = a.lists + ((static_cast<int64_t>(b) * a.hk + h) * a.nqb + qb) * a.max_blocks;
@@ -375,6 +417,7 @@ __global__ __launch_bounds__(64 * RW * KW, 2) void attn_dq(const AttnArgs a) {
           constexpr int kI = D / 32;
           auto ks = operands<2 * kI, kAhead>([&](int i) { return L::operand_t(kt, 32 * n + 16 * (i / kI), i % kI, lane); });
           row.ds(s, dp, key0 + 32 * n, c, lane, sum);
+          fit.scale(s, dq);
           ks.begin();
           add_dq<T, D>(s, ks, dq);
         }
@@ -384,10 +427,12 @@ __global__ __launch_bounds__(64 * RW * KW, 2) void attn_dq(const AttnArgs a) {
     if (walk == 0) {
       if (named <= kFew) row.delta += sum_groups<RW, KW>(lds, wave, lane, add_halves(sum));
       sum = 0.0f;
+      fit = Fit<T, D>();
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) dq[i] = zero16();
     }
   }
+  fit.back(dq);
   sum = add_halves(sum);
   if constexpr (KW > 1) {
     join_dq<D, RW, KW>(lds, wave, lane, dq, sum);
@@ -444,6 +489,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_stream(const AttnArgs a) {
   f32x16 dq[kI];
 #pragma unroll
   for (int i = 0; i < kI; ++i) dq[i] = zero16();
+  Fit<T, D> fit;
   float sum = 0.0f;
   const float c = a.scale * kLog2e;
   const int64_t head0 = (static_cast<int64_t>(b) * a.hk + h) * (PACK ? a.list_nqb : a.nqb);
@@ -513,6 +559,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_stream(const AttnArgs a) {
           }
         }
         row.ds(s, dp, key0, c, lane, sum);
+        fit.scale(s, dq);
         ts.begin();
         add_dq<T, D>(s, ts, dq);
         wait_lds();
@@ -523,6 +570,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_stream(const AttnArgs a) {
     if (pass == -2) {
       if (named <= kFew) row.delta += sum_groups<1, OWN ? 1 : 4>(lds, wave, lane, add_halves(sum));
     } else {
+      fit.back(dq);
       sum = add_halves(sum);
       if constexpr (!OWN) {
         join_dq<D, 1, 4>(lds, wave, lane, dq, sum);
@@ -541,6 +589,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_stream(const AttnArgs a) {
       }
     }
     sum = 0.0f;
+    fit = Fit<T, D>();
 #pragma unroll
     for (int i = 0; i < kI; ++i) dq[i] = zero16();
   }
@@ -705,6 +754,7 @@ __device__ __forceinline__ void dkv_item(const AttnArgs &a, char *lds, int64_t a
     for (int i = 0; i < kLoads; ++i)
       load_lds16(__builtin_amdgcn_readfirstlane(st + kHalf + (wave * kLoads + i) * 1024), gbuf, go[i]);
   };
+  Fit<T, D> fit;
   f32x16 dk[D / 32], dv[D / 32];
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
@@ -772,6 +822,7 @@ __device__ __forceinline__ void dkv_item(const AttnArgs &a, char *lds, int64_t a
         dp[4 * g4 + i] = s[4 * g4 + i] * (dp[4 * g4 + i] - d4[i]);
       }
     }
+    fit.scale(dp, dk);
     u32x4 w[4], low[4];
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
@@ -785,6 +836,7 @@ __device__ __forceinline__ void dkv_item(const AttnArgs &a, char *lds, int64_t a
       if constexpr (FINE) to = T::mma(x, low[i / kI], to);
     });
   }
+  fit.back(dk);
   {
   const AttnArgs a = args_again();
   // the row groups' sums, each group adding a share of them in group order

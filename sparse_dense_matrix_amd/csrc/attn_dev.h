@@ -35,6 +35,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 struct Bf16 {
   using E = __bf16;
+  static constexpr bool kNarrow = false;  // reaches as far as 32 bits
   __device__ static f32x16 mma(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -42,6 +43,7 @@ struct Bf16 {
 };
 struct F16 {
   using E = _Float16;
+  static constexpr bool kNarrow = true;  // infinite from 65520 on
   __device__ static f32x16 mma(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
                                                   __builtin_bit_cast(f16x8, b), c, 0, 0, 0);

@@ -869,3 +869,36 @@ def test_queries_before_a_block_do_not_reach_it(S):
         outs.append((dk[:, PAGE:], dv[:, PAGE:]))
     for x, y in zip(*outs):
         assert torch.isfinite(x).all() and torch.equal(x, y)
+
+
+# ---- gradients of f16 whose dS pass its range ------------------------------
+
+WIDE = [  # a list of many rows, short and longer sequences; of few rows, four waves, a wave, several lists to a tile
+    case(nq=64, d=128, blocks=1), case(nq=200, hk=1, blocks=4), case(nq=300, hq=8, hk=8, q_block=1, blocks=5),
+    case(nq=2100, hq=2, hk=2, q_block=1, blocks=33), case(nq=1100, hq=8, hk=4, q_block=1, blocks=18, d=128),
+]
+
+
+@pytest.mark.parametrize("step", [1.0, 2.0 ** -18])
+@pytest.mark.parametrize("n", range(len(WIDE)))
+def test_gradients_of_f16_with_dS_past_its_range(S, n, step):
+    """Values that are large and keys and queries that are not: dS goes to many
+    times 65504 where every gradient fits; the same with gradients 2^18 smaller."""
+    c = dict(WIDE[n], dtype=torch.float16)
+    q, k, v, grad, g = inputs(c, 1300 + n)
+    q, k, v, grad = (q.float() / 8).half(), (k.float() / 8).half(), v * 64, (grad.float() * 1000 * step).half()
+    nqb, nkb = -(-c["nq"] // c["q_block"]), -(-c["nk"] // PAGE)
+    lists = torch.arange(nkb, dtype=torch.int32).expand(1, c["hk"], nqb, nkb).contiguous()
+    P = plan(S, c, backward=True)
+    o, lse = run_forward(S, c, q.cuda(), k.cuda(), v.cuda(), lists.cuda(), None, None, P)
+    dq, dk, dv = (torch.full_like(t, float("nan")).cuda() for t in (q, k, v))
+    S.spmm_execute_attn_backward(P, grad.cuda(), q.cuda(), k.cuda(), v.cuda(), lists.cuda(), o, lse, dq, dk, dv)
+    w = torch.ones(c["nq"], c["nk"]).tril().double().expand(1, c["hk"], -1, -1)
+    want = R.attention(c, q.double(), k.double(), v.double(), w, grad.double())
+    for x in ("dq", "dk", "dv"):
+        assert want[x][0].abs().max() < 65504
+    if step == 1.0:  # the second query's dS for its two keys, in one head: of opposite signs, p (1 - p) grad . (v0 - v1)
+        gt, vt = grad[0, 1].double(), v[0, :2].repeat_interleave(c["hq"] // c["hk"], 1).double()
+        assert ((gt * (vt[0] - vt[1])).sum(-1).abs().max() / 4) > 2 * 65504
+    for name, got in (("o", o), ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv)):
+        R.check(name, got, *want[name])
