@@ -28,6 +28,7 @@ namespace {
 
 constexpr int kAhead = 4;               // operands read ahead of their product
 constexpr int kShort = 128;             // queries of a short sequence
+constexpr int kFewRows = 1024;          // rows of a short inverse list: one query block of 64 with 16 heads to a key head
 constexpr int kFew = 2;                 // blocks of a short list
 constexpr int kMaxChunk = 1024;         // query blocks of an item
 constexpr uint32_t kDeadRow = 0xffffff00u;  // offset past every buffer: a direct load gives zeros
@@ -609,6 +610,32 @@ __device__ __forceinline__ AttnArgs args_again() {
   return __builtin_bit_cast(AttnArgs, x);
 }
 
+// An item of the dk, dv kernel: key block kb (-1: none) of key head h, and part
+// `part` of the `same` entries of its inverse list, which stand from `less` on.
+struct DkvItem {
+  int b, h, slot, kb, part, less, same;
+  int32_t len, start;
+
+  __device__ __forceinline__ DkvItem(const AttnArgs &a, int64_t item) {
+    const uint32_t at = static_cast<uint32_t>(item);  // below 2^31
+    h = at % a.hk;
+    slot = at / a.hk % a.slots;
+    b = at / a.hk / a.slots;
+    const int64_t bh = static_cast<int64_t>(b) * a.hk + h;
+    kb = a.items[2 * (bh * a.slots + slot)];
+    if (kb < 0) return;
+    part = a.items[2 * (bh * a.slots + slot) + 1];
+    less = a.inv_ptr[2 * (bh * a.nkb + kb)];
+    same = a.inv_ptr[2 * (bh * a.nkb + kb) + 1];
+    len = attn_len(a.lens, b, a.nk);
+    start = attn_start(a.starts, b, a.nq, a.nk);
+  }
+  // few queries in the sequence, or few rows that may read the block
+  __device__ __forceinline__ bool few(const AttnArgs &a) const {
+    return min(a.nq, len - start) - max(0, -start) <= kShort || static_cast<int64_t>(same) * a.rows <= kFewRows;
+  }
+};
+
 // dk and dv of one item: 64 keys, up to `chunk` query blocks of the inverse
 // list.  RG row groups of two waves; a wave owns 32 keys (K rows in registers
 // as B operands, V rows in LDS) and 32 of the 32 RG rows staged at a time, so
@@ -622,13 +649,16 @@ __device__ __forceinline__ AttnArgs args_again() {
 // queues 640 us, 0.83 PFLOP/s: the matrix cores are busy for 37% of it, and the
 // rows come from beyond L2 in half of all loads (each is read once for every
 // key block that its list names).
-// FINE is for sequences of up to kShort queries: P and dS enter their products
-// as two operands as dS does for dq.  With few rows to a key the rounding of a
-// single dS may be all of dk's error, up to twice that of rounding dk; past
-// 128 queries it is 1.4 times, and the second operands would cost a quarter more
-// products.
+// FINE is for key blocks that few rows read: P and dS enter their products as
+// two operands as dS does for dq, for a quarter more products.  With one operand
+// dk and dv are off by 1.3 to 1.4 times their own rounding, averaged over a
+// tensor, and single keys with few rows by up to 2.7 times; with two by their
+// own rounding alone.  It goes by the sequence's own queries and the block's own
+// list, so that a sequence's gradients are as exact next to a longer one.
 template <class T, int D, int RG, bool FINE>
-__device__ __forceinline__ void dkv_item(const AttnArgs &a, char *lds, int64_t at) {
+__device__ __forceinline__ void dkv_item(char *lds, int64_t at) {
+  const AttnArgs a = args_again();
+  const DkvItem it(a, at);
   using L = Tile<D>;
   constexpr int kRows = 32 * RG;
   constexpr int kHalf = kRows * L::kRowBytes;     // Q or dO of a stage
@@ -652,20 +682,12 @@ __device__ __forceinline__ void dkv_item(const AttnArgs &a, char *lds, int64_t a
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int kh = wave & 1, rg = wave >> 1;
   const int h2 = lane >> 5;
-  const int h = at % a.hk;
-  at /= a.hk;
-  const int slot = at % a.slots;
-  const int b = static_cast<int>(at / a.slots);
+  const int h = it.h, b = it.b, kb = it.kb, same = it.same;
+  const int32_t len = it.len, start = it.start;
   const int64_t bh = static_cast<int64_t>(b) * a.hk + h;
-  const int kb = a.items[2 * (bh * a.slots + slot)];
-  if (kb < 0) return;
-  const int part = a.items[2 * (bh * a.slots + slot) + 1];
-  const int less = a.inv_ptr[2 * (bh * a.nkb + kb)], same = a.inv_ptr[2 * (bh * a.nkb + kb) + 1];
-  const int count = min(a.chunk, same - part * a.chunk);
-  const int32_t len = attn_len(a.lens, b, a.nk);
-  const int32_t start = attn_start(a.starts, b, a.nq, a.nk);
+  const int count = min(a.chunk, same - it.part * a.chunk);
   {
-    const int32_t *from = a.inv_ids + bh * a.nqb * a.max_blocks + less + part * a.chunk;
+    const int32_t *from = a.inv_ids + bh * a.nqb * a.max_blocks + it.less + it.part * a.chunk;
     for (int i = tid; i < count; i += 128 * RG) ids[i] = from[i];
   }
   const int32_t key = kb * kAttnPage + 32 * kh + (lane & 31);
@@ -864,7 +886,7 @@ __device__ __forceinline__ void dkv_item(const AttnArgs &a, char *lds, int64_t a
         sum[e] = x;
       }
       if (same > a.chunk) {
-        float *out = a.part_kv + (bh * a.slots + slot) * 2 * kAttnPage * D + which * kAttnPage * D +
+        float *out = a.part_kv + (bh * a.slots + it.slot) * 2 * kAttnPage * D + which * kAttnPage * D +
                      (32 * kh + (lane & 31)) * D + 32 * i + 4 * h2;
 #pragma unroll
         for (int g4 = 0; g4 < 4; ++g4)
@@ -892,15 +914,24 @@ __device__ __forceinline__ void dkv_item(const AttnArgs &a, char *lds, int64_t a
 // it and the items differ in length.  Queue x holds every eighth item, so that
 // with 8 key heads XCD x keeps to one of them; a workgroup whose queue is empty
 // goes on to the next one that is not.
-template <class T, int D, int RG, bool FINE>
+template <class T, int D, int RG>
 __global__ __launch_bounds__(128 * RG) void attn_dkv(const AttnArgs) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   __shared__ int32_t taken[2];  // queue, or -1: nothing is left; place in it
   int64_t item = blockIdx.x;
   for (;;) {
+    int how = 0;
+    {
+      const AttnArgs a = args_again();
+      if (item < static_cast<int64_t>(a.b) * a.slots * a.hk) {
+        const DkvItem it(a, item);
+        how = it.kb < 0 ? 0 : (it.few(a) ? 1 : 2);
+      }
+    }
+    if (how == 1) dkv_item<T, D, RG, true>(lds, item);
+    if (how == 2) dkv_item<T, D, RG, false>(lds, item);
     const AttnArgs a = args_again();
     const int64_t items = static_cast<int64_t>(a.b) * a.slots * a.hk;
-    if (item < items) dkv_item<T, D, RG, FINE>(a, lds, item);
     if (items <= gridDim.x) return;
     __syncthreads();
     if (threadIdx.x < 64) {
@@ -975,16 +1006,16 @@ hipError_t run_dq_stream(const AttnArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <class T, int D, bool FINE>
+template <class T, int D>
 hipError_t run_dkv(const AttnArgs &a, hipStream_t s) {
   constexpr int kRG = 4;
   const size_t lds = 4 * 32 * kRG * D * 2 + kAttnPage * D * 2 + 2 * (2 * 32 * kRG * 4) + 4 * (3 * 32 * kRG * 4 + 16) +
                      static_cast<size_t>(a.chunk) * 4;
   const int64_t grid = static_cast<int64_t>(a.b) * a.hk * a.slots;
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
-  hipError_t e = allow_dynamic_lds(reinterpret_cast<const void *>(&attn_dkv<T, D, kRG, FINE>), lds + (kMaxChunk - a.chunk) * 4);
+  hipError_t e = allow_dynamic_lds(reinterpret_cast<const void *>(&attn_dkv<T, D, kRG>), lds + (kMaxChunk - a.chunk) * 4);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((attn_dkv<T, D, kRG, FINE>), dim3(static_cast<unsigned>(std::min<int64_t>(grid, kCus))), dim3(128 * kRG), lds, s, a);
+  hipLaunchKernelGGL((attn_dkv<T, D, kRG>), dim3(static_cast<unsigned>(std::min<int64_t>(grid, kCus))), dim3(128 * kRG), lds, s, a);
   return hipGetLastError();
 }
 
@@ -1018,7 +1049,7 @@ hipError_t run_backward(const AttnArgs &a, hipStream_t s) {
     }
   }
   if (e != hipSuccess || a.nkb == 0) return e;
-  e = a.nq <= kShort ? run_dkv<T, D, true>(a, s) : run_dkv<T, D, false>(a, s);
+  e = run_dkv<T, D>(a, s);
   if (e != hipSuccess || a.slots == a.nkb) return e;
   const int64_t merge = static_cast<int64_t>(a.b) * a.hk * a.nkb * (2 * kAttnPage * D / 4 / 256);
   if (merge > 0x7fffffff) return hipErrorInvalidValue;

@@ -902,3 +902,78 @@ def test_gradients_of_f16_with_dS_past_its_range(S, n, step):
         assert ((gt * (vt[0] - vt[1])).sum(-1).abs().max() / 4) > 2 * 65504
     for name, got in (("o", o), ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv)):
         R.check(name, got, *want[name])
+
+
+# ---- keys that few rows read, in long sequences ----------------------------
+
+def own_rounding(c, q, k, v, grad, w):
+    """dq, dk and dv with bounds that hold their own rounding and the errors of
+    32-bit sums alone: P, dS and delta are kept to two steps of their rounding."""
+    u, e32 = torch.finfo(c["dtype"]).eps / 2, 2.0 ** -24
+    tiny = torch.finfo(c["dtype"]).smallest_normal * u
+    d, n, group, scale = c["d"], c["nk"], c["hq"] // c["hk"], 1.0 / math.sqrt(c["d"])
+    q, k, v, grad = (t.double().permute(0, 2, 1, 3) for t in (q, k, v, grad))
+    k, v, w = (t.repeat_interleave(group, 1) for t in (k, v, w))
+    on = w > 0
+    k, v = (torch.where(on.any(-2)[..., None], t, 0.0) for t in (k, v))
+    q, grad = (torch.where(on.any(-1)[..., None], t, 0.0) for t in (q, grad))
+    s = (scale * (q @ k.transpose(-1, -2))).masked_fill(~on, -math.inf)
+    p = torch.where(on, torch.softmax(s, -1), 0.0)
+    dp = grad @ v.transpose(-1, -2)
+    delta = (p * dp).sum(-1, keepdim=True)
+    ds = p * (dp - delta)
+    # relative errors of a weight: its score's d + 2 terms, exponents, the rounded lse
+    ew = torch.where(on, 2 * (d + 2) * scale * (q.abs() @ k.abs().transpose(-1, -2)), 0.0).amax(-1, keepdim=True)
+    ew = (ew + 64 + 8 * torch.where(on, s, 0.0).abs().amax(-1, keepdim=True)) * e32
+    edp = (d + 2) * e32 * (grad.abs() @ v.abs().transpose(-1, -2))
+    edelta = (p * (edp + (ew + 2 * n * e32) * dp.abs())).sum(-1, keepdim=True)
+    eds = 1.02 * ((u * u + ew) * ds.abs() + p * (edp + edelta + 4 * e32 * (dp.abs() + delta.abs()))) + tiny * on
+    ep = 1.02 * (u * u + ew) * p + tiny * on
+
+    def per_key(x):
+        return x.reshape(c["b"], c["hk"], group, *x.shape[2:]).sum(2)
+
+    rows, out = group * c["nq"], {}
+    for name, want, off in (
+            ("dq", scale * (ds @ k), scale * ((eds + n * e32 * ds.abs()) @ k.abs())),
+            ("dk", per_key(scale * (ds.transpose(-1, -2) @ q)), per_key(scale * ((eds + rows * e32 * ds.abs()).transpose(-1, -2) @ q.abs()))),
+            ("dv", per_key(p.transpose(-1, -2) @ grad), per_key((ep + rows * e32 * p).transpose(-1, -2) @ grad.abs()))):
+        out[name] = (want.permute(0, 2, 1, 3), ((u + 4 * e32) * (want.abs() + off) + off + tiny).permute(0, 2, 1, 3))
+    return out
+
+
+def gradients(S, c, q, k, v, grad, lists, lens=None):
+    P = plan(S, c, backward=True)
+    x = [t.cuda() for t in (q, k, v, grad, lists)]
+    lens = dev(lens)
+    o, lse = run_forward(S, c, *x[:3], x[4], lens, None, P)
+    out = [torch.full_like(t, float("nan")) for t in x[:3]]
+    S.spmm_execute_attn_backward(P, x[3], *x[:3], x[4], o, lse, *out, lens=lens)
+    return dict(zip(("dq", "dk", "dv"), out), o=o, lse=lse)
+
+
+@pytest.mark.parametrize("hk,q_block,dtype", [(2, 64, torch.bfloat16), (1, 16, torch.bfloat16), (2, 1, torch.float16)])
+def test_short_sequences_next_to_a_long_one(S, hk, q_block, dtype):
+    """Sequences of 10 to 128 tokens in tensors of 500: dq, dk and dv are off by
+    their own rounding, as they are alone."""
+    c = case(b=6, nq=500, hq=2, hk=hk, d=128, q_block=q_block, blocks=2, dtype=dtype)
+    q, k, v, grad, g = inputs(c, 1400 + q_block)
+    lens = torch.tensor([10, 33, 64, 100, 115, 128], dtype=torch.int32)
+    lists = torch.tensor([0, 1], dtype=torch.int32).expand(6, hk, -(-500 // q_block), 2).contiguous()
+    got = gradients(S, c, q, k, v, grad, lists, lens)
+    want = own_rounding(c, q, k, v, grad, R.sees(c, lists, lens, [0] * 6, None))
+    for name in ("dq", "dk", "dv"):
+        R.check(name, got[name], *want[name])
+
+
+@pytest.mark.parametrize("nq,q_block,hq,hk,dtype", [(700, 64, 8, 8, torch.bfloat16), (700, 16, 4, 1, torch.float16), (1300, 64, 16, 1, torch.bfloat16)])
+def test_blocks_that_few_rows_read(S, nq, q_block, hq, hk, dtype):
+    """A long sequence whose lists name their own block: up to 1024 rows read it."""
+    c = case(nq=nq, hq=hq, hk=hk, d=128, q_block=q_block, blocks=1, dtype=dtype)
+    q, k, v, grad, g = inputs(c, 1410 + q_block)
+    nqb = -(-nq // q_block)
+    lists = (torch.arange(nqb, dtype=torch.int32) * q_block // PAGE).reshape(1, 1, nqb, 1).expand(1, hk, nqb, 1).contiguous()
+    got = gradients(S, c, q, k, v, grad, lists)
+    want = own_rounding(c, q, k, v, grad, R.sees(c, lists, [nq], [0], None))
+    for name in ("dq", "dk", "dv"):
+        R.check(name, got[name], *want[name])
