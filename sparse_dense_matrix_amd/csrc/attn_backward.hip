@@ -317,8 +317,8 @@ __device__ __forceinline__ float sum_groups(char *lds, int wave, int lane, float
   return sum;
 }
 
-// Both dq kernels walk a list twice where it is short, the first time for
-// delta (what it adds to dq is dropped: a branch around it costs registers).
+// Both dq kernels walk a list twice where it is short, whatever its neighbours
+// in a shared tile are, the first time for delta (what it adds to dq is dropped: a branch around it costs registers).
 // With few keys the error of do . o would be the larger part of dq's (14 keys
 // in bf16: dq off by 2.9e-3 of its norm, 1.7e-3 with it corrected; past two
 // blocks 2.1e-3, where another walk would cost half of the kernel's time).
@@ -501,10 +501,22 @@ __global__ __launch_bounds__(256, 2) void attn_dq_stream(const AttnArgs a) {
   constexpr int kStep = OWN ? 1 : 4;
   const int first = OWN ? 0 : wave;
 
-  // for delta if the list is short; all lists together; then if need be one by one
+  uint32_t brief = 0;  // the lists of up to kFew blocks
+  if constexpr (PACK) {
+    const int of = lane / a.max_blocks;  // the list that entry `lane` is of
+    const int32_t len = attn_len(a.lens, b, a.nk), start = attn_start(a.starts, b, a.nq, a.nk);
+    const int id = lane < entries ? list[lane] : -1;
+    const uint64_t named =
+        __ballot(attn_names(id, last_key_of(a, a.q_block / a.pack, qb * a.pack + of, len, start)));
+    for (int l = 0; l < lists; ++l)
+      if (__builtin_popcountll(named >> (l * a.max_blocks) & ((uint64_t(1) << a.max_blocks) - 1)) <= kFew)
+        brief |= 1u << l;
+  }
+
+  // for delta of short lists; all lists together; then if need be one by one
 #pragma unroll 1
   for (int pass = -2; pass < (PACK ? lists : 0); ++pass) {
-    const uint32_t take = pass < 0 ? ~0u : 1u << pass;
+    const uint32_t take = pass == -2 ? brief : (pass < 0 ? ~0u : 1u << pass);
     int named = 0;
     for (int32_t e = 0; e < entries; e += 64) {
       Shared blocks;
@@ -515,7 +527,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_stream(const AttnArgs a) {
         blocks = Shared{n.id, n.page, 1, n.n};
       }
       named += blocks.n;
-      if (pass == -2 && named > kFew) break;
+      if (!PACK && pass == -2 && named > kFew) break;
       const int tiles = blocks.n * kSubs;
       // past the last tile the loads are of no bytes, so that the waits below
       // always count the same loads
@@ -569,7 +581,8 @@ __global__ __launch_bounds__(256, 2) void attn_dq_stream(const AttnArgs a) {
       wait_vm<0>();  // the loads of no bytes
     }
     if (pass == -2) {
-      if (named <= kFew) row.delta += sum_groups<1, OWN ? 1 : 4>(lds, wave, lane, add_halves(sum));
+      if (!PACK && named <= kFew) row.delta += sum_groups<1, OWN ? 1 : 4>(lds, wave, lane, add_halves(sum));
+      if (PACK) row.delta += brief >> mine & 1 ? add_halves(sum) : 0.0f;
     } else {
       fit.back(dq);
       sum = add_halves(sum);

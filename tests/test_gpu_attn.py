@@ -977,3 +977,26 @@ def test_blocks_that_few_rows_read(S, nq, q_block, hq, hk, dtype):
     want = own_rounding(c, q, k, v, grad, R.sees(c, lists, [nq], [0], None))
     for name in ("dq", "dk", "dv"):
         R.check(name, got[name], *want[name])
+
+
+@pytest.mark.parametrize("hq,d,dtype", [(8, 64, torch.bfloat16), (16, 128, torch.float16)])
+def test_a_short_list_keeps_its_delta_next_to_long_ones(S, hq, d, dtype):
+    """Lists of one and two blocks that share a tile with lists of seven: their
+    dq is off by its own rounding."""
+    c = case(nq=1100, hq=hq, hk=8, d=d, q_block=1, blocks=8, dtype=dtype)
+    q, k, v, grad, g = inputs(c, 1430)
+    nkb, t = -(-c["nq"] // PAGE), torch.arange(c["nq"])
+    lists = torch.full((1, 8, c["nq"], 8), -1, dtype=torch.int32)
+    for j in range(7):
+        lists[..., j] = (t[None] * (j + 1) + 5 * torch.arange(8)[:, None]) % nkb
+    lists = lists.sort(-1).values
+    lists[:, :, ::2, :6] = -1  # a block, and the query's own
+    lists[:, :, ::2, 7] = (t[::2] // PAGE).int()
+    lists[:, :, ::4, 6] = nkb - 1 - lists[:, :, ::4, 6] % 4  # most see nothing of it
+    got = gradients(S, c, q, k, v, grad, lists)
+    w = R.sees(c, lists, [c["nq"]], [0], None)
+    want = own_rounding(c, q, k, v, grad, w.clamp(max=1.0))["dq"]
+    once = (w[0].amax(-1) <= 1).repeat_interleave(hq // 8, 0).T  # no block named twice
+    short = once & (t % 2 == 0)[:, None]
+    assert short.sum() > 300 * hq // 2
+    R.check("dq", got["dq"].cpu()[0][short], want[0][0][short], want[1][0][short])
