@@ -65,7 +65,7 @@ __device__ __forceinline__ Row row_of(const AttnArgs &a, const Item &it, int til
   r.live = r.real && r.pos >= 0 && r.pos < r.len;
   const int last_row = min(a.rows, (it.rt + 1) * tile_rows) - 1;
   const int last_tok = min(a.nq - 1, it.qb * a.q_block + last_row / a.group);
-  r.last_key = a.tree ? r.len - 1 : min(r.len - 1, r.start + last_tok);
+  r.last_key = min(r.len - 1, r.start + (a.tree ? 63 : last_tok));  // a tree's mask has 64 bits
   int32_t open = r.live ? (a.tree ? min(r.start, r.len) : r.pos + 1) : INT32_MAX;
 #pragma unroll
   for (int m = 1; m < 32; m *= 2) open = min(open, __shfl_xor(open, m));

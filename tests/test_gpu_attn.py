@@ -1000,3 +1000,22 @@ def test_a_short_list_keeps_its_delta_next_to_long_ones(S, hq, d, dtype):
     short = once & (t % 2 == 0)[:, None]
     assert short.sum() > 300 * hq // 2
     R.check("dq", got["dq"].cpu()[0][short], want[0][0][short], want[1][0][short])
+
+
+@pytest.mark.parametrize("nq,hq,listed", [(4, 4, False), (40, 8, True), (64, 16, False)])
+def test_tree_keys_past_every_bit_may_hold_anything(S, nq, hq, listed):
+    """A mask has 64 bits: keys 64 and more past the text are seen by no drafted token."""
+    c = case(b=2, nq=nq, nk=640, hq=hq, hk=2, d=128, blocks=10)
+    q, k, v, _, g = inputs(c, 1440 + nq)
+    starts, lens = torch.tensor([130, 400], dtype=torch.int32), torch.tensor([400, 640], dtype=torch.int32)
+    tree = torch.randint(-2 ** 63, 2 ** 63 - 1, (2, nq), generator=g)
+    for i in range(2):
+        at = int(starts[i]) + 64
+        k[i, at::2], k[i, at + 1::2] = float("nan"), float("inf")
+        v[i, at::2], v[i, at + 1::2] = float("inf"), float("nan")
+    kp, vp, table = paged(c, k, v, g)
+    lists = torch.arange(10, dtype=torch.int32).expand(2, 2, 1, 10).contiguous() if listed else None
+    o, lse = run_cache(S, c, q, kp, vp, table=table, lists=lists, lens=lens, starts=starts, tree=tree)
+    want = R.attention(c, q.double(), k.double(), v.double(), R.sees(c, lists, lens, starts, tree))
+    R.check("o", o, *want["o"])
+    R.check("lse", lse, *want["lse"])
