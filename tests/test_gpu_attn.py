@@ -1019,3 +1019,68 @@ def test_tree_keys_past_every_bit_may_hold_anything(S, nq, hq, listed):
     want = R.attention(c, q.double(), k.double(), v.double(), R.sees(c, lists, lens, starts, tree))
     R.check("o", o, *want["o"])
     R.check("lse", lse, *want["lse"])
+
+
+# ---- lists and sequences that are cut into ranges --------------------------
+
+def ranges(P, c, listed):
+    """Ranges of a list, or of a whole sequence (then the larger of the two)."""
+    if listed:
+        rows = min(c["q_block"], c["nq"]) * (c["hq"] // c["hk"])
+        tiles = -(-rows // P.info()["tile_m"])
+        return P.info()["grid"] // (c["b"] * c["hk"] * tiles)
+    return P.info()["workspace_bytes"] // (c["b"] * c["hq"] * c["nq"] * (c["d"] * 4 + 8))
+
+
+TREES = [  # row tiles of 32, 64, 128, 256 rows, several of 128 and of 256
+    case(b=3, nq=4, nk=6000, hq=8, hk=2, d=128, blocks=2), case(b=2, nq=12, nk=5000, hq=4, hk=1, blocks=2),
+    case(b=3, nq=24, nk=4500, hq=8, hk=2, d=128, blocks=2), case(b=2, nq=24, nk=5000, hq=8, hk=1, blocks=2, dtype=torch.float16),
+    case(b=1, nq=24, nk=7000, hq=16, hk=1, d=128, blocks=2), case(b=2, nq=64, nk=4200, hq=16, hk=1, d=128, blocks=2),
+]
+
+
+@pytest.mark.parametrize("listed", [False, True])
+@pytest.mark.parametrize("n", range(len(TREES)))
+def test_cache_tree_in_ranges(S, n, listed):
+    c = dict(TREES[n], blocks=48) if listed else TREES[n]
+    assert ranges(plan(S, c), c, listed) > 1, "the case must be cut"
+    q, k, v, _, g = inputs(c, 1500 + n)
+    lens = torch.tensor([c["nk"], c["nk"] // 3 + 5, c["nq"] - 1][:c["b"]], dtype=torch.int32)
+    starts = lens - c["nq"]
+    tree = torch.randint(-2 ** 63, 2 ** 63 - 1, (c["b"], c["nq"]), generator=g)
+    kp, vp, table = paged(c, k, v, g)
+    lists = random_lists(c, g) if listed else None
+    if listed:  # with the drafted tokens' own block, and a gap before it
+        lists[..., -2], lists[..., -1] = -1, ((lens - 1) // PAGE)[:, None, None]
+    o, lse = run_cache(S, c, q, kp, vp, table=table, lists=lists, lens=lens, starts=starts, tree=tree)
+    want = R.attention(c, q.double(), k.double(), v.double(), R.sees(c, lists, lens, starts, tree))
+    R.check("o", o, *want["o"])
+    R.check("lse", lse, *want["lse"])
+
+
+LISTED = [  # a row, few rows, 32 rows to a list; long lists
+    case(b=4, nq=1, nk=8192, hq=2, hk=2, d=128, blocks=32), case(b=4, nq=1, nk=8000, hq=8, hk=2, d=128, blocks=32, dtype=torch.float16),
+    case(b=2, nq=5, nk=8192, hq=4, hk=2, blocks=48), case(b=1, nq=2, nk=3000, hq=16, hk=1, d=128, blocks=47),
+    case(b=2, nq=1, nk=30000, hq=4, hk=1, blocks=300),
+]
+
+
+@pytest.mark.parametrize("kind", ["full", "ragged", "odd"])
+@pytest.mark.parametrize("n", range(len(LISTED)))
+def test_lists_of_few_rows_in_ranges(S, n, kind):
+    """Lists that end inside a range, with gaps, doubles and blocks past the
+    end, empty ones, and pages that are none."""
+    c = LISTED[n]
+    assert ranges(plan(S, c), c, True) > 1, "the case must be cut"
+    q, k, v, _, g = inputs(c, 1520 + n)
+    lens, starts = lengths(c, g, kind)
+    lists = random_lists(c, g, empty=0.2)
+    lists[:, 0, :, 3], lists[:, 0, :, 9] = -1, 2 ** 31 - 1
+    lists[:, -1, :, 1] = lists[:, -1, :, 0]
+    kp, vp, table = paged(c, k, v, g)
+    ok = torch.ones(table.shape)
+    table[0, 2], table[-1, 5], ok[0, 2], ok[-1, 5] = -1, kp.shape[0], 0, 0
+    o, lse = run_cache(S, c, q, kp, vp, table=table, lists=lists, lens=lens, starts=starts)
+    want = R.attention(c, q.double(), k.double(), v.double(), R.sees(c, lists, lens, starts, None, ok))
+    R.check("o", o, *want["o"])
+    R.check("lse", lse, *want["lse"])
