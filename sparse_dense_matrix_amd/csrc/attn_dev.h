@@ -157,14 +157,6 @@ __device__ __forceinline__ void load_lds16(uint32_t lds, i32x4 buf, uint32_t vof
                : "s"(lds), "v"(voff), "s"(buf)
                : "memory", "m0");
 }
-// The same from an address of the lane's own.
-__device__ __forceinline__ void load_lds16(uint32_t lds, const char *p) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
-               :
-               : "s"(lds), "v"(p)
-               : "memory", "m0");
-}
-
 // 4 bytes a lane: LDS[lds + 4 * lane] = *p.
 __device__ __forceinline__ void load_lds4(uint32_t lds, const float *p) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
