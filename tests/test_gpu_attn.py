@@ -966,9 +966,9 @@ def test_short_sequences_next_to_a_long_one(S, hk, q_block, dtype):
         R.check(name, got[name], *want[name])
 
 
-@pytest.mark.parametrize("nq,q_block,hq,hk,dtype", [(700, 64, 8, 8, torch.bfloat16), (700, 16, 4, 1, torch.float16), (1300, 64, 16, 1, torch.bfloat16)])
+@pytest.mark.parametrize("nq,q_block,hq,hk,dtype", [(700, 64, 8, 8, torch.bfloat16), (700, 16, 4, 1, torch.float16), (1300, 64, 4, 1, torch.bfloat16)])
 def test_blocks_that_few_rows_read(S, nq, q_block, hq, hk, dtype):
-    """A long sequence whose lists name their own block: up to 1024 rows read it."""
+    """A long sequence whose lists name their own block: up to 256 rows read it."""
     c = case(nq=nq, hq=hq, hk=hk, d=128, q_block=q_block, blocks=1, dtype=dtype)
     q, k, v, grad, g = inputs(c, 1410 + q_block)
     nqb = -(-nq // q_block)
