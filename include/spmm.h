@@ -401,10 +401,17 @@ spmm_status_t spmm_execute_sddmm(spmm_plan_t p, const void *x_dev, int64_t ldx, 
  * nothing and writes nothing.
  *
  * Products run on bf16 or f16 operands with fp32 sums; softmax statistics are
- * fp32; weights and their gradients are rounded to the element type (nearest
- * even) for the products that take them; gradients of f16 weights at a power
- * of two of each row and key, so that they may pass the type's range where dq
- * and dk do not.  Same inputs, same bits.
+ * fp32.  A weight exp(s_tj - lse_t) is rounded to the element type (nearest
+ * even) for the product with v: o is off by about 1.35 times its own rounding.
+ * In the gradients, what enters dq is kept to twice the type's digits, and so
+ * is what enters dk and dv where few rows read a key block: in sequences of up
+ * to 128 queries in [0, lens[i]), and where the lists that name the block have
+ * up to 256 rows (queries times heads of the key head) between them.  Elsewhere
+ * it is rounded once, and dk and dv are off by about 1.4 times their own
+ * rounding.  The sum grad . o, which carries o's rounding, is made exact for
+ * lists that name one or two blocks.  In f16 these values stand at a power of
+ * two of each row or key, so that they may pass the type's range where dq and
+ * dk do not.  Same inputs, same bits.
  * Every execute only launches kernels on `stream`: it allocates nothing, does
  * not synchronise and can be captured into a graph.  A plan's workspace
  * allows one execute in flight at a time. */
