@@ -409,9 +409,9 @@ spmm_status_t spmm_execute_sddmm(spmm_plan_t p, const void *x_dev, int64_t ldx, 
  * up to 256 rows (queries times heads of the key head) between them.  Elsewhere
  * it is rounded once, and dk and dv are off by about 1.4 times their own
  * rounding.  The sum grad . o, which carries o's rounding, is made exact for
- * lists that name one or two blocks.  In f16 these values stand at a power of
- * two of each row or key, so that they may pass the type's range where dq and
- * dk do not.  Same inputs, same bits.
+ * lists that name one or two blocks.  The gradients of f16 weights stand at a
+ * power of two of each row or key, so that they may pass the type's range where
+ * dq and dk do not.  Same inputs, same bits.
  * Every execute only launches kernels on `stream`: it allocates nothing, does
  * not synchronise and can be captured into a graph.  A plan's workspace
  * allows one execute in flight at a time. */
