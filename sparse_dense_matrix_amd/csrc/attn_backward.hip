@@ -447,7 +447,7 @@ __global__ __launch_bounds__(64 * RW * KW, 2) void attn_dq(const AttnArgs a) {
 // the next V loads during the scores and dS, the next K during do . v.  The
 // four waves share a list, or with OWN have one each; with PACK the lists of
 // neighbouring query blocks share a wave's 32 rows as in the forward kernel.
-// 4k queries with a list each, 16 heads to a key head: 212 us (543 us with four
+// 4k queries with a list each, 16 heads to a key head: 205 us (543 us with four
 // waves, two stages and a barrier a list, 285 us without PACK).
 template <class T, int D, bool OWN, bool PACK>
 __global__ __launch_bounds__(256, 2) void attn_dq_stream(const AttnArgs a) {
@@ -659,9 +659,9 @@ struct DkvItem {
 // against 1022 us for 16k tokens, 32 heads over 8, 1024 keys a query).
 // 64 keys and 512 registers a wave halve the LDS reads, but one wave a SIMD
 // waits for each of them: 1218 us.  With operands read ahead and items from
-// queues 640 us, 0.83 PFLOP/s: the matrix cores are busy for 37% of it, and the
-// rows come from beyond L2 in half of all loads (each is read once for every
-// key block that its list names).
+// queues 650 to 670 us, 0.80 PFLOP/s: the matrix cores are busy for 37% of it,
+// and the rows come from beyond L2 in half of all loads (each is read once for
+// every key block that its list names), at 4.2 TB/s.
 // FINE is for key blocks that few rows read: P and dS enter their products as
 // two operands as dS does for dq, for a quarter more products.  With one operand
 // dk and dv are off by 1.4 times their own rounding, averaged over a tensor, and

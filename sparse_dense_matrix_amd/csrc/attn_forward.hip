@@ -239,7 +239,8 @@ __device__ __forceinline__ void store(const AttnArgs &a, const Item &it, const R
 // Many rows to a list: RW waves of 32 rows share each staged tile of KT keys;
 // KW groups of them take the tiles in turn.  Two stages: the next tile loads
 // while this one is multiplied.  32k tokens, 32 heads over 8, 2048 keys a
-// query: 1.09 ms, 0.96 PFLOP/s, 79% of the rate of a large matrix product.
+// query: 1.07 to 1.12 ms on different cards, 0.94 to 0.98 PFLOP/s, 77 to 80% of
+// the rate of a large matrix product.
 // Scores, softmax and the product with V follow one another in a wave, and ask
 // for LDS, vector units and matrix cores for about half of the time each, so
 // what counts is how many waves a SIMD holds: three (four waves of 32 rows a
