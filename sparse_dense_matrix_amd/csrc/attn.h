@@ -47,7 +47,7 @@ struct AttnArgs {
   // inverse lists (backward)
   int32_t *inv_ids;            // [b * hk][nqb * max_blocks] query blocks of each key block, key block major
   int32_t *inv_ptr;            // [b * hk][nkb][2] first entry and count of each key block
-  int32_t *items;              // [b * hk][slots] key block | chunk pairs, key block -1: none
+  int32_t *items;              // [b * hk][slots] key block (-1: none) and part of its inverse list, pairs
   int32_t *queue;              // [8] items taken of each queue of the dk, dv kernel
   int32_t chunk, slots;        // entries of an item; items of a head at most
   float *part_kv;              // [b * hk][slots][2][64][d] partial dk, dv of split key blocks

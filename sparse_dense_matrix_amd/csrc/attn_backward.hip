@@ -30,6 +30,7 @@ constexpr int kAhead = 4;               // operands read ahead of their product
 constexpr int kShort = 128;             // queries of a short sequence
 constexpr int kFewRows = 256;           // rows of a short inverse list: one query block of 64 with 4 heads to a key head
 constexpr int kFew = 2;                 // blocks of a short list
+constexpr int kFewBit = 1 << 30;        // of an item's part: few rows read the key block
 constexpr int kMaxChunk = 1024;         // query blocks of an item
 constexpr uint32_t kDeadRow = 0xffffff00u;  // offset past every buffer: a direct load gives zeros
 
@@ -54,6 +55,7 @@ __device__ void invert(const AttnArgs &a, int64_t which, char *lds) {
   const int b = bh / a.hk;
   const int32_t len = attn_len(a.lens, b, a.nk), start = attn_start(a.starts, b, a.nq, a.nk);
   const int nqb = a.pack ? a.list_nqb : a.nqb, q_block = a.pack ? a.q_block / a.pack : a.q_block;  // of one list
+  const int rows = a.pack ? a.rows / a.pack : a.rows;
   const uint32_t entries = static_cast<uint32_t>(nqb) * a.max_blocks;  // below 2^31
   const int32_t *lists = a.lists + bh * static_cast<int64_t>(entries);
   int *sums = reinterpret_cast<int *>(lds);  // [waves][2]
@@ -109,9 +111,11 @@ __device__ void invert(const AttnArgs &a, int64_t which, char *lds) {
   const int first = kb + less / a.chunk;
   const int next = kb + 1 == a.nkb ? a.slots : kb + 1 + (less + same) / a.chunk;
   const int n = max(1, (same + a.chunk - 1) / a.chunk);
+  // few queries in the sequence, or few rows that may read the block
+  const bool few = min(a.nq, len - start) - max(0, -start) <= kShort || static_cast<int64_t>(same) * rows <= kFewRows;
   for (int i = tid; i < next - first; i += nt) {
     items[2 * (first + i)] = i < n ? kb : -1;
-    items[2 * (first + i) + 1] = i;
+    items[2 * (first + i) + 1] = few ? i | kFewBit : i;
   }
   if (tid == 0) {
     a.inv_ptr[2 * (bh * a.nkb + kb)] = less;
@@ -627,6 +631,7 @@ __device__ __forceinline__ AttnArgs args_again() {
 // `part` of the `same` entries of its inverse list, which stand from `less` on.
 struct DkvItem {
   int b, h, slot, kb, part, less, same;
+  bool few;
   int32_t len, start;
 
   __device__ __forceinline__ DkvItem(const AttnArgs &a, int64_t item) {
@@ -638,14 +643,12 @@ struct DkvItem {
     kb = a.items[2 * (bh * a.slots + slot)];
     if (kb < 0) return;
     part = a.items[2 * (bh * a.slots + slot) + 1];
+    few = part & kFewBit;
+    part &= kFewBit - 1;
     less = a.inv_ptr[2 * (bh * a.nkb + kb)];
     same = a.inv_ptr[2 * (bh * a.nkb + kb) + 1];
     len = attn_len(a.lens, b, a.nk);
     start = attn_start(a.starts, b, a.nq, a.nk);
-  }
-  // few queries in the sequence, or few rows that may read the block
-  __device__ __forceinline__ bool few(const AttnArgs &a) const {
-    return min(a.nq, len - start) - max(0, -start) <= kShort || static_cast<int64_t>(same) * a.rows <= kFewRows;
   }
 };
 
@@ -941,7 +944,7 @@ __global__ __launch_bounds__(128 * RG) void attn_dkv(const AttnArgs) {
       const AttnArgs a = args_again();
       if (item < static_cast<int64_t>(a.b) * a.slots * a.hk) {
         const DkvItem it(a, item);
-        how = it.kb < 0 ? 0 : (it.few(a) ? 1 : 2);
+        how = it.kb < 0 ? 0 : (it.few ? 1 : 2);
       }
     }
     if (how == 1) dkv_item<T, D, RG, true>(lds, item);
