@@ -81,7 +81,8 @@ typedef enum {
   SPMM_FORMAT_24 = 2,
   SPMM_FORMAT_TVW = 3,   /* tile-vector-wise: 2:4 inside the stored tiles of a tile grid */
   SPMM_FORMAT_SLIDE = 4, /* (2N-2):2N as overlapping 2:4 windows                        */
-  SPMM_FORMAT_ATTN = 5   /* plans of spmm_plan_attn: no packed matrix                   */
+  SPMM_FORMAT_ATTN = 5,  /* plans of spmm_plan_attn: no packed matrix                   */
+  SPMM_FORMAT_ROPE = 6   /* plans of spmm_plan_attn_rope: no packed matrix              */
 } spmm_format_t;
 
 /* Packed sparse operand: immutable host arrays in the canonical layout below,
@@ -499,6 +500,120 @@ spmm_status_t spmm_execute_attn_cache(spmm_plan_t p, const spmm_attn_tensor_t *q
                                       const int32_t *table, const int32_t *lists_dev,
                                       const uint64_t *tree, const int32_t *lens, const int32_t *starts,
                                       hipStream_t stream);
+
+/* ---- attention over a cache in 8 bits ----
+ *
+ * A row is one token's key or value of one head.  It stands as codes with a
+ * scale: with top = max_c |x_c|,
+ *   scale = top / 127,   code_c = round(127 x_c / top), ties to the even code
+ * (codes 0 and scale 0 for top = 0; a row with an infinity or a NaN has codes 0
+ * and that scale, and stands for NaN).  code_c * scale is what it stands for.
+ *
+ * k8 and v8 are int8 tensors of the cache's shape, [pages][64][heads_kv][dim]
+ * reached through a table, or without one [batch][keys][heads_kv][dim], with
+ * strides in elements, multiples of 16, 16-byte aligned.  k_scale and v_scale
+ * are float[slots][heads_kv][64], slot = the block's page with a table, else
+ * i * ceil(keys / 64) + block, and the key's place in its block last.  All
+ * calls take a plan of spmm_plan_attn, whose dtype is that of q, k, v and o. */
+
+/* New tokens to the cache: token t of sequence i, k and v [batch][queries]
+ * [heads_kv][dim], goes to position starts[i] + t.  Tokens whose position is not
+ * in [0, lens[i]) or stands in no page write nothing, and nothing else of the
+ * cache is touched.  Two tokens must not go to one place (else it holds either's
+ * codes and scale, or some of both). */
+spmm_status_t spmm_execute_attn_write(spmm_plan_t p, const spmm_attn_tensor_t *k, const spmm_attn_tensor_t *v,
+                                      const spmm_attn_tensor_t *k8, const spmm_attn_tensor_t *v8,
+                                      float *k_scale_dev, float *v_scale_dev, int64_t pages,
+                                      const int32_t *table, const int32_t *lens, const int32_t *starts,
+                                      hipStream_t stream);
+
+/* The cache back to k and v [batch][keys][heads_kv][dim], code * scale rounded
+ * to the plan's type: what the calls over tensors of 16 bits take.  Keys at or
+ * past lens[i] are left as they were; keys in no page are zeros. */
+spmm_status_t spmm_execute_attn_read(spmm_plan_t p, const spmm_attn_tensor_t *k8, const spmm_attn_tensor_t *v8,
+                                     const float *k_scale_dev, const float *v_scale_dev, int64_t pages,
+                                     const spmm_attn_tensor_t *k, const spmm_attn_tensor_t *v, const int32_t *table,
+                                     const int32_t *lens, hipStream_t stream);
+
+/* spmm_execute_attn_pool of the keys that the codes stand for (code * scale, not
+ * rounded), for spmm_execute_attn_select. */
+spmm_status_t spmm_execute_attn_pool8(spmm_plan_t p, const spmm_attn_tensor_t *k8, const float *k_scale_dev,
+                                      int64_t pages, int8_t *pooled_dev, float *pooled_scale_dev,
+                                      const int32_t *table, const int32_t *lens, const int32_t *first,
+                                      hipStream_t stream);
+
+/* spmm_execute_attn_cache over such a cache.  Codes enter the products as they
+ * are: a score is the 32-bit sum of q times codes, times the key's scale, and
+ * a weight takes the value's scale before it is rounded, to bf16 (bf16 plans:
+ * within 2^-8 of itself) or to two bf16 parts (f16 plans: 2^-16).  A key or
+ * value that stands for NaN spreads as one does there. */
+spmm_status_t spmm_execute_attn_cache8(spmm_plan_t p, const spmm_attn_tensor_t *q, const spmm_attn_tensor_t *k8,
+                                       const spmm_attn_tensor_t *v8, const float *k_scale_dev,
+                                       const float *v_scale_dev, int64_t pages, const spmm_attn_tensor_t *o,
+                                       float *lse_dev, const int32_t *table, const int32_t *lists_dev,
+                                       const uint64_t *tree, const int32_t *lens, const int32_t *starts,
+                                       hipStream_t stream);
+
+/* ---- norm and rotation of queries and keys ----
+ *
+ * For each token's row x of each head of q (and of k), in one pass:
+ *   y_c = x_c w_c / sqrt(mean_c x_c^2 + eps)    (w NULL: y = x)
+ *   (o_u, o_v) = (y_u cos a - y_v sin a, y_u sin a + y_v cos a)
+ * for pair p = 0 .. pairs - 1 of channels (u, v) = (p, pairs + p), or
+ * interleaved (2 p, 2 p + 1), with the angle
+ *   a = positions[axis[p]][i][t] * freqs[p];
+ * channels from 2 * pairs on keep y.  positions is int32[axes][batch][tokens],
+ * or NULL: starts[i] + t on every axis.  One axis turns texts; images and video
+ * have pairs for time, height and width.  w is float[dim], one for all query
+ * heads and one for all key heads.
+ *
+ * With lens, tokens whose position starts[i] + t is not in [0, lens[i]) are
+ * left out: their outputs stay as they were, their gradients are zero, and they
+ * add nothing to a weight's (whatever stands in them).  lens NULL takes every
+ * token; starts NULL means 0.
+ *
+ * Tensors are [batch][tokens][heads][dim] as above, q and k of one buffer
+ * among them.  An output may be its own input (same data and strides); else it
+ * must not overlap one.  Angles are taken in 64 bits, the rest in 32, outputs
+ * rounded once; squares of a row must sum up below 2^128.  Same inputs, same
+ * bits.  The calls only launch kernels on `stream`. */
+typedef struct {
+  int64_t batch, tokens;        /* batch * tokens at most 2^31 - 1 (else UNSUPPORTED)   */
+  int32_t heads_q, heads_kv;
+  int32_t dim;                  /* 64 or 128 (else UNSUPPORTED)                         */
+  int32_t dtype;                /* SPMM_BF16 or SPMM_F16 (else UNSUPPORTED)             */
+  int32_t pairs;                /* a multiple of 8 (else UNSUPPORTED), at most dim / 2; 0: the norm alone */
+  int32_t axes;                 /* of positions, at least 1                             */
+  int32_t interleaved;          /* 1: neighbours are pairs; 0: halves                   */
+  int32_t backward;             /* 1: with workspace for spmm_execute_attn_rope_backward */
+  float eps;
+  const double *freqs;          /* host, [pairs]: radians a position                    */
+  const int32_t *axis;          /* host, [pairs], or NULL: all 0                        */
+} spmm_rope_desc_t;
+
+/* A plan for one shape on `device`; freqs and axis are copied.  spmm_plan_info:
+ * m = batch * tokens, k = heads_q + heads_kv, n = dim.  The other execute calls
+ * refuse it, and these two refuse other plans (INVALID_ARG). */
+spmm_status_t spmm_plan_attn_rope(const spmm_rope_desc_t *desc, int32_t device, spmm_plan_t *out);
+
+spmm_status_t spmm_execute_attn_rope(spmm_plan_t p, const spmm_attn_tensor_t *q, const spmm_attn_tensor_t *k,
+                                     const float *q_weight_dev, const float *k_weight_dev,
+                                     const spmm_attn_tensor_t *q_out, const spmm_attn_tensor_t *k_out,
+                                     const int32_t *positions, const int32_t *lens, const int32_t *starts,
+                                     hipStream_t stream);
+
+/* Gradients from q_grad and k_grad, those of the outputs: every element of dq, dk
+ * and, where there is a weight, of dq_weight and dk_weight (float[dim]) is
+ * written.  q and k are the forward call's inputs, read only where there is a
+ * weight (else they may be NULL).  dq may be q_grad or q itself, dk likewise.
+ * A plan's workspace allows one execute in flight at a time. */
+spmm_status_t spmm_execute_attn_rope_backward(spmm_plan_t p, const spmm_attn_tensor_t *q_grad,
+                                              const spmm_attn_tensor_t *k_grad, const spmm_attn_tensor_t *q,
+                                              const spmm_attn_tensor_t *k, const float *q_weight_dev,
+                                              const float *k_weight_dev, const spmm_attn_tensor_t *dq,
+                                              const spmm_attn_tensor_t *dk, float *dq_weight_dev,
+                                              float *dk_weight_dev, const int32_t *positions,
+                                              const int32_t *lens, const int32_t *starts, hipStream_t stream);
 
 /* ---- errors ---- */
 const char *spmm_status_str(spmm_status_t s);

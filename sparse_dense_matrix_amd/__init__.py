@@ -19,7 +19,7 @@ import numpy as np
 
 __all__ = [
     "SpmmError", "Matrix", "Plan", "F32", "BF16", "I8", "I32", "F16",
-    "FORMAT_BCSR", "FORMAT_WCSR", "FORMAT_24", "FORMAT_TVW", "FORMAT_SLIDE", "FORMAT_ATTN",
+    "FORMAT_BCSR", "FORMAT_WCSR", "FORMAT_24", "FORMAT_TVW", "FORMAT_SLIDE", "FORMAT_ATTN", "FORMAT_ROPE",
     "ARRAY_ROW_PTR", "ARRAY_COL_IDX", "ARRAY_VALS", "ARRAY_META",
     "ARRAY_CHUNK_WINDOW", "ARRAY_CHUNK_BEGIN", "ARRAY_ROW_PERM", "ARRAY_COL_PERM",
     "spmm_pack_bcsr", "spmm_pack_bcsr_csr", "spmm_pack_wcsr", "spmm_pack_24", "spmm_pack_tvw", "spmm_pack_slide",
@@ -28,6 +28,8 @@ __all__ = [
     "spmm_plan_sddmm", "spmm_execute_sddmm",
     "spmm_plan_attn", "spmm_execute_attn_pool", "spmm_execute_attn_select", "spmm_execute_attn",
     "spmm_execute_attn_backward", "spmm_execute_attn_cache",
+    "spmm_execute_attn_write", "spmm_execute_attn_read", "spmm_execute_attn_pool8", "spmm_execute_attn_cache8",
+    "spmm_plan_attn_rope", "spmm_execute_attn_rope", "spmm_execute_attn_rope_backward",
     "spmm_status_str", "spmm_last_error", "LIB_PATH", "EXPORTS",
 ]
 
@@ -37,7 +39,7 @@ LIB_PATH = os.environ.get("SPMM_LIBRARY") or os.path.join(HERE, "libspmm.so")
 
 F32, BF16, I8, I32, F16 = 0, 1, 2, 3, 4
 _ELEM = {F32: 4, BF16: 2, I8: 1, I32: 4}  # bytes per element of each type
-FORMAT_BCSR, FORMAT_WCSR, FORMAT_24, FORMAT_TVW, FORMAT_SLIDE, FORMAT_ATTN = 0, 1, 2, 3, 4, 5
+FORMAT_BCSR, FORMAT_WCSR, FORMAT_24, FORMAT_TVW, FORMAT_SLIDE, FORMAT_ATTN, FORMAT_ROPE = 0, 1, 2, 3, 4, 5, 6
 (ARRAY_ROW_PTR, ARRAY_COL_IDX, ARRAY_VALS, ARRAY_META, ARRAY_CHUNK_WINDOW,
  ARRAY_CHUNK_BEGIN, ARRAY_ROW_PERM, ARRAY_COL_PERM) = range(8)
 
@@ -55,6 +57,8 @@ EXPORTS = (
     "spmm_execute_sddmm",
     "spmm_plan_attn", "spmm_execute_attn_pool", "spmm_execute_attn_select", "spmm_execute_attn",
     "spmm_execute_attn_backward", "spmm_execute_attn_cache",
+    "spmm_execute_attn_write", "spmm_execute_attn_read", "spmm_execute_attn_pool8", "spmm_execute_attn_cache8",
+    "spmm_plan_attn_rope", "spmm_execute_attn_rope", "spmm_execute_attn_rope_backward",
     "spmm_status_str", "spmm_last_error",
 )
 
@@ -81,6 +85,13 @@ class AttnDesc(C.Structure):
                 ("dtype", C.c_int32), ("q_block", C.c_int32), ("max_blocks", C.c_int32),
                 ("sink_blocks", C.c_int32), ("local_blocks", C.c_int32), ("backward", C.c_int32),
                 ("scale", C.c_float)]
+
+
+class RopeDesc(C.Structure):
+    _fields_ = [("batch", C.c_int64), ("tokens", C.c_int64), ("heads_q", C.c_int32), ("heads_kv", C.c_int32),
+                ("dim", C.c_int32), ("dtype", C.c_int32), ("pairs", C.c_int32), ("axes", C.c_int32),
+                ("interleaved", C.c_int32), ("backward", C.c_int32), ("eps", C.c_float),
+                ("freqs", C.c_void_p), ("axis", C.c_void_p)]
 
 
 def _load():
@@ -120,6 +131,13 @@ def _load():
         "spmm_execute_attn": (st, [P] * 10),
         "spmm_execute_attn_backward": (st, [P] * 14),
         "spmm_execute_attn_cache": (st, [P, P, P, P, i64] + [P] * 8),
+        "spmm_execute_attn_write": (st, [P] * 7 + [i64] + [P] * 4),
+        "spmm_execute_attn_read": (st, [P] * 5 + [i64] + [P] * 5),
+        "spmm_execute_attn_pool8": (st, [P] * 3 + [i64] + [P] * 6),
+        "spmm_execute_attn_cache8": (st, [P] * 6 + [i64] + [P] * 8),
+        "spmm_plan_attn_rope": (st, [C.POINTER(RopeDesc), i32, C.POINTER(P)]),
+        "spmm_execute_attn_rope": (st, [P] * 11),
+        "spmm_execute_attn_rope_backward": (st, [P] * 15),
         "spmm_status_str": (C.c_char_p, [st]),
         "spmm_last_error": (C.c_char_p, []),
     }
@@ -474,7 +492,8 @@ def _attn_expect(d: AttnDesc, device: int) -> dict:
         "q": ((b, nq, hq, dim), t), "k": ((b, nk, hk, dim), t), "page": ((64, hk, dim), t),
         "lse": ((b, hq, nq), torch.float32), "lists": ((b, hk, nqb, d.max_blocks), torch.int32),
         "table": ((b, nkb), torch.int32), "seq": ((b,), torch.int32), "tree": ((b, nq), torch.int64),
-        "slots": b * nkb, "int8": torch.int8}}
+        "slots": b * nkb, "int8": torch.int8, "page8": ((64, hk, dim), torch.int8), "k8": ((b, nk, hk, dim), torch.int8),
+        "new": ((b, nq, hk, dim), t)}}
 
 
 _pack_tensor = struct.Struct("=4q").pack
@@ -623,3 +642,145 @@ def spmm_execute_attn_cache(plan: Plan, q, k, v, o, lse, table=None, lists=None,
         _opt("starts", starts, w["seq"], d), _stream_of(stream, d))
     if st:
         _check(st, "spmm_execute_attn_cache")
+
+
+def _codes(w, d, k8, v8, k_scale, v_scale, table):
+    """Pointers of a cache in 8 bits, and its pages."""
+    pages, slots, kw = 0, w["slots"], w["k8"]
+    if table is not None:
+        pages = slots = k8.shape[0]
+        kw = ((pages,) + w["page8"][0], w["page8"][1])
+    sw = ((slots, kw[0][2], 64), w["lse"][1])
+    return (_heads("k8", k8, kw, d), _heads("v8", v8, kw, d), _flat("k_scale", k_scale, sw, d),
+            _flat("v_scale", v_scale, sw, d), pages)
+
+
+def spmm_execute_attn_write(plan: Plan, k, v, k8, v8, k_scale, v_scale, table=None, lens=None, starts=None,
+                            stream=None):
+    """New tokens k, v [batch, queries, heads_kv, dim] to a cache in 8 bits, from
+    position starts on: k8 and v8 are pages [pages, 64, heads_kv, dim] int8 with a
+    table, else [batch, keys, heads_kv, dim]; k_scale and v_scale are [slots,
+    heads_kv, 64] float32 (slots = pages, or batch * blocks)."""
+    w, d = _attn_want(plan), plan.expect["device"]
+    st = _lib.spmm_execute_attn_write(
+        plan.handle, _heads("k", k, w["new"], d), _heads("v", v, w["new"], d),
+        *_codes(w, d, k8, v8, k_scale, v_scale, table), _opt("table", table, w["table"], d),
+        _opt("lens", lens, w["seq"], d), _opt("starts", starts, w["seq"], d), _stream_of(stream, d))
+    if st:
+        _check(st, "spmm_execute_attn_write")
+
+
+def spmm_execute_attn_read(plan: Plan, k8, v8, k_scale, v_scale, k, v, table=None, lens=None, stream=None):
+    """A cache in 8 bits (as spmm_execute_attn_write has it) back to k and v
+    [batch, keys, heads_kv, dim]; keys at or past lens are left as they were."""
+    w, d = _attn_want(plan), plan.expect["device"]
+    st = _lib.spmm_execute_attn_read(
+        plan.handle, *_codes(w, d, k8, v8, k_scale, v_scale, table), _heads("k", k, w["k"], d),
+        _heads("v", v, w["k"], d), _opt("table", table, w["table"], d), _opt("lens", lens, w["seq"], d),
+        _stream_of(stream, d))
+    if st:
+        _check(st, "spmm_execute_attn_read")
+
+
+def spmm_execute_attn_pool8(plan: Plan, k8, k_scale, pooled, pooled_scale, lens=None, table=None, first=None,
+                            stream=None):
+    """spmm_execute_attn_pool of the keys of a cache in 8 bits."""
+    w, d = _attn_want(plan), plan.expect["device"]
+    pages, slots, kw = 0, w["slots"], w["k8"]
+    if table is not None:
+        pages = slots = k8.shape[0]
+        kw = ((pages,) + w["page8"][0], w["page8"][1])
+    _, hk, dim = w["page"][0]
+    st = _lib.spmm_execute_attn_pool8(
+        plan.handle, _heads("k8", k8, kw, d), _flat("k_scale", k_scale, ((slots, hk, 64), w["lse"][1]), d), pages,
+        _flat("pooled", pooled, ((slots, hk, dim), w["int8"]), d),
+        _flat("pooled_scale", pooled_scale, ((slots, hk), w["lse"][1]), d), _opt("table", table, w["table"], d),
+        _opt("lens", lens, w["seq"], d), _opt("first", first, w["seq"], d), _stream_of(stream, d))
+    if st:
+        _check(st, "spmm_execute_attn_pool8")
+
+
+def spmm_execute_attn_cache8(plan: Plan, q, k8, v8, k_scale, v_scale, o, lse, table=None, lists=None, tree=None,
+                             lens=None, starts=None, stream=None):
+    """spmm_execute_attn_cache over a cache in 8 bits (as spmm_execute_attn_write
+    has it)."""
+    w, d = _attn_want(plan), plan.expect["device"]
+    qw = w["q"]
+    st = _lib.spmm_execute_attn_cache8(
+        plan.handle, _heads("q", q, qw, d), *_codes(w, d, k8, v8, k_scale, v_scale, table), _heads("o", o, qw, d),
+        _flat("lse", lse, w["lse"], d), _opt("table", table, w["table"], d), _opt("lists", lists, w["lists"], d),
+        _opt("tree", tree, w["tree"], d), _opt("lens", lens, w["seq"], d), _opt("starts", starts, w["seq"], d),
+        _stream_of(stream, d))
+    if st:
+        _check(st, "spmm_execute_attn_cache8")
+
+
+def spmm_plan_attn_rope(batch: int, tokens: int, heads_q: int, heads_kv: int, dim: int, freqs, axis=None,
+                        dtype: int = BF16, interleaved: bool = False, eps: float = 1e-6, backward: bool = False,
+                        axes: int | None = None, device: int = 0) -> Plan:
+    """Plan the norm of each head of queries and keys with the rotation of
+    len(freqs) pairs of channels: pair p turns by freqs[p] radians a position of
+    axis[p] (default: one axis).  Pairs are (p, pairs + p), or neighbours where
+    interleaved."""
+    f = np.ascontiguousarray(freqs, dtype=np.float64)
+    if f.ndim != 1:
+        raise ValueError("freqs must be 1-D")
+    x = None if axis is None else np.ascontiguousarray(axis, dtype=np.int32)
+    if x is not None and x.shape != f.shape:
+        raise ValueError("axis must have an entry for each pair")
+    if axes is None:
+        axes = 1 if x is None or not len(x) else int(x.max()) + 1
+    desc = RopeDesc(batch, tokens, heads_q, heads_kv, dim, dtype, len(f), axes, int(bool(interleaved)),
+                    int(bool(backward)), eps, _ptr(f), None if x is None else _ptr(x))
+    h = C.c_void_p()
+    _check(_lib.spmm_plan_attn_rope(C.byref(desc), device, C.byref(h)), "spmm_plan_attn_rope")
+    import torch
+    t = torch.bfloat16 if dtype == BF16 else torch.float16
+    return Plan(h, {"device": device, "rope": {
+        "q": ((batch, tokens, heads_q, dim), t), "k": ((batch, tokens, heads_kv, dim), t),
+        "weight": ((dim,), torch.float32), "positions": ((axes, batch, tokens), torch.int32),
+        "seq": ((batch,), torch.int32)}})
+
+
+def _rope_want(plan: Plan) -> dict:
+    want = plan.expect.get("rope")
+    if want is None:
+        raise ValueError("not a plan of spmm_plan_attn_rope")
+    return want
+
+
+def spmm_execute_attn_rope(plan: Plan, q, k, q_out, k_out, q_weight=None, k_weight=None, positions=None, lens=None,
+                           starts=None, stream=None):
+    """q_out and k_out: q [batch, tokens, heads_q, dim] and k [.., heads_kv, dim]
+    normed where there is a weight [dim] float32, and turned.  positions is
+    [axes, batch, tokens] int32, by default starts + t.  Tokens whose starts + t
+    is not in [0, lens) are left as they were."""
+    w, d = _rope_want(plan), plan.expect["device"]
+    qw, kw = w["q"], w["k"]
+    st = _lib.spmm_execute_attn_rope(
+        plan.handle, _heads("q", q, qw, d), _heads("k", k, kw, d), _opt("q_weight", q_weight, w["weight"], d),
+        _opt("k_weight", k_weight, w["weight"], d), _heads("q_out", q_out, qw, d), _heads("k_out", k_out, kw, d),
+        _opt("positions", positions, w["positions"], d), _opt("lens", lens, w["seq"], d),
+        _opt("starts", starts, w["seq"], d), _stream_of(stream, d))
+    if st:
+        _check(st, "spmm_execute_attn_rope")
+
+
+def spmm_execute_attn_rope_backward(plan: Plan, q_grad, k_grad, q, k, dq, dk, q_weight=None, k_weight=None,
+                                    dq_weight=None, dk_weight=None, positions=None, lens=None, starts=None,
+                                    stream=None):
+    """dq and dk (and dq_weight and dk_weight [dim] float32, where there are
+    weights) from the gradients of q_out and k_out; q and k are the forward
+    call's inputs (None where there is no weight).  The plan must have been made
+    with backward=True."""
+    w, d = _rope_want(plan), plan.expect["device"]
+    qw, kw, ww = w["q"], w["k"], w["weight"]
+    st = _lib.spmm_execute_attn_rope_backward(
+        plan.handle, _heads("q_grad", q_grad, qw, d), _heads("k_grad", k_grad, kw, d),
+        None if q is None else _heads("q", q, qw, d), None if k is None else _heads("k", k, kw, d),
+        _opt("q_weight", q_weight, ww, d), _opt("k_weight", k_weight, ww, d), _heads("dq", dq, qw, d),
+        _heads("dk", dk, kw, d), _opt("dq_weight", dq_weight, ww, d), _opt("dk_weight", dk_weight, ww, d),
+        _opt("positions", positions, w["positions"], d), _opt("lens", lens, w["seq"], d),
+        _opt("starts", starts, w["seq"], d), _stream_of(stream, d))
+    if st:
+        _check(st, "spmm_execute_attn_rope_backward")

@@ -84,22 +84,6 @@ spmm_status_t plan_workspace(spmm_plan_s *p, size_t bytes, void **dst) {
   return SPMM_OK;
 }
 
-// SPMM_LOG set to anything but "" or "0": every plan that succeeds prints
-// its decisions (kernel, tile, grid, schedule, device and workspace bytes)
-// as one line on stderr.  Read at each call.
-bool plan_log_on() {
-  const char *v = std::getenv("SPMM_LOG");
-  return v && v[0] && std::strcmp(v, "0") != 0;
-}
-
-namespace {
-
-// A new packed operand, owned until it is handed to the caller.
-std::unique_ptr<spmm_matrix_s> new_matrix() {
-  if (alloc_hook_fail()) throw std::bad_alloc();
-  return std::unique_ptr<spmm_matrix_s>(new spmm_matrix_s());
-}
-
 // hipMalloc + copy; the pointer is owned by the plan.
 spmm_status_t upload(spmm_plan_s *p, const void *src, size_t bytes, void **dst) {
   *dst = nullptr;
@@ -119,6 +103,22 @@ spmm_status_t upload(spmm_plan_s *p, const void *src, size_t bytes, void **dst) 
   }
   *dst = d;
   return SPMM_OK;
+}
+
+// SPMM_LOG set to anything but "" or "0": every plan that succeeds prints
+// its decisions (kernel, tile, grid, schedule, device and workspace bytes)
+// as one line on stderr.  Read at each call.
+bool plan_log_on() {
+  const char *v = std::getenv("SPMM_LOG");
+  return v && v[0] && std::strcmp(v, "0") != 0;
+}
+
+namespace {
+
+// A new packed operand, owned until it is handed to the caller.
+std::unique_ptr<spmm_matrix_s> new_matrix() {
+  if (alloc_hook_fail()) throw std::bad_alloc();
+  return std::unique_ptr<spmm_matrix_s>(new spmm_matrix_s());
 }
 
 template <class T>
@@ -785,7 +785,8 @@ spmm_status_t spmm_matrix_array(spmm_matrix_t a, int32_t which, const void **dat
         return a->dtype == SPMM_BF16 ? give(a->vals24_bf16) : give(a->vals24);
       if (which == SPMM_ARRAY_META) return give(a->meta24);
       break;
-    case SPMM_FORMAT_ATTN:  // plans only: no matrix has it
+    case SPMM_FORMAT_ATTN:  // plans only: no matrix has them
+    case SPMM_FORMAT_ROPE:
       break;
   }
   return fail(SPMM_ERR_INVALID_ARG, "spmm_matrix_array: no such array for this format");
@@ -871,6 +872,7 @@ spmm_status_t execute(const char *fn, spmm_plan_t p, const void *b_dev, int64_t 
   if (!p) return fail(SPMM_ERR_INVALID_ARG, name + ": plan is NULL");
   if (p->sddmm) return fail(SPMM_ERR_INVALID_ARG, name + ": plan is an SDDMM plan");
   if (p->attn) return fail(SPMM_ERR_INVALID_ARG, name + ": plan is an attention plan");
+  if (p->rope) return fail(SPMM_ERR_INVALID_ARG, name + ": plan is a rotation plan");
   const Matrix &a = *p->a;
   const int64_t n = p->n;
   if (n == 0 || a.m == 0) return SPMM_OK;

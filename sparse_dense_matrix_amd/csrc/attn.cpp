@@ -51,9 +51,10 @@ bool rows_overlap(int64_t outer, int64_t sb, int64_t tokens, int64_t st, int64_t
 }
 
 // A tensor [batch][tokens][heads][dim] as the kernels take it.  `outer` is the
-// number of sequences or pages.  Strides of an extent of one do not matter.
+// number of sequences or pages, `elem` the bytes of an element.  Strides of an
+// extent of one do not matter.
 spmm_status_t view(const char *fn, const char *name, const spmm_attn_tensor_t *t, int64_t outer, int64_t tokens,
-                   int64_t heads, int64_t dim, bool written, bool keys, AttnView *v) {
+                   int64_t heads, int64_t dim, bool written, bool keys, AttnView *v, int64_t elem = kElem) {
   *v = AttnView{nullptr, 0, 0, 0};
   if (!t) return bad(fn, std::string(name) + " is NULL");
   if (outer == 0 || tokens == 0) return SPMM_OK;  // holds nothing
@@ -61,22 +62,24 @@ spmm_status_t view(const char *fn, const char *name, const spmm_attn_tensor_t *t
   if (reinterpret_cast<uintptr_t>(t->data) & 15u) return bad(fn, std::string(name) + " is not 16-byte aligned");
   const int64_t sb = outer > 1 ? t->stride_batch : 0, st = tokens > 1 ? t->stride_token : dim,
                 sh = heads > 1 ? t->stride_head : 0;
-  if (sb < 0 || st < 0 || sh < 0 || sb % 8 || st % 8 || sh % 8)
-    return bad(fn, std::string(name) + ": strides must be multiples of 8 elements, none negative");
+  if (sb < 0 || st < 0 || sh < 0 || sb % (16 / elem) || st % (16 / elem) || sh % (16 / elem))
+    return bad(fn, std::string(name) + ": strides must be multiples of " + std::to_string(16 / elem) +
+                       " elements, none negative");
   const int64_t most = int64_t(1) << 60;
-  if (sb > most / kElem / std::max<int64_t>(1, outer) || st > most / kElem / std::max<int64_t>(1, tokens) ||
-      sh > most / kElem / std::max<int64_t>(1, heads))
+  if (sb > most / elem / std::max<int64_t>(1, outer) || st > most / elem / std::max<int64_t>(1, tokens) ||
+      sh > most / elem / std::max<int64_t>(1, heads))
     return bad(fn, std::string(name) + ": strides too large");
   if (written && rows_overlap(outer, sb, tokens, st, heads, sh, dim))
     return bad(fn, std::string(name) + " is written: its rows must not overlap");
   // the kernels bound a block's rows by their byte offset from its first one
-  if (keys && (st < dim || st * kElem * kAttnPage >= (int64_t(1) << 31)))
+  if (keys && (st < dim || st * elem * kAttnPage >= (int64_t(1) << 31)))
     return fail(SPMM_ERR_UNSUPPORTED, std::string(fn) + ": " + name +
-                                          ": the token stride must be at least dim and below 16 Mi elements");
+                                          ": the token stride must be at least dim and below " + std::to_string(32 / elem) +
+                                          " Mi elements");
   v->p = static_cast<char *>(t->data);
-  v->sb = sb * kElem;
-  v->st = st * kElem;
-  v->sh = sh * kElem;
+  v->sb = sb * elem;
+  v->st = st * elem;
+  v->sh = sh * elem;
   return SPMM_OK;
 }
 
@@ -91,6 +94,12 @@ spmm_status_t whole(const char *fn, const char *name, const void *p, uintptr_t t
 spmm_status_t attn_plan_of(const char *fn, spmm_plan_t p) {
   if (!p) return bad(fn, "plan is NULL");
   if (!p->attn) return bad(fn, "plan is not an attention plan");
+  return SPMM_OK;
+}
+
+spmm_status_t rope_plan_of(const char *fn, spmm_plan_t p) {
+  if (!p) return bad(fn, "plan is NULL");
+  if (!p->rope) return bad(fn, "plan is not a rotation plan");
   return SPMM_OK;
 }
 
@@ -124,6 +133,20 @@ void attn_log(const spmm_plan_s *p) {
                static_cast<int>(p->attn_split_all[0]), static_cast<int>(a.chunk), static_cast<int>(i.tile_m),
                static_cast<int>(i.tile_n), static_cast<long long>(i.grid), static_cast<long long>(i.device_bytes),
                static_cast<long long>(i.workspace_bytes));
+  std::fflush(stderr);
+}
+
+void rope_log(const spmm_plan_s *p) {
+  const spmm_plan_info_t &i = p->info;
+  const RopeArgs &a = p->rope_args;
+  std::fprintf(stderr,
+               "[spmm] spmm_plan_attn_rope: format=rope device=%d m=%lld k=%lld n=%lld kernel=rope_forward%s pairs=%d "
+               "axes=%d interleaved=%d tile=%dx%d grid=%lld device_bytes=%lld workspace_bytes=%lld\n",
+               static_cast<int>(i.device), static_cast<long long>(i.m), static_cast<long long>(i.k),
+               static_cast<long long>(i.n), p->rope_desc.backward ? "+rope_backward+rope_weights" : "",
+               static_cast<int>(a.pairs), static_cast<int>(a.axes), static_cast<int>(a.interleaved),
+               static_cast<int>(i.tile_m), static_cast<int>(i.tile_n), static_cast<long long>(i.grid),
+               static_cast<long long>(i.device_bytes), static_cast<long long>(i.workspace_bytes));
   std::fflush(stderr);
 }
 
@@ -237,7 +260,109 @@ spmm_status_t attn_shape(const spmm_attn_desc_t &d, spmm_plan_s *p) {
   return SPMM_OK;
 }
 
+spmm_status_t rope_shape(const spmm_rope_desc_t &d, spmm_plan_s *p) {
+  const char *fn = "spmm_plan_attn_rope";
+  if (d.batch < 0 || d.tokens < 0 || d.batch > INT32_MAX || d.tokens > INT32_MAX)
+    return bad(fn, "batch and tokens must be 0 .. 2^31 - 1");
+  if (d.heads_q < 1 || d.heads_kv < 1) return bad(fn, "heads_q and heads_kv must be positive");
+  if (d.pairs < 0 || d.pairs > d.dim / 2) return bad(fn, "pairs must be 0 .. dim / 2");
+  if (d.axes < 1) return bad(fn, "axes must be positive");
+  if ((d.interleaved != 0 && d.interleaved != 1) || (d.backward != 0 && d.backward != 1))
+    return bad(fn, "interleaved and backward must be 0 or 1");
+  if (!(d.eps >= 0.0f) || std::isinf(d.eps)) return bad(fn, "eps must be finite and not negative");
+  if (d.pairs > 0 && !d.freqs) return bad(fn, "freqs is NULL");
+  for (int32_t i = 0; i < d.pairs; ++i) {
+    if (!std::isfinite(d.freqs[i])) return bad(fn, "freqs must be finite");
+    if (d.axis && (d.axis[i] < 0 || d.axis[i] >= d.axes)) return bad(fn, "axis must be 0 .. axes - 1");
+  }
+  if (d.dtype != SPMM_BF16 && d.dtype != SPMM_F16) return fail(SPMM_ERR_UNSUPPORTED, std::string(fn) + ": bf16 or f16 only");
+  if (d.dim != 64 && d.dim != 128) return fail(SPMM_ERR_UNSUPPORTED, std::string(fn) + ": dim must be 64 or 128");
+  if (d.pairs % 8 != 0) return fail(SPMM_ERR_UNSUPPORTED, std::string(fn) + ": pairs must be a multiple of 8");
+  if (d.heads_q > 65536 || d.heads_kv > 65536)
+    return fail(SPMM_ERR_UNSUPPORTED, std::string(fn) + ": more than 65536 heads");
+  if (d.batch * d.tokens > INT32_MAX) return fail(SPMM_ERR_UNSUPPORTED, std::string(fn) + ": batch * tokens above 2^31 - 1");
+  p->rope = true;
+  p->rope_desc = d;
+  p->rope_desc.freqs = nullptr;
+  p->rope_desc.axis = nullptr;
+  RopeArgs &a = p->rope_args;
+  a = RopeArgs{};
+  a.b = static_cast<int32_t>(d.batch);
+  a.n = static_cast<int32_t>(d.tokens);
+  a.heads[0] = d.heads_q;
+  a.heads[1] = d.heads_kv;
+  a.pairs = d.pairs;
+  a.axes = d.axes;
+  a.interleaved = d.interleaved;
+  a.eps = d.eps;
+  const int64_t tiles = rope_tiles(d.batch * d.tokens);
+  // four workgroups a CU take the tiles in turn, so that each leaves one sum
+  a.grid = static_cast<int32_t>(std::min<int64_t>(tiles, 1024));
+  p->info.format = SPMM_FORMAT_ROPE;
+  p->info.m = d.batch * d.tokens;
+  p->info.k = d.heads_q + d.heads_kv;
+  p->info.n = d.dim;
+  p->info.tile_m = static_cast<int32_t>(rope_tile());
+  p->info.tile_n = d.dim;
+  p->info.grid = tiles;
+  return SPMM_OK;
+}
+
 namespace {
+
+spmm_status_t plan_rope(spmm_plan_s *p, const spmm_rope_desc_t &d) {
+  RopeArgs &a = p->rope_args;
+  constexpr int32_t kMost = 64;  // pairs
+  double turns[kMost] = {};
+  int32_t axis[kMost] = {};
+  for (int32_t i = 0; i < d.pairs; ++i) {
+    turns[i] = d.freqs[i] / 6.283185307179586476925;
+    axis[i] = d.axis ? d.axis[i] : 0;
+  }
+  void *ptr = nullptr;
+  ATTN_TRY(upload(p, turns, sizeof(turns), &ptr));
+  a.turns = static_cast<const double *>(ptr);
+  ATTN_TRY(upload(p, axis, sizeof(axis), &ptr));
+  a.axis = static_cast<const int32_t *>(ptr);
+  if (!d.backward) return SPMM_OK;
+  ATTN_TRY(plan_workspace(p, static_cast<size_t>(a.grid) * 2 * d.dim * 4, &ptr));
+  a.part = static_cast<float *>(ptr);
+  return SPMM_OK;
+}
+
+// What the two rotation calls share.
+spmm_status_t rope_args(const char *fn, spmm_plan_t p, const spmm_attn_tensor_t *q, const spmm_attn_tensor_t *k,
+                        const float *qw, const float *kw, const int32_t *positions, const int32_t *lens,
+                        const int32_t *starts, bool inputs, RopeArgs *a) {
+  const int64_t dim = p->rope_desc.dim;
+  if (inputs || qw) ATTN_TRY(view(fn, "q", q, a->b, a->n, a->heads[0], dim, false, false, &a->x[0]));
+  if (inputs || kw) ATTN_TRY(view(fn, "k", k, a->b, a->n, a->heads[1], dim, false, false, &a->x[1]));
+  ATTN_TRY(whole(fn, "q_weight", qw, 4, false));
+  ATTN_TRY(whole(fn, "k_weight", kw, 4, false));
+  ATTN_TRY(whole(fn, "positions", positions, 4, false));
+  ATTN_TRY(whole(fn, "lens", lens, 4, false));
+  ATTN_TRY(whole(fn, "starts", starts, 4, false));
+  a->w[0] = qw;
+  a->w[1] = kw;
+  a->positions = positions;
+  a->lens = lens;
+  a->starts = starts;
+  return SPMM_OK;
+}
+
+// The codes and scales of a cache in 8 bits.
+spmm_status_t codes_args(const char *fn, const AttnArgs &a, int64_t dim, const spmm_attn_tensor_t *k8,
+                         const spmm_attn_tensor_t *v8, const float *k_scale, const float *v_scale, int64_t outer,
+                         const int32_t *table, bool written, AttnView *kv, AttnView *vv) {
+  const int64_t tokens = table ? kAttnPage : a.nk;
+  ATTN_TRY(view(fn, "k8", k8, outer, tokens, a.hk, dim, written, true, kv, 1));
+  if (vv) ATTN_TRY(view(fn, "v8", v8, outer, tokens, a.hk, dim, written, true, vv, 1));
+  const bool some = outer > 0 && a.nkb > 0;
+  ATTN_TRY(whole(fn, "k_scale", k_scale, 4, some));
+  if (vv) ATTN_TRY(whole(fn, "v_scale", v_scale, 4, some));
+  ATTN_TRY(whole(fn, "table", table, 4, false));
+  return SPMM_OK;
+}
 
 spmm_status_t plan_attn(spmm_plan_s *p) {
   AttnArgs &a = p->attn_args;
@@ -269,36 +394,14 @@ spmm_status_t plan_attn(spmm_plan_s *p) {
   return SPMM_OK;
 }
 
-// q, k, v, o, lse and the lengths: what the forward calls share
-spmm_status_t forward_args(const char *fn, spmm_plan_t p, const spmm_attn_tensor_t *q, const spmm_attn_tensor_t *k,
-                           const spmm_attn_tensor_t *v, int64_t outer, int64_t tokens, const spmm_attn_tensor_t *o,
-                           bool o_written, float *lse, const int32_t *lens, const int32_t *starts, AttnArgs *a) {
-  const int64_t dim = p->attn_desc.dim;
-  ATTN_TRY(view(fn, "q", q, a->b, a->nq, a->hq, dim, false, false, &a->q));
-  ATTN_TRY(view(fn, "k", k, outer, tokens, a->hk, dim, false, true, &a->k));
-  ATTN_TRY(view(fn, "v", v, outer, tokens, a->hk, dim, false, true, &a->v));
-  ATTN_TRY(view(fn, "o", o, a->b, a->nq, a->hq, dim, o_written, false, &a->o));
-  ATTN_TRY(whole(fn, "lse", lse, 4, static_cast<int64_t>(a->b) * a->nq > 0));
-  ATTN_TRY(whole(fn, "lens", lens, 4, false));
-  ATTN_TRY(whole(fn, "starts", starts, 4, false));
-  a->lse = lse;
-  a->lens = lens;
-  a->starts = starts;
-  return SPMM_OK;
-}
-
-}  // namespace
-}  // namespace sdm
-
-using namespace sdm;
-
-extern "C" {
-
-spmm_status_t spmm_plan_attn(const spmm_attn_desc_t *desc, int32_t device, spmm_plan_t *out) {
+// A plan without a matrix: `shape` checks the descriptor, `make` allocates.
+template <class Desc, class Shape, class Make, class Log>
+spmm_status_t plan_of(const std::string &fn, const Desc *desc, int32_t device, spmm_plan_t *out, Shape shape, Make make,
+                      Log log) {
   alloc_hook_begin();
-  if (!out) return fail(SPMM_ERR_INVALID_ARG, "spmm_plan_attn: out is NULL");
+  if (!out) return fail(SPMM_ERR_INVALID_ARG, fn + ": out is NULL");
   *out = nullptr;
-  if (!desc) return fail(SPMM_ERR_INVALID_ARG, "spmm_plan_attn: desc is NULL");
+  if (!desc) return fail(SPMM_ERR_INVALID_ARG, fn + ": desc is NULL");
   return guarded([&]() -> spmm_status_t {
     if (alloc_hook_fail()) throw std::bad_alloc();
     auto *p = new spmm_plan_s();
@@ -306,16 +409,16 @@ spmm_status_t spmm_plan_attn(const spmm_attn_desc_t *desc, int32_t device, spmm_
     p->info.device = device;
     spmm_status_t s = SPMM_ERR_INTERNAL;
     try {
-      s = attn_shape(*desc, p);
+      s = shape(*desc, p);
       if (s == SPMM_OK) {
         int ndev = 0;
         hipError_t e = hipGetDeviceCount(&ndev);
         if (e != hipSuccess) s = hip_fail(e, "hipGetDeviceCount");
-        else if (device < 0 || device >= ndev) s = fail(SPMM_ERR_INVALID_ARG, "spmm_plan_attn: no such device");
+        else if (device < 0 || device >= ndev) s = fail(SPMM_ERR_INVALID_ARG, fn + ": no such device");
       }
       if (s == SPMM_OK) {
         DeviceScope ds(device);
-        s = ds.err != hipSuccess ? hip_fail(ds.err, "hipSetDevice") : plan_attn(p);
+        s = ds.err != hipSuccess ? hip_fail(ds.err, "hipSetDevice") : make(p, *desc);
       }
     } catch (...) {
       free_plan(p);
@@ -326,28 +429,51 @@ spmm_status_t spmm_plan_attn(const spmm_attn_desc_t *desc, int32_t device, spmm_
       return s;
     }
     *out = p;
-    if (plan_log_on()) attn_log(p);
+    if (plan_log_on()) log(p);
     return SPMM_OK;
   });
 }
 
-spmm_status_t spmm_execute_attn_pool(spmm_plan_t p, const spmm_attn_tensor_t *k, int64_t pages, int8_t *pooled_dev,
-                                     float *scale_dev, const int32_t *table, const int32_t *lens,
-                                     const int32_t *first, hipStream_t stream) {
-  const char *fn = "spmm_execute_attn_pool";
+// q, k, v, o, lse and the lengths: what the forward calls share
+spmm_status_t forward_args(const char *fn, spmm_plan_t p, const spmm_attn_tensor_t *q, const spmm_attn_tensor_t *k,
+                           const spmm_attn_tensor_t *v, int64_t outer, int64_t tokens, const spmm_attn_tensor_t *o,
+                           bool o_written, float *lse, const int32_t *lens, const int32_t *starts, AttnArgs *a,
+                           int64_t kv_elem = kElem) {
+  const int64_t dim = p->attn_desc.dim;
+  ATTN_TRY(view(fn, "q", q, a->b, a->nq, a->hq, dim, false, false, &a->q));
+  ATTN_TRY(view(fn, kv_elem == 1 ? "k8" : "k", k, outer, tokens, a->hk, dim, false, true, &a->k, kv_elem));
+  ATTN_TRY(view(fn, kv_elem == 1 ? "v8" : "v", v, outer, tokens, a->hk, dim, false, true, &a->v, kv_elem));
+  ATTN_TRY(view(fn, "o", o, a->b, a->nq, a->hq, dim, o_written, false, &a->o));
+  ATTN_TRY(whole(fn, "lse", lse, 4, static_cast<int64_t>(a->b) * a->nq > 0));
+  ATTN_TRY(whole(fn, "lens", lens, 4, false));
+  ATTN_TRY(whole(fn, "starts", starts, 4, false));
+  a->lse = lse;
+  a->lens = lens;
+  a->starts = starts;
+  return SPMM_OK;
+}
+
+// spmm_execute_attn_pool, and with `codes` spmm_execute_attn_pool8
+spmm_status_t pool(const char *fn, spmm_plan_t p, const spmm_attn_tensor_t *k, const float *k_scale, bool codes,
+                   int64_t pages, int8_t *pooled_dev, float *scale_dev, const int32_t *table, const int32_t *lens,
+                   const int32_t *first, hipStream_t stream) {
   return guarded([&]() -> spmm_status_t {
     ATTN_TRY(attn_plan_of(fn, p));
     const AttnArgs &a = p->attn_args;
     int64_t outer = 0;
     ATTN_TRY(pages_of(fn, a, table, pages, &outer));
     AttnPoolArgs x{};
-    ATTN_TRY(view(fn, "k", k, outer, table ? kAttnPage : a.nk, a.hk, p->attn_desc.dim, false, true, &x.k));
     const bool some = outer > 0 && a.nkb > 0;
+    if (codes)
+      ATTN_TRY(codes_args(fn, a, p->attn_desc.dim, k, nullptr, k_scale, nullptr, outer, table, false, &x.k, nullptr));
+    else
+      ATTN_TRY(view(fn, "k", k, outer, table ? kAttnPage : a.nk, a.hk, p->attn_desc.dim, false, true, &x.k));
     ATTN_TRY(whole(fn, "pooled", pooled_dev, 16, some));
     ATTN_TRY(whole(fn, "pooled_scale", scale_dev, 4, some));
     ATTN_TRY(whole(fn, "table", table, 4, false));
     ATTN_TRY(whole(fn, "lens", lens, 4, false));
     ATTN_TRY(whole(fn, "first", first, 4, false));
+    x.k_scale = codes ? k_scale : nullptr;
     x.pooled = pooled_dev;
     x.pooled_scale = scale_dev;
     x.table = table;
@@ -365,6 +491,110 @@ spmm_status_t spmm_execute_attn_pool(spmm_plan_t p, const spmm_attn_tensor_t *k,
     if (ds.err != hipSuccess) return hip_fail(ds.err, "hipSetDevice");
     return launched(launch_attn_pool(x, static_cast<spmm_dtype_t>(p->attn_desc.dtype), p->attn_desc.dim, stream));
   });
+}
+
+// spmm_execute_attn_cache, and with scales spmm_execute_attn_cache8
+spmm_status_t cache(const char *fn, spmm_plan_t p, const spmm_attn_tensor_t *q, const spmm_attn_tensor_t *k,
+                    const spmm_attn_tensor_t *v, const AttnScales *scales, int64_t pages, const spmm_attn_tensor_t *o,
+                    float *lse_dev, const int32_t *table, const int32_t *lists_dev, const uint64_t *tree,
+                    const int32_t *lens, const int32_t *starts, hipStream_t stream) {
+  return guarded([&]() -> spmm_status_t {
+    ATTN_TRY(attn_plan_of(fn, p));
+    AttnArgs a = p->attn_args;
+    int64_t outer = 0;
+    ATTN_TRY(pages_of(fn, a, table, pages, &outer));
+    ATTN_TRY(forward_args(fn, p, q, k, v, outer, table ? kAttnPage : a.nk, o, true, lse_dev, lens, starts, &a,
+                          scales ? 1 : kElem));
+    if (scales) {
+      const bool some = outer > 0 && a.nkb > 0;
+      ATTN_TRY(whole(fn, "k_scale", scales->k, 4, some));
+      ATTN_TRY(whole(fn, "v_scale", scales->v, 4, some));
+    }
+    ATTN_TRY(whole(fn, "table", table, 4, false));
+    ATTN_TRY(whole(fn, "lists", lists_dev, 4, false));
+    ATTN_TRY(whole(fn, "tree", tree, 8, false));
+    if (tree && a.nq > 64) return fail(SPMM_ERR_UNSUPPORTED, std::string(fn) + ": a tree holds at most 64 tokens");
+    if (static_cast<int64_t>(a.b) * a.nq == 0) return SPMM_OK;
+    a.table = table;
+    a.pages = static_cast<int32_t>(pages);
+    a.lists = lists_dev;
+    a.tree = tree;
+    a.entries = lists_dev ? a.max_blocks : a.nkb;
+    const int32_t *split = lists_dev ? p->attn_split_listed : p->attn_split_all;
+    a.nsplit = split[0];
+    a.per_split = split[1];
+    const spmm_dtype_t t = static_cast<spmm_dtype_t>(p->attn_desc.dtype);
+    DeviceScope ds(p->device);
+    if (ds.err != hipSuccess) return hip_fail(ds.err, "hipSetDevice");
+    return launched(scales ? launch_attn_cache8(a, *scales, t, p->attn_desc.dim, stream)
+                           : launch_attn_forward(a, t, p->attn_desc.dim, stream));
+  });
+}
+
+// spmm_execute_attn_write and spmm_execute_attn_read: `n` tokens of each
+// sequence go from k, v to the cache, or come from it.
+spmm_status_t codes(const char *fn, bool read, spmm_plan_t p, const spmm_attn_tensor_t *k, const spmm_attn_tensor_t *v,
+                    const spmm_attn_tensor_t *k8, const spmm_attn_tensor_t *v8, float *k_scale, float *v_scale,
+                    int64_t pages, const int32_t *table, const int32_t *lens, const int32_t *starts, hipStream_t stream) {
+  return guarded([&]() -> spmm_status_t {
+    ATTN_TRY(attn_plan_of(fn, p));
+    const AttnArgs &a = p->attn_args;
+    const int64_t dim = p->attn_desc.dim;
+    int64_t outer = 0;
+    ATTN_TRY(pages_of(fn, a, table, pages, &outer));
+    AttnCodesArgs x{};
+    x.n = read ? a.nk : a.nq;
+    ATTN_TRY(view(fn, "k", k, a.b, x.n, a.hk, dim, read, false, &x.k));
+    ATTN_TRY(view(fn, "v", v, a.b, x.n, a.hk, dim, read, false, &x.v));
+    ATTN_TRY(codes_args(fn, a, dim, k8, v8, k_scale, v_scale, outer, table, !read, &x.k8, &x.v8));
+    ATTN_TRY(whole(fn, "lens", lens, 4, false));
+    ATTN_TRY(whole(fn, "starts", starts, 4, false));
+    if (static_cast<double>(a.b) * x.n * a.hk > 8.0 * 0x7fffffff)  // eight rows a workgroup at least
+      return fail(SPMM_ERR_UNSUPPORTED, std::string(fn) + ": more workgroups than a launch holds");
+    x.k_scale = k_scale;
+    x.v_scale = v_scale;
+    x.table = table;
+    x.lens = lens;
+    x.starts = starts;
+    x.b = a.b;
+    x.nk = a.nk;
+    x.hk = a.hk;
+    x.nkb = a.nkb;
+    x.pages = static_cast<int32_t>(pages);
+    if (a.b == 0 || x.n == 0 || a.nkb == 0) return SPMM_OK;
+    const spmm_dtype_t t = static_cast<spmm_dtype_t>(p->attn_desc.dtype);
+    DeviceScope ds(p->device);
+    if (ds.err != hipSuccess) return hip_fail(ds.err, "hipSetDevice");
+    return launched(read ? launch_attn_read(x, t, p->attn_desc.dim, stream) : launch_attn_write(x, t, p->attn_desc.dim, stream));
+  });
+}
+
+}  // namespace
+}  // namespace sdm
+
+using namespace sdm;
+
+extern "C" {
+
+spmm_status_t spmm_plan_attn(const spmm_attn_desc_t *desc, int32_t device, spmm_plan_t *out) {
+  return plan_of("spmm_plan_attn", desc, device, out, attn_shape,
+                 [](spmm_plan_s *p, const spmm_attn_desc_t &) { return plan_attn(p); }, attn_log);
+}
+
+spmm_status_t spmm_plan_attn_rope(const spmm_rope_desc_t *desc, int32_t device, spmm_plan_t *out) {
+  return plan_of("spmm_plan_attn_rope", desc, device, out, rope_shape, plan_rope, rope_log);
+}
+
+spmm_status_t spmm_execute_attn_pool(spmm_plan_t p, const spmm_attn_tensor_t *k, int64_t pages, int8_t *pooled_dev,
+                                     float *scale_dev, const int32_t *table, const int32_t *lens,
+                                     const int32_t *first, hipStream_t stream) {
+  return pool("spmm_execute_attn_pool", p, k, nullptr, false, pages, pooled_dev, scale_dev, table, lens, first, stream);
+}
+
+spmm_status_t spmm_execute_attn_pool8(spmm_plan_t p, const spmm_attn_tensor_t *k8, const float *k_scale_dev,
+                                      int64_t pages, int8_t *pooled_dev, float *scale_dev, const int32_t *table,
+                                      const int32_t *lens, const int32_t *first, hipStream_t stream) {
+  return pool("spmm_execute_attn_pool8", p, k8, k_scale_dev, true, pages, pooled_dev, scale_dev, table, lens, first, stream);
 }
 
 spmm_status_t spmm_execute_attn_select(spmm_plan_t p, const spmm_attn_tensor_t *q, const int8_t *pooled_dev,
@@ -474,29 +704,84 @@ spmm_status_t spmm_execute_attn_cache(spmm_plan_t p, const spmm_attn_tensor_t *q
                                       float *lse_dev, const int32_t *table, const int32_t *lists_dev,
                                       const uint64_t *tree, const int32_t *lens, const int32_t *starts,
                                       hipStream_t stream) {
-  const char *fn = "spmm_execute_attn_cache";
+  return cache("spmm_execute_attn_cache", p, q, k, v, nullptr, pages, o, lse_dev, table, lists_dev, tree, lens, starts,
+               stream);
+}
+
+spmm_status_t spmm_execute_attn_cache8(spmm_plan_t p, const spmm_attn_tensor_t *q, const spmm_attn_tensor_t *k8,
+                                       const spmm_attn_tensor_t *v8, const float *k_scale_dev,
+                                       const float *v_scale_dev, int64_t pages, const spmm_attn_tensor_t *o,
+                                       float *lse_dev, const int32_t *table, const int32_t *lists_dev,
+                                       const uint64_t *tree, const int32_t *lens, const int32_t *starts,
+                                       hipStream_t stream) {
+  const AttnScales scales{k_scale_dev, v_scale_dev};
+  return cache("spmm_execute_attn_cache8", p, q, k8, v8, &scales, pages, o, lse_dev, table, lists_dev, tree, lens, starts,
+               stream);
+}
+
+spmm_status_t spmm_execute_attn_write(spmm_plan_t p, const spmm_attn_tensor_t *k, const spmm_attn_tensor_t *v,
+                                      const spmm_attn_tensor_t *k8, const spmm_attn_tensor_t *v8, float *k_scale_dev,
+                                      float *v_scale_dev, int64_t pages, const int32_t *table, const int32_t *lens,
+                                      const int32_t *starts, hipStream_t stream) {
+  return codes("spmm_execute_attn_write", false, p, k, v, k8, v8, k_scale_dev, v_scale_dev, pages, table, lens, starts,
+               stream);
+}
+
+spmm_status_t spmm_execute_attn_read(spmm_plan_t p, const spmm_attn_tensor_t *k8, const spmm_attn_tensor_t *v8,
+                                     const float *k_scale_dev, const float *v_scale_dev, int64_t pages,
+                                     const spmm_attn_tensor_t *k, const spmm_attn_tensor_t *v, const int32_t *table,
+                                     const int32_t *lens, hipStream_t stream) {
+  return codes("spmm_execute_attn_read", true, p, k, v, k8, v8, const_cast<float *>(k_scale_dev),
+               const_cast<float *>(v_scale_dev), pages, table, lens, nullptr, stream);
+}
+
+spmm_status_t spmm_execute_attn_rope(spmm_plan_t p, const spmm_attn_tensor_t *q, const spmm_attn_tensor_t *k,
+                                     const float *q_weight_dev, const float *k_weight_dev,
+                                     const spmm_attn_tensor_t *q_out, const spmm_attn_tensor_t *k_out,
+                                     const int32_t *positions, const int32_t *lens, const int32_t *starts,
+                                     hipStream_t stream) {
+  const char *fn = "spmm_execute_attn_rope";
   return guarded([&]() -> spmm_status_t {
-    ATTN_TRY(attn_plan_of(fn, p));
-    AttnArgs a = p->attn_args;
-    int64_t outer = 0;
-    ATTN_TRY(pages_of(fn, a, table, pages, &outer));
-    ATTN_TRY(forward_args(fn, p, q, k, v, outer, table ? kAttnPage : a.nk, o, true, lse_dev, lens, starts, &a));
-    ATTN_TRY(whole(fn, "table", table, 4, false));
-    ATTN_TRY(whole(fn, "lists", lists_dev, 4, false));
-    ATTN_TRY(whole(fn, "tree", tree, 8, false));
-    if (tree && a.nq > 64) return fail(SPMM_ERR_UNSUPPORTED, std::string(fn) + ": a tree holds at most 64 tokens");
-    if (static_cast<int64_t>(a.b) * a.nq == 0) return SPMM_OK;
-    a.table = table;
-    a.pages = static_cast<int32_t>(pages);
-    a.lists = lists_dev;
-    a.tree = tree;
-    a.entries = lists_dev ? a.max_blocks : a.nkb;
-    const int32_t *split = lists_dev ? p->attn_split_listed : p->attn_split_all;
-    a.nsplit = split[0];
-    a.per_split = split[1];
+    ATTN_TRY(rope_plan_of(fn, p));
+    RopeArgs a = p->rope_args;
+    const int64_t dim = p->rope_desc.dim;
+    ATTN_TRY(rope_args(fn, p, q, k, q_weight_dev, k_weight_dev, positions, lens, starts, true, &a));
+    ATTN_TRY(view(fn, "q_out", q_out, a.b, a.n, a.heads[0], dim, true, false, &a.y[0]));
+    ATTN_TRY(view(fn, "k_out", k_out, a.b, a.n, a.heads[1], dim, true, false, &a.y[1]));
+    if (static_cast<int64_t>(a.b) * a.n == 0) return SPMM_OK;
     DeviceScope ds(p->device);
     if (ds.err != hipSuccess) return hip_fail(ds.err, "hipSetDevice");
-    return launched(launch_attn_forward(a, static_cast<spmm_dtype_t>(p->attn_desc.dtype), p->attn_desc.dim, stream));
+    return launched(launch_rope(a, static_cast<spmm_dtype_t>(p->rope_desc.dtype), p->rope_desc.dim, stream));
+  });
+}
+
+spmm_status_t spmm_execute_attn_rope_backward(spmm_plan_t p, const spmm_attn_tensor_t *q_grad,
+                                              const spmm_attn_tensor_t *k_grad, const spmm_attn_tensor_t *q,
+                                              const spmm_attn_tensor_t *k, const float *q_weight_dev,
+                                              const float *k_weight_dev, const spmm_attn_tensor_t *dq,
+                                              const spmm_attn_tensor_t *dk, float *dq_weight_dev,
+                                              float *dk_weight_dev, const int32_t *positions, const int32_t *lens,
+                                              const int32_t *starts, hipStream_t stream) {
+  const char *fn = "spmm_execute_attn_rope_backward";
+  return guarded([&]() -> spmm_status_t {
+    ATTN_TRY(rope_plan_of(fn, p));
+    if (!p->rope_desc.backward) return bad(fn, "the plan was made without backward");
+    RopeArgs a = p->rope_args;
+    const int64_t dim = p->rope_desc.dim;
+    ATTN_TRY(rope_args(fn, p, q, k, q_weight_dev, k_weight_dev, positions, lens, starts, false, &a));
+    ATTN_TRY(view(fn, "q_grad", q_grad, a.b, a.n, a.heads[0], dim, false, false, &a.g[0]));
+    ATTN_TRY(view(fn, "k_grad", k_grad, a.b, a.n, a.heads[1], dim, false, false, &a.g[1]));
+    ATTN_TRY(view(fn, "dq", dq, a.b, a.n, a.heads[0], dim, true, false, &a.dx[0]));
+    ATTN_TRY(view(fn, "dk", dk, a.b, a.n, a.heads[1], dim, true, false, &a.dx[1]));
+    ATTN_TRY(whole(fn, "dq_weight", dq_weight_dev, 4, q_weight_dev != nullptr));
+    ATTN_TRY(whole(fn, "dk_weight", dk_weight_dev, 4, k_weight_dev != nullptr));
+    if ((dq_weight_dev && !q_weight_dev) || (dk_weight_dev && !k_weight_dev))
+      return bad(fn, "the gradient of a weight that is NULL");
+    a.dw[0] = dq_weight_dev;
+    a.dw[1] = dk_weight_dev;
+    DeviceScope ds(p->device);
+    if (ds.err != hipSuccess) return hip_fail(ds.err, "hipSetDevice");
+    return launched(launch_rope_backward(a, static_cast<spmm_dtype_t>(p->rope_desc.dtype), p->rope_desc.dim, stream));
   });
 }
 

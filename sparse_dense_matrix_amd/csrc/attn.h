@@ -53,8 +53,40 @@ struct AttnArgs {
   float *part_kv;              // [b * hk][slots][2][64][d] partial dk, dv of split key blocks
 };
 
+// Scales of a cache in 8 bits: [slots][hk][64], slot = page or b * nkb + block.
+struct AttnScales {
+  const float *k, *v;
+};
+
+// New tokens to a cache in 8 bits, or the cache back to tensors.
+struct AttnCodesArgs {
+  AttnView k, v;               // [b][nq or nk] tensors of 16 bits
+  AttnView k8, v8;             // pages, or [b][nk]
+  float *k_scale, *v_scale;    // [slots][hk][64]
+  const int32_t *table, *lens, *starts;
+  int32_t b, n, nk, hk, nkb, pages;  // n: tokens of a sequence in k and v
+};
+
+// Norm and rotation of queries and keys, and their gradients.
+struct RopeArgs {
+  AttnView x[2], y[2];         // queries, keys: inputs; outputs
+  AttnView g[2], dx[2];        // gradients of the outputs and of the inputs (backward)
+  const float *w[2];           // [d] weights of the norm, or null: no norm
+  float *dw[2];                // [d] their gradients
+  int32_t heads[2];
+  const double *turns;         // [pairs] turns (of 2 pi) that one position makes
+  const int32_t *axis;         // [pairs] axis whose positions turn the pair
+  const int32_t *positions;    // [axes][b][n], or null: starts + t on every axis
+  const int32_t *lens, *starts;
+  float *part;                 // [grid][2][d] workspace: partial gradients of the weights (backward)
+  int32_t b, n, pairs, axes, interleaved;
+  int32_t grid;                // workgroups of the backward kernel at most
+  float eps;
+};
+
 struct AttnPoolArgs {
   AttnView k;
+  const float *k_scale;        // of a cache in 8 bits: [slots][hk][64]; null: k is 16 bits
   int8_t *pooled;              // [pages or b * nkb][hk][d]
   float *pooled_scale;         // [pages or b * nkb][hk]
   const int32_t *table, *lens, *first;
@@ -118,6 +150,16 @@ void attn_split(int64_t tiles, int32_t tile_rows, int32_t entries, int32_t max_e
 void attn_chunks(int64_t heads, int64_t entries, int32_t nqb, int32_t rows, int32_t nkb, int32_t *chunk, int32_t *slots);
 
 hipError_t launch_attn_forward(const AttnArgs &a, spmm_dtype_t t, int d, hipStream_t s);
+// The ranges' partial sums of launch_attn_forward and launch_attn_cache8.
+hipError_t launch_attn_merge(const AttnArgs &a, spmm_dtype_t t, int d, hipStream_t s);
+hipError_t launch_attn_cache8(const AttnArgs &a, const AttnScales &x, spmm_dtype_t t, int d, hipStream_t s);
+hipError_t launch_attn_write(const AttnCodesArgs &a, spmm_dtype_t t, int d, hipStream_t s);
+hipError_t launch_attn_read(const AttnCodesArgs &a, spmm_dtype_t t, int d, hipStream_t s);
+// Tokens of a workgroup of the rope kernels at a time, and such tiles of `tokens` tokens.
+int rope_tile();
+int64_t rope_tiles(int64_t tokens);
+hipError_t launch_rope(const RopeArgs &a, spmm_dtype_t t, int d, hipStream_t s);
+hipError_t launch_rope_backward(const RopeArgs &a, spmm_dtype_t t, int d, hipStream_t s);
 hipError_t launch_attn_backward(const AttnArgs &a, spmm_dtype_t t, int d, hipStream_t s);
 hipError_t launch_attn_pool(const AttnPoolArgs &a, spmm_dtype_t t, int d, hipStream_t s);
 hipError_t launch_attn_select(const AttnSelectArgs &a, spmm_dtype_t t, int d, hipStream_t s);

@@ -111,6 +111,28 @@ __device__ __forceinline__ float add_halves(float x) {
   return h.lo + h.hi;
 }
 
+// Reductions over aligned groups of N = 8 or 16 lanes: neighbours, pairs, then
+// the mirror images of 8 and 16 lanes, whose partners hold the other half.
+template <int CTRL>
+__device__ __forceinline__ unsigned dpp(unsigned x) {
+  return static_cast<unsigned>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), CTRL, 0xf, 0xf, true));
+}
+template <int N, class F>
+__device__ __forceinline__ unsigned over_lanes(unsigned x, F f) {
+  static_assert(N == 8 || N == 16, "lanes of a row");
+  x = f(x, dpp<0xb1>(x));   // lane ^ 1
+  x = f(x, dpp<0x4e>(x));   // lane ^ 2
+  x = f(x, dpp<0x141>(x));  // 7 - lane
+  if constexpr (N == 16) x = f(x, dpp<0x140>(x));  // 15 - lane
+  return x;
+}
+template <int N>
+__device__ __forceinline__ float sum_lanes(float x) {
+  return __builtin_bit_cast(float, over_lanes<N>(__builtin_bit_cast(unsigned, x), [](unsigned p, unsigned q) {
+    return __builtin_bit_cast(unsigned, __builtin_bit_cast(float, p) + __builtin_bit_cast(float, q));
+  }));
+}
+
 // s_waitcnt vmcnt(n), leaving the other counters alone
 template <int N>
 __device__ __forceinline__ void wait_vm() {

@@ -1,0 +1,339 @@
+// attn_rope.hip -- what queries and keys go through before attention: the norm
+// of each head, then the rotation of pairs of its channels by their position,
+//   y_c = x_c r w_c,  r = (mean_c x_c^2 + eps)^(-1/2),
+//   (o_u, o_v) = (y_u cos a - y_v sin a, y_u sin a + y_v cos a),
+//   a = positions[axis of the pair] * freq of the pair,
+// and the gradients, with g that of o:
+//   (dy_u, dy_v) = (g_u cos a + g_v sin a, g_v cos a - g_u sin a),
+//   dw_c = sum over rows of dy_c x_c r,
+//   dx_c = r (dy_c w_c - x_c r^2 mean_c(dy_c w_c x_c)).
+//
+// An angle is taken in turns, in 64 bits: the fraction of a turn is then good
+// to 2^-24 of a turn at any 32-bit position.  Each token's angles are computed
+// once for all heads, one a thread, and kept in LDS.  Everything else is in 32
+// bits, rounded once at the output.
+#include "attn_dev.h"
+#include "internal.h"
+
+namespace sdm {
+namespace attn {
+namespace {
+
+constexpr int kTile = 4;  // tokens of a workgroup at a time
+
+// Tokens t0 .. t0 + count - 1 of all sequences' tokens in one row.
+struct Tokens {
+  int32_t b[kTile], t[kTile];
+  int32_t live[kTile];
+};
+template <int D>
+struct RopeShared {
+  float cosine[kTile][D / 2], sine[kTile][D / 2];
+  float w[2][D];
+  Tokens tok;
+};
+
+template <int D>
+__device__ __forceinline__ void angles(const RopeArgs &a, RopeShared<D> &sh, int64_t t0, int count) {
+  for (int i = threadIdx.x; i < count * max(a.pairs, 1); i += 256) {
+    const int tt = i / max(a.pairs, 1), p = i % max(a.pairs, 1);
+    const int64_t token = t0 + tt;
+    const int64_t b = token / a.n;
+    const int32_t t = static_cast<int32_t>(token % a.n);
+    const int64_t at = static_cast<int64_t>(a.starts ? a.starts[b] : 0) + t;
+    if (p == 0) {
+      sh.tok.b[tt] = static_cast<int32_t>(b);
+      sh.tok.t[tt] = t;
+      sh.tok.live[tt] = !a.lens || (at >= 0 && at < a.lens[b]);
+    }
+    if (a.pairs > 0) {
+      const double pos = static_cast<double>(
+          a.positions ? a.positions[(static_cast<int64_t>(a.axis[p]) * a.b + b) * a.n + t] : at);
+      const double turns = pos * a.turns[p];
+      float s, c;
+      sincospif(2.0f * static_cast<float>(turns - rint(turns)), &s, &c);
+      sh.cosine[tt][p] = c;
+      sh.sine[tt][p] = s;
+    }
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void load_weights(const RopeArgs &a, RopeShared<D> &sh) {
+  for (int i = threadIdx.x; i < 2 * D; i += 256) {
+    const float *w = a.w[i / D];
+    sh.w[i / D][i % D] = w ? w[i % D] : 1.0f;
+  }
+}
+
+__device__ __forceinline__ char *row_at(const AttnView &v, int32_t b, int32_t t, int32_t h, int lane) {
+  return v.p + b * v.sb + t * v.st + h * v.sh + 16 * lane;
+}
+
+// What a lane needs to turn its eight channels: where its angles and its
+// partner's channels stand.
+struct Turn {
+  int first;    // of the lane's angles (8, or 4 where neighbours are pairs)
+  int partner;  // lane of the row that holds the pairs' other channels
+  bool turned, second;
+};
+template <int D>
+__device__ __forceinline__ Turn turn_of(const RopeArgs &a, int lane) {
+  Turn u;
+  const int half = a.pairs / 8;  // lanes of the first channels
+  if (a.interleaved) {
+    u = {4 * lane, lane, 4 * lane < a.pairs, false};
+  } else {
+    u.second = lane >= half;
+    u.turned = lane < 2 * half;
+    u.first = 8 * (u.second ? lane - half : lane);
+    u.partner = !u.turned ? lane : (u.second ? lane - half : lane + half);
+  }
+  if (!u.turned) u.first = 0;
+  return u;
+}
+
+// x turned by its angles (back: the other way).  `other` are the pairs' other
+// channels where the halves are paired.
+template <int D>
+__device__ __forceinline__ void rotate(const RopeArgs &a, const RopeShared<D> &sh, int tt, const Turn &u, bool back, float *x,
+                                       const float *other) {
+  if (!u.turned) return;
+  const float *c = sh.cosine[tt] + u.first, *s = sh.sine[tt] + u.first;
+  if (a.interleaved) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float sn = back ? -s[i] : s[i], p = x[2 * i], q = x[2 * i + 1];
+      x[2 * i] = p * c[i] - q * sn;
+      x[2 * i + 1] = p * sn + q * c[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = x[i] * c[i] + other[i] * (u.second != back ? s[i] : -s[i]);
+  }
+}
+
+// The partner lane's words.
+template <int D>
+__device__ __forceinline__ u32x4 from_partner(u32x4 v, const Turn &u) {
+  const int from = 4 * ((threadIdx.x & 63 & ~(D / 8 - 1)) + u.partner);
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = static_cast<unsigned>(__builtin_amdgcn_ds_bpermute(from, static_cast<int>(v[i])));
+  return r;
+}
+
+// D / 8 lanes take a row, kU rows' loads in flight; rows of a tile are its
+// tokens times the heads first .. first + heads - 1 of queries and keys in one.
+template <class T, int D>
+__global__ __launch_bounds__(256) void rope_forward(const RopeArgs a, int heads_of, int chunks) {
+  constexpr int kLanes = D / 8, kGroups = 256 / kLanes, kU = 4;
+  __shared__ RopeShared<D> sh;
+  const int64_t tokens = static_cast<int64_t>(a.b) * a.n;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x / chunks) * kTile;
+  const int first = (blockIdx.x % chunks) * heads_of;
+  const int heads = min(heads_of, a.heads[0] + a.heads[1] - first);
+  const int count = static_cast<int>(min(static_cast<int64_t>(kTile), tokens - t0));
+  angles<D>(a, sh, t0, count);
+  load_weights<D>(a, sh);
+  __syncthreads();
+  const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  const Turn u = turn_of<D>(a, lane);
+  for (int r0 = group; r0 < count * heads; r0 += kU * kGroups) {
+    u32x4 v[kU];
+    int tt[kU], h[kU];
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      const int r = r0 + i * kGroups;
+      tt[i] = min(r / heads, kTile - 1);
+      h[i] = r < count * heads && sh.tok.live[tt[i]] ? first + r % heads : -1;
+      if (h[i] < 0) continue;
+      const bool key = h[i] >= a.heads[0];
+      v[i] = *reinterpret_cast<const u32x4 *>(
+          row_at(key ? a.x[1] : a.x[0], sh.tok.b[tt[i]], sh.tok.t[tt[i]], key ? h[i] - a.heads[0] : h[i], lane));
+    }
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      if (h[i] < 0) continue;
+      const bool key = h[i] >= a.heads[0];
+      const u32x4 w = from_partner<D>(v[i], u);
+      float x[8], y[8], sum = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[e] = elem<T>(v[i][e / 2], e & 1);
+        y[e] = elem<T>(w[e / 2], e & 1);
+        sum = __builtin_fmaf(x[e], x[e], sum);
+      }
+      if (a.w[key]) {
+        const float r = rsqrtf(sum_lanes<kLanes>(sum) * (1.0f / D) + a.eps);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          x[e] = x[e] * r * sh.w[key][8 * lane + e];
+          y[e] = y[e] * r * sh.w[key][8 * u.partner + e];
+        }
+      }
+      rotate<D>(a, sh, tt[i], u, false, x, y);
+      u32x4 out;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out[e] = pack2<T>(x[2 * e], x[2 * e + 1]);
+      *reinterpret_cast<u32x4 *>(
+          row_at(key ? a.y[1] : a.y[0], sh.tok.b[tt[i]], sh.tok.t[tt[i]], key ? h[i] - a.heads[0] : h[i], lane)) = out;
+    }
+  }
+}
+
+// Workgroups take tiles in turn; each lane sums the weights' gradients of its
+// channels over its rows, and the workgroup's sums go to the workspace.
+template <class T, int D>
+__global__ __launch_bounds__(256) void rope_backward(const RopeArgs a) {
+  constexpr int kLanes = D / 8, kGroups = 256 / kLanes, kU = 2;
+  __shared__ RopeShared<D> sh;
+  __shared__ float sums[kGroups][D];
+  const int64_t tokens = static_cast<int64_t>(a.b) * a.n;
+  const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  const Turn u = turn_of<D>(a, lane);
+  load_weights<D>(a, sh);
+  float dw[2][8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) dw[0][e] = dw[1][e] = 0.0f;
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTile; t0 < tokens; t0 += static_cast<int64_t>(gridDim.x) * kTile) {
+    const int count = static_cast<int>(min(static_cast<int64_t>(kTile), tokens - t0));
+    __syncthreads();
+    angles<D>(a, sh, t0, count);
+    __syncthreads();
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      const int heads = a.heads[side];
+      const bool norm = a.w[side] != nullptr;
+      for (int r0 = group; r0 < count * heads; r0 += kU * kGroups) {
+        u32x4 gv[kU], xv[kU];
+        int tt[kU], h[kU];
+#pragma unroll
+        for (int i = 0; i < kU; ++i) {
+          const int r = r0 + i * kGroups;
+          tt[i] = min(r / heads, kTile - 1);
+          h[i] = r < count * heads ? r % heads : -1;
+          gv[i] = xv[i] = u32x4{0, 0, 0, 0};
+          if (h[i] < 0 || !sh.tok.live[tt[i]]) continue;
+          gv[i] = *reinterpret_cast<const u32x4 *>(row_at(a.g[side], sh.tok.b[tt[i]], sh.tok.t[tt[i]], h[i], lane));
+          if (norm) xv[i] = *reinterpret_cast<const u32x4 *>(row_at(a.x[side], sh.tok.b[tt[i]], sh.tok.t[tt[i]], h[i], lane));
+        }
+#pragma unroll
+        for (int i = 0; i < kU; ++i) {
+          if (h[i] < 0) continue;
+          const u32x4 w = from_partner<D>(gv[i], u);
+          float dy[8], other[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            dy[e] = elem<T>(gv[i][e / 2], e & 1);
+            other[e] = elem<T>(w[e / 2], e & 1);
+          }
+          rotate<D>(a, sh, tt[i], u, true, dy, other);
+          if (norm) {
+            float x[8], sum = 0.0f, dot = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              x[e] = elem<T>(xv[i][e / 2], e & 1);
+              sum = __builtin_fmaf(x[e], x[e], sum);
+            }
+            const float r = rsqrtf(sum_lanes<kLanes>(sum) * (1.0f / D) + a.eps);
+            if (!sh.tok.live[tt[i]]) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) dy[e] = 0.0f;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                dw[side][e] = __builtin_fmaf(dy[e], x[e] * r, dw[side][e]);
+                dy[e] *= sh.w[side][8 * lane + e];
+                dot = __builtin_fmaf(dy[e], x[e], dot);
+              }
+              const float f = sum_lanes<kLanes>(dot) * (1.0f / D) * r * r;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) dy[e] = r * (dy[e] - x[e] * f);
+            }
+          }
+          u32x4 out;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) out[e] = pack2<T>(dy[2 * e], dy[2 * e + 1]);
+          *reinterpret_cast<u32x4 *>(row_at(a.dx[side], sh.tok.b[tt[i]], sh.tok.t[tt[i]], h[i], lane)) = out;
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int side = 0; side < 2; ++side) {
+    if (!a.dw[side]) continue;
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sums[group][8 * lane + e] = dw[side][e];
+    __syncthreads();
+    if (threadIdx.x < D) {
+      float x = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) x += sums[i][threadIdx.x];
+      a.part[(static_cast<int64_t>(blockIdx.x) * 2 + side) * D + threadIdx.x] = x;
+    }
+  }
+}
+
+// The workgroups' sums, in their order: 32 rows of threads for 8 channels.
+template <int D>
+__global__ __launch_bounds__(256) void rope_weights(const RopeArgs a, int parts) {
+  __shared__ float sums[32][8];
+  const int c = threadIdx.x % 8, row = threadIdx.x / 8;
+  const int at = blockIdx.x * 8 + c, side = at / D;
+  float *to = a.dw[side];
+  if (!to) return;
+  float x = 0.0f;
+#pragma unroll 8
+  for (int i = row; i < parts; i += 32) x += a.part[static_cast<int64_t>(i) * 2 * D + at];
+  sums[row][c] = x;
+  __syncthreads();
+  if (row > 0) return;
+  for (int i = 1; i < 32; ++i) x += sums[i][c];
+  to[at % D] = x;
+}
+
+template <class T, int D>
+hipError_t run_forward(const RopeArgs &a, hipStream_t s) {
+  constexpr int kGroups = 256 / (D / 8);
+  const int64_t tiles = rope_tiles(static_cast<int64_t>(a.b) * a.n);
+  const int heads = a.heads[0] + a.heads[1];
+  // few tokens: their heads go to several workgroups, a row a group of lanes at least
+  int heads_of = heads;
+  while (heads_of * kTile > kGroups && tiles * ((heads + heads_of - 1) / heads_of) < 1024) heads_of = (heads_of + 1) / 2;
+  const int chunks = (heads + heads_of - 1) / heads_of;
+  if (tiles * chunks > 0x7fffffff) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((rope_forward<T, D>), dim3(static_cast<unsigned>(tiles * chunks)), dim3(256), 0, s, a, heads_of, chunks);
+  return hipGetLastError();
+}
+
+template <class T, int D>
+hipError_t run_backward(const RopeArgs &a, hipStream_t s) {
+  const int64_t tiles = rope_tiles(static_cast<int64_t>(a.b) * a.n);
+  const int grid = static_cast<int>(tiles < a.grid ? tiles : a.grid);
+  if (grid > 0) {
+    hipLaunchKernelGGL((rope_backward<T, D>), dim3(grid), dim3(256), 0, s, a);
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  }
+  if (!a.dw[0] && !a.dw[1]) return hipSuccess;
+  hipLaunchKernelGGL((rope_weights<D>), dim3(2 * D / 8), dim3(256), 0, s, a, grid);
+  return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace attn
+
+int rope_tile() { return attn::kTile; }
+int64_t rope_tiles(int64_t tokens) { return (tokens + attn::kTile - 1) / attn::kTile; }
+
+hipError_t launch_rope(const RopeArgs &a, spmm_dtype_t t, int d, hipStream_t s) {
+  if (t == SPMM_BF16) return d == 64 ? attn::run_forward<attn::Bf16, 64>(a, s) : attn::run_forward<attn::Bf16, 128>(a, s);
+  return d == 64 ? attn::run_forward<attn::F16, 64>(a, s) : attn::run_forward<attn::F16, 128>(a, s);
+}
+hipError_t launch_rope_backward(const RopeArgs &a, spmm_dtype_t t, int d, hipStream_t s) {
+  if (t == SPMM_BF16) return d == 64 ? attn::run_backward<attn::Bf16, 64>(a, s) : attn::run_backward<attn::Bf16, 128>(a, s);
+  return d == 64 ? attn::run_backward<attn::F16, 64>(a, s) : attn::run_backward<attn::F16, 128>(a, s);
+}
+
+}  // namespace sdm

@@ -99,6 +99,75 @@ __global__ __launch_bounds__(256) void attn_pool(const AttnPoolArgs a) {
   if (lane == 0) a.pooled_scale[at] = top == 0.0 ? 0.0f : static_cast<float>(top / (127.0 * kept));
 }
 
+// The same from a cache in 8 bits, whose keys are code * scale: a product of 31
+// bits, so that its sums in 64 bits are exact as long as the scales of a block
+// are within 2^16 of one another.  Codes take half the lanes of a row.
+template <int D>
+__global__ __launch_bounds__(256) void attn_pool8(const AttnPoolArgs a) {
+  constexpr int kPieces = D / 16, kStep = 64 / kPieces;
+  const int lane = threadIdx.x & 63;
+  int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int h = item % a.hk;
+  item /= a.hk;
+  const int w = item % a.width;
+  const int64_t b = item / a.width;
+  if (b >= a.b) return;
+  const int32_t len = attn_len(a.lens, b, a.nk);
+  int32_t first = a.first ? a.first[b] : 0;
+  first = first < 0 ? 0 : first;
+  const int64_t id = static_cast<int64_t>(first / kAttnPage) + w;
+  if (id * kAttnPage >= len) return;
+  const int32_t kept = static_cast<int32_t>(min(static_cast<int64_t>(kAttnPage), len - id * kAttnPage));
+  int64_t slot;
+  const char *p;
+  if (a.table) {
+    slot = attn_page(a.table + b * a.nkb, static_cast<int32_t>(id), a.pages);
+    if (slot < 0) return;
+    p = a.k.p + slot * a.k.sb;
+  } else {
+    slot = b * a.nkb + id;
+    p = a.k.p + b * a.k.sb + id * kAttnPage * a.k.st;
+  }
+  p += h * a.k.sh + (lane % kPieces) * 16;
+  const int64_t at = slot * a.hk + h;
+  const float *scale = a.k_scale + at * kAttnPage;
+  constexpr int kRounds = kAttnPage / kStep;
+  u32x4 v[kRounds];
+  float x[kRounds];
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    const int r = i * kStep + lane / kPieces;
+    v[i] = u32x4{0, 0, 0, 0};
+    x[i] = 0.0f;
+    if (r < kept) {
+      v[i] = *reinterpret_cast<const u32x4 *>(p + r * a.k.st);
+      x[i] = scale[r];
+    }
+  }
+  double sum[16];
+#pragma unroll
+  for (int c = 0; c < 16; ++c) sum[c] = 0.0;
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    const double f = x[i];
+#pragma unroll
+    for (int c = 0; c < 16; ++c)
+      sum[c] = fma(static_cast<double>(static_cast<int8_t>(v[i][c / 4] >> (8 * (c % 4)))), f, sum[c]);
+  }
+#pragma unroll
+  for (int m = kPieces; m < 64; m *= 2)
+#pragma unroll
+    for (int c = 0; c < 16; ++c) sum[c] += __shfl_xor(sum[c], m);
+  double top = 0.0;
+#pragma unroll
+  for (int c = 0; c < 16; ++c) top = top_of(top, fabs(sum[c]));
+#pragma unroll
+  for (int m = 1; m < kPieces; m *= 2) top = top_of(top, __shfl_xor(top, m));
+  const u32x2 lo = round8(sum, top), hi = round8(sum + 8, top);
+  if (lane < kPieces) *reinterpret_cast<u32x4 *>(a.pooled + at * D + lane * 16) = u32x4{lo[0], lo[1], hi[0], hi[1]};
+  if (lane == 0) a.pooled_scale[at] = top == 0.0 ? 0.0f : static_cast<float>(top / (127.0 * kept));
+}
+
 // Scores as whole numbers in the same order; what is no number comes lowest.
 __device__ __forceinline__ unsigned ordered(float x) {
   if (x != x) return 0;
@@ -263,7 +332,11 @@ hipError_t run_pool(const AttnPoolArgs &a, hipStream_t s) {
   const int64_t items = static_cast<int64_t>(a.b) * a.width * a.hk;
   if ((items + 3) / 4 > 0x7fffffff) return hipErrorInvalidValue;
   if (items == 0) return hipSuccess;
-  hipLaunchKernelGGL((attn_pool<T, D>), dim3(static_cast<unsigned>((items + 3) / 4)), dim3(256), 0, s, a);
+  const dim3 grid(static_cast<unsigned>((items + 3) / 4));
+  if (a.k_scale)
+    hipLaunchKernelGGL((attn_pool8<D>), grid, dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((attn_pool<T, D>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

@@ -327,6 +327,7 @@ hipError_t launch_sp24(const Sp24Launch &a, hipStream_t s);
 struct spmm_plan_s {
   sdm::Matrix *a = nullptr;
   bool attn = false;   // plan of spmm_plan_attn: no matrix
+  bool rope = false;   // plan of spmm_plan_attn_rope: no matrix
   bool sddmm = false;  // plan of spmm_plan_sddmm rather than spmm_plan
   spmm_dtype_t sddmm_dtype = SPMM_F32;  // element type of X and Y
   int32_t device = 0;
@@ -340,6 +341,8 @@ struct spmm_plan_s {
   sdm::SddmmBcsrLaunch sddb{};
   spmm_attn_desc_t attn_desc{};
   sdm::AttnArgs attn_args{};  // shape and workspace; the executes fill in the rest
+  spmm_rope_desc_t rope_desc{};  // without the caller's arrays
+  sdm::RopeArgs rope_args{};     // shape, tables and workspace
   int32_t attn_split_listed[2] = {1, 0};  // ranges and entries of each: lists
   int32_t attn_split_all[2] = {1, 0};     // ... and every block of a cache
 };
@@ -381,8 +384,12 @@ struct DeviceScope {
 void free_plan(spmm_plan_s *p);
 // hipMalloc of `bytes` of workspace that the plan owns (null for 0 bytes).
 spmm_status_t plan_workspace(spmm_plan_s *p, size_t bytes, void **dst);
+// hipMalloc + copy; the pointer is owned by the plan.
+spmm_status_t upload(spmm_plan_s *p, const void *src, size_t bytes, void **dst);
 bool plan_log_on();
 // Checks an attention descriptor and fills in the plan's shape (no device).
 spmm_status_t attn_shape(const spmm_attn_desc_t &d, spmm_plan_s *p);
+// The same for norm and rotation.
+spmm_status_t rope_shape(const spmm_rope_desc_t &d, spmm_plan_s *p);
 
 }  // namespace sdm
