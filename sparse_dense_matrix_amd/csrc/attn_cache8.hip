@@ -19,6 +19,8 @@ namespace sdm {
 namespace attn {
 namespace {
 
+constexpr int kAhead = 2;  // operands read ahead of their product
+
 // Four codes as a pair of operand words: converted to 32 bits each, where a
 // whole number up to 127 leaves the lower half of the word zero (bf16), or
 // packed exactly (f16).
@@ -89,6 +91,45 @@ struct Form<T, 16> {
   }
 };
 
+// One workgroup's part of the work.  Workgroups go to the XCDs in turn; each
+// XCD takes all key heads of a range one after another, so that what is read of
+// a token is read by one XCD at about one time.
+__device__ __forceinline__ Item item8_of(const AttnArgs &a) {
+  const uint32_t hk = a.hk, n = gridDim.x / hk, i = blockIdx.x;
+  const uint32_t even = n / 8 * 8;  // ranges that go round all XCDs
+  uint32_t item;
+  Item r;
+  if (i < even * hk) {
+    item = i / (8 * hk) * 8 + i % 8;
+    r.h = i % (8 * hk) / 8;
+  } else {
+    item = even + (i - even * hk) % (n - even);
+    r.h = (i - even * hk) / (n - even);
+  }
+  r.rt = item % a.rtiles;
+  item /= a.rtiles;
+  r.split = item % a.nsplit;
+  item /= a.nsplit;
+  r.qb = item % a.nqb;
+  r.b = item / a.nqb;
+  return r;
+}
+
+// The entries that a range takes.  Where every block is read, a sequence's own
+// blocks are dealt evenly to the ranges (four at least): cut by the longest
+// sequence's, 32 sequences of 21.5k of up to 32k keys fill 2.6 rounds of
+// workgroups and take 330 us, dealt evenly 4 shorter ones and 278 us.
+__device__ __forceinline__ Range range8_of(const AttnArgs &a, const Item &it, const Row &r) {
+  Range x = range_of(a, it, r);
+  if (!x.list && a.nsplit > 1) {
+    const int32_t blocks = r.last_key < 0 ? 0 : r.last_key / kAttnPage + 1;
+    const int32_t per = min(a.per_split, max(4, (blocks + a.nsplit - 1) / a.nsplit));
+    x.e0 = it.split * per;
+    x.e1 = min(blocks, x.e0 + per);
+  }
+  return x;
+}
+
 // 32 staged rows of D codes in 16-byte pieces, piece c of row r at piece
 // c ^ f(r).  Rows 2r and 2r + 1 (4r .. 4r + 3 at D = 64) share a 256-byte row
 // of banks; f is such that 16 lanes that read one piece each of rows 0..15, or
@@ -128,22 +169,40 @@ __device__ __forceinline__ void load_lds4(uint32_t lds, i32x4 buf, uint32_t voff
                : "memory", "m0");
 }
 
-// `kept` rows of codes from key `first` of a block on, and their scales, as buffers
-// (zeros past them).
-template <int D>
-__device__ __forceinline__ i32x4 codes_of(const AttnArgs &a, const AttnView &x, const Item &it, int id, int page,
-                                          int32_t first, int32_t kept) {
-  const char *p = x.p + it.h * x.sh;
-  if (a.table)
-    p += page * x.sb + first * x.st;
-  else
-    p += it.b * x.sb + (static_cast<int64_t>(id) * kAttnPage + first) * x.st;
-  return buffer(p, kept > 0 ? static_cast<int32_t>((kept - 1) * x.st + D) : 0);
+// The kernels' first argument, read again: what only the end of a kernel needs
+// would else stay in registers across its loop, with all that was loaded with it.
+__device__ __forceinline__ const AttnArgs &again() {
+  auto p = __builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const AttnArgs *)p;
 }
-__device__ __forceinline__ const float *scales_at(const AttnArgs &a, const float *x, const Item &it, int id, int page,
-                                                  int32_t first) {
-  const int64_t slot = a.table ? page : static_cast<int64_t>(it.b) * a.nkb + id;
-  return x + (slot * a.hk + it.h) * kAttnPage + first;
+
+// Where a head's codes and scales stand: at base + block * step + key * row,
+// `block` its page, or without a table its own number.
+struct Source {
+  const char *codes;
+  const float *scales;
+  int64_t step;
+  int32_t row, scale_step;
+};
+__device__ __forceinline__ Source source_of(const AttnArgs &a, const AttnView &x, const float *scales, const Item &it) {
+  Source s;
+  s.codes = x.p + it.h * x.sh + (a.table ? 0 : it.b * x.sb);
+  s.step = a.table ? x.sb : kAttnPage * x.st;
+  s.row = static_cast<int32_t>(x.st);
+  s.scales = scales + ((a.table ? 0 : static_cast<int64_t>(it.b) * a.nkb) * a.hk + it.h) * kAttnPage;
+  s.scale_step = a.hk * kAttnPage;
+  // in registers of their own: the compiler else keeps all arguments that were
+  // loaded with them across the loop, and spills them
+  asm("s_mov_b64 %0, %1" : "=&s"(s.step) : "s"(s.step));
+  asm("s_mov_b32 %0, %1" : "=&s"(s.row) : "s"(s.row));
+  return s;
+}
+__device__ __forceinline__ const char *codes_at(const Source &s, int block, int32_t first) {
+  return s.codes + block * s.step + first * s.row;
+}
+__device__ __forceinline__ const float *scales_at(const Source &s, int block, int32_t first) {
+  return s.scales + static_cast<int64_t>(block) * s.scale_step + first;
 }
 
 // The scores s of 32 keys from key0 on (each lane's, times ks already) become
@@ -186,6 +245,54 @@ __device__ __forceinline__ void softmax8(const AttnArgs &a, const Row &r, int32_
     st.l += s[e];
   }
 }
+
+// A buffer of `bytes` bytes from p: loads past its end give zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t records(const void *p, int32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, bytes, 0x00020000);
+}
+
+// What O is counted in.  bf16 reaches as far as 32 bits: one.  For f16 a power
+// of two that the largest scale of values so far does not pass, so that a weight
+// times a scale stays below 2^15 in its units; O moves with it, which few tiles
+// ask for.
+__device__ __forceinline__ float largest(float x) {  // of the wave's lanes; NaN and infinity count as 2^100
+  float y = fminf(x, 0x1p100f);
+#pragma unroll
+  for (int m = 1; m < 64; m *= 2) y = fmaxf(y, __shfl_xor(y, m));
+  return y;
+}
+template <class T>
+struct Unit {
+  __device__ __forceinline__ float in(float x) const { return x; }
+  template <int N, class Acc>
+  __device__ __forceinline__ void out(Acc *) const {}
+};
+template <>
+struct Unit<F16> {
+  float top = 0x1p-100f;
+  // what weights are multiplied by: 2^7 / top, for weights of up to 2^8
+  float by = 0x1p107f;
+  template <int N, class Acc>
+  __device__ __forceinline__ void raise(float x, Acc *o) {
+    if (__builtin_amdgcn_readfirstlane(x > top)) {
+      const float next = __builtin_bit_cast(float, (__builtin_bit_cast(unsigned, x) & 0x7f800000u) + 0x00800000u);
+      const float f = top / next;
+      top = next;
+      by = 0x1p7f / next;
+      rescale<N>(f, o);
+    }
+  }
+  __device__ __forceinline__ float in(float x) const { return x * by; }
+  template <int N, class Acc>
+  __device__ __forceinline__ void out(Acc *o) const {
+    rescale<N>(top * 0x1p-7f, o);
+  }
+  template <int N, class Acc>
+  __device__ __forceinline__ static void rescale(float f, Acc *o) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] *= f;
+  }
+};
 
 // Eight weights as the operand of a product with codes, and what their
 // rounding left out (f16 outputs).
@@ -251,9 +358,10 @@ __global__ __launch_bounds__(64 * KW, M == 16 ? 4 : 3) void attn_stream8(const A
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Item it = item_of(a);
+  const Item it = item8_of(a);
   const Row row = row_of<M>(a, it, M, 0, lane);
-  const Range range = range_of(a, it, row);
+  const Range range = range8_of(a, it, row);
+  const Source ksrc = source_of(a, a.k, scales.k, it), vsrc = source_of(a, a.v, scales.v, it);
   const int g = lane / M;
   u32x4 q[D / 8 / F::kGroups];
   {
@@ -271,8 +379,8 @@ __global__ __launch_bounds__(64 * KW, M == 16 ? 4 : 3) void attn_stream8(const A
 #pragma unroll
   for (int i = 0; i < L::kLoads; ++i) {
     const int r = L::load_row(i, lane), c = L::load_byte(i, lane);
-    koff[i] = static_cast<uint32_t>(r * a.k.st + c);
-    voff[i] = static_cast<uint32_t>(r * a.v.st + c);
+    koff[i] = static_cast<uint32_t>(r * ksrc.row + c);
+    voff[i] = static_cast<uint32_t>(r * vsrc.row + c);
   }
   // rows of the transposing reads: the eight keys whose weights a lane holds
   const int i8 = (lane >> 1) & 7;
@@ -294,9 +402,9 @@ __global__ __launch_bounds__(64 * KW, M == 16 ? 4 : 3) void attn_stream8(const A
       const int page = __builtin_amdgcn_readlane(blocks.page, at);
       const int32_t first = (t % kSubs) * 32;
       const int32_t kept = t < tiles ? min(32, row.last_key + 1 - id * kAttnPage - first) : 0;
-      const i32x4 buf = codes_of<D>(a, values ? a.v : a.k, it, id, page, first, kept);
-      const i32x4 sbuf = buffer(reinterpret_cast<const char *>(scales_at(a, values ? scales.v : scales.k, it, id, page, first)),
-                                kept > 0 ? kept * 4 : 0);
+      const Source &x = values ? vsrc : ksrc;
+      const i32x4 buf = buffer(codes_at(x, page, first), kept > 0 ? (kept - 1) * x.row + D : 0);
+      const i32x4 sbuf = buffer(reinterpret_cast<const char *>(scales_at(x, page, first)), kept > 0 ? kept * 4 : 0);
 #pragma unroll
       for (int i = 0; i < L::kLoads; ++i)
         load_lds16(lds_k + (values ? kTile : 0) + i * 1024, buf, values ? voff[i] : koff[i]);
@@ -375,7 +483,7 @@ __global__ __launch_bounds__(64 * KW, M == 16 ? 4 : 3) void attn_stream8(const A
     }
     __syncthreads();
     if (wave > 0) return;
-#pragma unroll
+#pragma unroll 1
     for (int w2 = 1; w2 < KW; ++w2) {
       const float *p = buf + (w2 - 1) * (kFloats + 2) * 64 + lane;
       const float m2 = p[kFloats * 64], l2 = p[(kFloats + 1) * 64];
@@ -389,135 +497,165 @@ __global__ __launch_bounds__(64 * KW, M == 16 ? 4 : 3) void attn_stream8(const A
       st.m = next;
     }
   }
-  store8<T, D, M>(a, it, row, lane, st.m, st.l, o);
+  store8<T, D, M>(again(), it, row, lane, st.m, st.l, o);
 }
 
-// More rows to a list: RW waves of 32 rows share each staged tile of KT keys.
-// The codes are widened once, on their way to LDS, which then holds the tiles
-// that the 16-bit kernel stages; the next tile's codes come in during the
-// products of this one.
-template <class T, int D, int RW, int KT>
-__global__ __launch_bounds__(64 * RW, 2) void attn_forward8(const AttnArgs a, const AttnScales scales) {
+// More rows to a list: RW waves of 32 rows share each staged tile of KT keys,
+// KW groups of them take the tiles in turn.  The codes are widened once, on
+// their way through registers to LDS, which then holds the tiles that the 16-bit
+// kernel stages; the next tile's codes load during this one's products.  A
+// group's first wave brings the scales, and the largest of the values'.
+template <class T, int D, int RW, int KW, int KT>
+__global__ __launch_bounds__(64 * RW * KW, 2) void attn_forward8(const AttnArgs a,
+                                                                                         const AttnScales scales) {
   using L = Tile<D>;
   using F = Form<T, 32>;
   constexpr int kThreads = 64 * RW;
-  constexpr int kHalf = KT * L::kRowBytes, kStage = 2 * kHalf + 2 * KT * 4;
-  constexpr int kPieces = D / 16;                  // 16-byte pieces of codes in a row
+  constexpr int kHalf = KT * L::kRowBytes;
+  constexpr int kPieces = D / 16;                      // 16-byte pieces of codes in a row
   constexpr int kFetch = 2 * KT * kPieces / kThreads;  // of K and V together, a thread's
-  static_assert(kFetch >= 1 && kFetch * kThreads == 2 * KT * kPieces, "pieces of a tile");
-  static_assert(2 * KT <= kThreads, "scales of a tile");
-  constexpr int kSubs = kAttnPage / KT, kE = KT / 2;
+  static_assert(kFetch >= 1 && kFetch * kThreads == 2 * KT * kPieces && KT * kPieces % 64 == 0, "pieces of a tile");
+  constexpr int kSubs = kAttnPage / KT;
+  constexpr int kScales = 2 * KT + 4;  // floats of a stage: K's, V's, the largest of V's
   extern __shared__ __attribute__((aligned(1024))) char lds[];
 
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const Item it = item_of(a);
-  const Row row = row_of(a, it, 32 * RW, 32 * wave, lane);
-  const Range range = range_of(a, it, row);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rw = wave % RW, kw = wave / RW;
+  const Item it = item8_of(a);
+  const Row row = row_of(a, it, 32 * RW, 32 * rw, lane);
+  const Range range = range8_of(a, it, row);
+  const Source ksrc = source_of(a, a.k, scales.k, it), vsrc = source_of(a, a.v, scales.v, it);
+  const bool some = __any(row.live);  // a wave without rows only stages
   u32x4 q[D / 16];
   load_q<D>(a, it, row, lane, q);
+
+  char *tiles_at = lds + kw * 4 * kHalf;  // two stages of K and V
+  float *scales_of = reinterpret_cast<float *>(lds + KW * 4 * kHalf) + kw * 2 * kScales;
+  // a thread's pieces: where they stand in the block, and in the stage (the
+  // second half of the widened piece at ^ 16)
+  uint32_t from[kFetch], to[kFetch];
+#pragma unroll
+  for (int i = 0; i < kFetch; ++i) {
+    const int at = 64 * rw + lane + i * kThreads;
+    const bool values = 64 * rw + i * kThreads >= KT * kPieces;
+    const int r = at / kPieces % KT, p = at % kPieces;
+    from[i] = static_cast<uint32_t>(r * (values ? vsrc.row : ksrc.row) + 16 * p);
+    to[i] = (values ? kHalf : 0) + r * L::kRowBytes + (((2 * p) ^ L::f(r)) << 4);
+  }
 
   f32x16 o[D / 32];
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) o[i] = zero16();
   Stats st;
+  Unit<T> unit;
   const float c = a.scale * kLog2e;
 
   for (int32_t e = range.e0; e < range.e1; e += 64) {
     const Named blocks = named_blocks(range.list, range.table_row, a.pages, e, range.e1, row.last_key, lane);
     const int tiles = blocks.n * kSubs;
+    const int rounds = (tiles + KW - 1) / KW;
     u32x4 codes[kFetch];
-    float scale = 0.0f;
-    // rows past the last key that some row sees count as zeros: what stands
-    // there may be anything
-    auto fetch = [&](int t) {
-      if (t >= tiles) return;
-      const int id = __builtin_amdgcn_readlane(blocks.id, t / kSubs);
-      const int page = __builtin_amdgcn_readlane(blocks.page, t / kSubs);
-      const int32_t first = (t % kSubs) * KT, kept = row.last_key + 1 - id * kAttnPage - first;
+    float ks = 0.0f, vs = 0.0f;
+    // rows past the last key that some row sees are zeros, as are their scales
+    auto fetch = [&](int round) {
+      const int t = round * KW + kw;
+      const int at = t < tiles ? t / kSubs : 0;
+      const int id = __builtin_amdgcn_readlane(blocks.id, at);
+      const int page = __builtin_amdgcn_readlane(blocks.page, at);
+      const int32_t first = (t % kSubs) * KT;
+      const int32_t kept = t < tiles ? min(KT, row.last_key + 1 - id * kAttnPage - first) : 0;
+      const auto kbuf = records(codes_at(ksrc, page, first), kept > 0 ? (kept - 1) * ksrc.row + D : 0);
+      const auto vbuf = records(codes_at(vsrc, page, first), kept > 0 ? (kept - 1) * vsrc.row + D : 0);
 #pragma unroll
       for (int i = 0; i < kFetch; ++i) {
-        const int at = tid + i * kThreads;
-        const bool values = at >= KT * kPieces;
-        const int r = at / kPieces % KT, p = at % kPieces;
-        const AttnView &x = values ? a.v : a.k;
-        const char *src = x.p + it.h * x.sh;
-        src += a.table ? page * x.sb + (first + r) * x.st
-                       : it.b * x.sb + (static_cast<int64_t>(id) * kAttnPage + first + r) * x.st;
-        codes[i] = u32x4{0, 0, 0, 0};
-        if (r < kept) codes[i] = *reinterpret_cast<const u32x4 *>(src + 16 * p);
+        const bool values = 64 * rw + i * kThreads >= KT * kPieces;
+        codes[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(values ? vbuf : kbuf, from[i], 0, 0));
       }
-      if (tid < 2 * KT) {
-        const int r = tid % KT;
-        scale = r < kept ? scales_at(a, tid < KT ? scales.k : scales.v, it, id, page, first)[r] : 0.0f;
+      if (rw == 0) {
+        const int bytes = kept > 0 ? kept * 4 : 0;
+        ks = __builtin_bit_cast(
+            float, __builtin_amdgcn_raw_buffer_load_b32(records(scales_at(ksrc, page, first), bytes), 4 * lane, 0, 0));
+        vs = __builtin_bit_cast(
+            float, __builtin_amdgcn_raw_buffer_load_b32(records(scales_at(vsrc, page, first), bytes), 4 * lane, 0, 0));
       }
     };
-    auto stage = [&](int t) {
-      if (t >= tiles) return;
-      char *to = lds + (t & 1) * kStage;
+    auto stage = [&](int round) {
+      char *dst = tiles_at + (round & 1) * 2 * kHalf;
 #pragma unroll
       for (int i = 0; i < kFetch; ++i) {
-        const int at = tid + i * kThreads;
-        const bool values = at >= KT * kPieces;
-        const int r = at / kPieces % KT, p = at % kPieces;
-        char *dst = to + (values ? kHalf : 0) + r * L::kRowBytes;
-        const u32x4 x = codes[i];
-        const u32x4 lo = values ? widen8<Bf16>(x[0], x[1]) : widen8<T>(x[0], x[1]);
-        const u32x4 hi = values ? widen8<Bf16>(x[2], x[3]) : widen8<T>(x[2], x[3]);
-        *reinterpret_cast<u32x4 *>(dst + (((2 * p) ^ L::f(r)) << 4)) = lo;
-        *reinterpret_cast<u32x4 *>(dst + (((2 * p + 1) ^ L::f(r)) << 4)) = hi;
+        *reinterpret_cast<u32x4 *>(dst + to[i]) = widen8<T>(codes[i][0], codes[i][1]);
+        *reinterpret_cast<u32x4 *>(dst + (to[i] ^ 16)) = widen8<T>(codes[i][2], codes[i][3]);
       }
-      if (tid < 2 * KT) reinterpret_cast<float *>(to + 2 * kHalf)[tid] = scale;
+      if (rw == 0) {
+        float *x = scales_of + (round & 1) * kScales;
+        if (lane < KT) {
+          x[lane] = ks;
+          x[KT + lane] = vs;
+        }
+        if constexpr (T::kNarrow) {
+          const float top = largest(vs);
+          if (lane == 0) x[2 * KT] = top;
+        }
+      }
     };
-    fetch(0);
-    stage(0);
-    fetch(1);
-    for (int t = 0; t < tiles; ++t) {
-      __syncthreads();
-      stage(t + 1);
-      fetch(t + 2);
-      const char *kt = lds + (t & 1) * kStage, *vt = kt + kHalf;
-      const float *ks = reinterpret_cast<const float *>(vt + kHalf), *vs = ks + KT;
+    if (rounds > 0) {
+      fetch(0);
+      stage(0);
+      fetch(1);
+    }
+    for (int round = 0; round < rounds; ++round) {
+      barrier();
+      const char *kt = tiles_at + (round & 1) * 2 * kHalf, *vt = kt + kHalf;
+      const float *xs = scales_of + (round & 1) * kScales;
+      if (round + 1 < rounds) {
+        stage(round + 1);
+        fetch(round + 2);
+      }
+      const int t = round * KW + kw;
+      if (t >= tiles || !some) continue;
       const int32_t key0 = __builtin_amdgcn_readlane(blocks.id, t / kSubs) * kAttnPage + (t % kSubs) * KT;
+      if constexpr (T::kNarrow) unit.template raise<D / 32>(xs[2 * KT], o);
 #pragma unroll
       for (int n = 0; n < KT / 32; ++n) {
         f32x16 acc = zero16();
-#pragma unroll
-        for (int x = 0; x < D / 16; ++x) acc = T::mma(L::operand(kt, 32 * n, x, lane), q[x], acc);
-        float s[16], w[16];
+        auto kx = operands<D / 16, kAhead>([&](int x) { return L::operand(kt, 32 * n, x, lane); });
+        kx.begin();
+        kx.run([&](int x, u32x4 k) { acc = T::mma(k, q[x], acc); });
+        float s[16];
+        const float *x = xs + 32 * n + F::first_key(lane);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const f32x4 x = *reinterpret_cast<const f32x4 *>(ks + 32 * n + F::first_key(lane) + 8 * i);
+          const f32x4 f = *reinterpret_cast<const f32x4 *>(x + 8 * i);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s[4 * i + j] = acc[4 * i + j] * x[j];
+          for (int j = 0; j < 4; ++j) s[4 * i + j] = acc[4 * i + j] * f[j];
         }
+        constexpr int kI = D / 32;
+        auto vx = operands<2 * kI, kAhead>([&](int i) { return L::operand_t(vt, 32 * n + 16 * (i / kI), i % kI, lane); });
+        vx.begin();
         softmax8<T, D, 32>(a, row, key0 + 32 * n, lane, c, s, st, o);
+        u32x4 p[2];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const f32x4 x = *reinterpret_cast<const f32x4 *>(vs + 32 * n + F::first_key(lane) + 8 * i);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) w[4 * i + j] = s[4 * i + j] * x[j];
+          const f32x4 f = *reinterpret_cast<const f32x4 *>(x + KT + 8 * i);
+          p[i / 2][2 * (i % 2)] = pack2<T>(s[4 * i] * unit.in(f[0]), s[4 * i + 1] * unit.in(f[1]));
+          p[i / 2][2 * (i % 2) + 1] = pack2<T>(s[4 * i + 2] * unit.in(f[2]), s[4 * i + 3] * unit.in(f[3]));
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          u32x4 hi, lo;
-          weights8(w + 8 * h, hi, T::kNarrow ? &lo : nullptr);
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            const u32x4 v = L::operand_t(vt, 32 * n + 16 * h, i, lane);
-            o[i] = Bf16::mma(v, hi, o[i]);
-            if constexpr (T::kNarrow) o[i] = Bf16::mma(v, lo, o[i]);
-          }
-        }
+        vx.run([&](int i, u32x4 v) { o[i % kI] = T::mma(v, p[i / kI], o[i % kI]); });
       }
     }
-    // the next entries' first tile goes where the last one may still be read
-    __syncthreads();
+    // the next entries' first tiles go where the last ones may still be read
+    barrier();
   }
 
+  unit.template out<D / 32>(o);
   st.l = add_halves(st.l);
   if (!row.live) st = Stats();
-  store8<T, D, 32>(a, it, row, lane, st.m, st.l, o);
+  if constexpr (KW > 1) {
+    join_groups<D, RW, KW>(lds, wave, lane, st, o);
+    if (kw > 0) return;
+  }
+  store8<T, D, 32>(again(), it, row, lane, st.m, st.l, o);
 }
 
 int64_t grid_of(const AttnArgs &a) {
@@ -535,12 +673,15 @@ hipError_t run_stream8(const AttnArgs &a, const AttnScales &x, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <class T, int D, int RW, int KT>
+template <class T, int D, int RW, int KW, int KT>
 hipError_t run_forward8(const AttnArgs &a, const AttnScales &x, hipStream_t s) {
-  constexpr size_t kLds = 2 * (static_cast<size_t>(4) * KT * D + 8 * KT);
-  hipError_t e = allow_dynamic_lds(reinterpret_cast<const void *>(&attn_forward8<T, D, RW, KT>), kLds);
+  constexpr size_t kTiles = KW * (static_cast<size_t>(8) * KT * D + 2 * (2 * KT + 4) * 4);
+  constexpr size_t kSums = static_cast<size_t>(KW - 1) * RW * (D / 2 + 2) * 256;
+  constexpr size_t kLds = kTiles > kSums ? kTiles : kSums;
+  hipError_t e = allow_dynamic_lds(reinterpret_cast<const void *>(&attn_forward8<T, D, RW, KW, KT>), kLds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((attn_forward8<T, D, RW, KT>), dim3(static_cast<unsigned>(grid_of(a))), dim3(64 * RW), kLds, s, a, x);
+  hipLaunchKernelGGL((attn_forward8<T, D, RW, KW, KT>), dim3(static_cast<unsigned>(grid_of(a))), dim3(64 * RW * KW), kLds, s,
+                     a, x);
   return hipGetLastError();
 }
 
@@ -559,9 +700,10 @@ hipError_t run8(const AttnArgs &a, const AttnScales &x, spmm_dtype_t t, hipStrea
         e = alone ? run_stream8<T, D, 32, 1>(a, x, s) : run_stream8<T, D, 32, 4>(a, x, s);
       break;
     }
-    case 2: e = run_forward8<T, D, 2, 32>(a, x, s); break;
-    case 4: e = run_forward8<T, D, 4, 32>(a, x, s); break;
-    default: e = run_forward8<T, D, 8, 64>(a, x, s); break;
+    case 2: e = run_forward8<T, D, 2, 2, 32>(a, x, s); break;
+    // up to a workgroup a CU, two groups of waves share its list
+    case 4: e = grid_of(a) <= kCus ? run_forward8<T, D, 4, 2, 32>(a, x, s) : run_forward8<T, D, 4, 1, 32>(a, x, s); break;
+    default: e = run_forward8<T, D, 8, 1, 64>(a, x, s); break;
   }
   return e != hipSuccess || a.nsplit == 1 ? e : launch_attn_merge(a, t, D, s);
 }
