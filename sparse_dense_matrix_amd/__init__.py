@@ -13,7 +13,6 @@ from __future__ import annotations
 
 import ctypes as C
 import os
-import struct
 
 import numpy as np
 
@@ -496,12 +495,20 @@ def _attn_expect(d: AttnDesc, device: int) -> dict:
         "new": ((b, nq, hk, dim), t)}}
 
 
-_pack_tensor = struct.Struct("=4q").pack
 _raw_stream = None
+_bind = None
 
 # Marshalling of the attention calls: each tensor is checked against the plan
-# (a few attribute reads, no objects made: the smallest calls take as long as
-# their marshalling), then goes as a pointer, a tensor of heads with strides.
+# (in csrc/binding.cpp: the smallest calls take as long as their marshalling),
+# then goes as a pointer, a tensor of heads with strides.
+
+
+def _load_binding():
+    global _bind
+    import torch  # noqa: F401
+    from . import _binding
+    _bind = _binding
+    return _bind
 
 
 def _attn_want(plan: Plan) -> dict:
@@ -521,23 +528,22 @@ def _refuse(name: str, t, shape, dtype, device):
 
 def _heads(name: str, t, want, device):
     """A tensor of heads: its strides go along."""
-    shape, dtype = want
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
-        _refuse(name, t, shape, dtype, device)
-    sb, st, sh, sd = t.stride()
-    if sd != 1 and t.numel():
-        raise ValueError(f"{name}: the elements of a head must be consecutive")
-    return _pack_tensor(t.data_ptr(), sb, st, sh)
+    r = (_bind or _load_binding()).heads(t, want, device)
+    if r:
+        return r
+    if r is None:
+        _refuse(name, t, *want, device)
+    raise ValueError(f"{name}: the elements of a head must be consecutive")
 
 
 def _flat(name: str, t, want, device):
     """A contiguous tensor."""
-    shape, dtype = want
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
-        _refuse(name, t, shape, dtype, device)
-    if not t.is_contiguous():
+    r = (_bind or _load_binding()).flat(t, want, device)
+    if r is None:
+        _refuse(name, t, *want, device)
+    if r is False:
         raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    return r
 
 
 def _opt(name: str, t, want, device):

@@ -10,6 +10,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libspmm.so")
+BINDING = os.path.join(HERE, "_binding.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["api.cpp", "pack.cpp", "bcsr_bf16.hip", "wcsr_f32.hip", "sp24.hip", "sddmm_csr.hip", "sddmm_bcsr.hip",
@@ -44,6 +45,28 @@ def _compile(src: str, verbose: bool, extra=(), build_dir: str = BUILD_DIR) -> s
     if out.strip() and verbose:
         print(out)
     return obj
+
+
+def build_binding(verbose: bool = False) -> str:
+    """Compile the Python module that checks tensors (host code only)."""
+    import sysconfig
+
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
+    for d in (os.path.join(os.path.dirname(torch.__file__), "include"),
+              os.path.join(os.path.dirname(torch.__file__), "include", "torch", "csrc", "api", "include"),
+              sysconfig.get_paths()["include"]):
+        cmd += ["-isystem", d]
+    cmd += [os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10",
+            f"-Wl,-rpath,{libs}"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build(verbose: bool = False, out: str = LIB, build_dir: str = BUILD_DIR) -> str:
@@ -108,3 +131,4 @@ if __name__ == "__main__":
         print(build_sanitized(verbose="-v" in sys.argv))
     else:
         print(build(verbose="-v" in sys.argv))
+        print(build_binding(verbose="-v" in sys.argv))

@@ -295,14 +295,15 @@ spmm_status_t rope_shape(const spmm_rope_desc_t &d, spmm_plan_s *p) {
   a.axes = d.axes;
   a.interleaved = d.interleaved;
   a.eps = d.eps;
-  const int64_t tiles = rope_tiles(d.batch * d.tokens);
-  // four workgroups a CU take the tiles in turn, so that each leaves one sum
+  // tiles of four tokens, which four workgroups a CU take in turn, so that each
+  // leaves one sum
+  const int64_t tiles = (d.batch * d.tokens + 3) / 4;
   a.grid = static_cast<int32_t>(std::min<int64_t>(tiles, 1024));
   p->info.format = SPMM_FORMAT_ROPE;
   p->info.m = d.batch * d.tokens;
   p->info.k = d.heads_q + d.heads_kv;
   p->info.n = d.dim;
-  p->info.tile_m = static_cast<int32_t>(rope_tile());
+  p->info.tile_m = 4;
   p->info.tile_n = d.dim;
   p->info.grid = tiles;
   return SPMM_OK;

@@ -155,9 +155,6 @@ hipError_t launch_attn_merge(const AttnArgs &a, spmm_dtype_t t, int d, hipStream
 hipError_t launch_attn_cache8(const AttnArgs &a, const AttnScales &x, spmm_dtype_t t, int d, hipStream_t s);
 hipError_t launch_attn_write(const AttnCodesArgs &a, spmm_dtype_t t, int d, hipStream_t s);
 hipError_t launch_attn_read(const AttnCodesArgs &a, spmm_dtype_t t, int d, hipStream_t s);
-// Tokens of a workgroup of the rope kernels at a time, and such tiles of `tokens` tokens.
-int rope_tile();
-int64_t rope_tiles(int64_t tokens);
 hipError_t launch_rope(const RopeArgs &a, spmm_dtype_t t, int d, hipStream_t s);
 hipError_t launch_rope_backward(const RopeArgs &a, spmm_dtype_t t, int d, hipStream_t s);
 hipError_t launch_attn_backward(const AttnArgs &a, spmm_dtype_t t, int d, hipStream_t s);

@@ -42,6 +42,9 @@ __device__ __forceinline__ u32x4 widen8(unsigned lo, unsigned hi) {
   return u32x4{a[0], a[1], b[0], b[1]};
 }
 
+template <int M>
+using Scores = float __attribute__((ext_vector_type(M / 2)));  // a lane's, of 32 keys
+
 // Products for row tiles of M = 32 or 16 query rows.  Scores of 32 keys: a lane
 // holds row lane % M and 32 M / 64 keys.  O^T: floats i of a lane come in
 // groups of four consecutive elements of the head.
@@ -91,21 +94,12 @@ struct Form<T, 16> {
   }
 };
 
-// One workgroup's part of the work.  Workgroups go to the XCDs in turn; each
-// XCD takes all key heads of a range one after another, so that what is read of
-// a token is read by one XCD at about one time.
+// One workgroup's part of the work: all key heads of a range after one another
+// on one XCD.
 __device__ __forceinline__ Item item8_of(const AttnArgs &a) {
-  const uint32_t hk = a.hk, n = gridDim.x / hk, i = blockIdx.x;
-  const uint32_t even = n / 8 * 8;  // ranges that go round all XCDs
   uint32_t item;
   Item r;
-  if (i < even * hk) {
-    item = i / (8 * hk) * 8 + i % 8;
-    r.h = i % (8 * hk) / 8;
-  } else {
-    item = even + (i - even * hk) % (n - even);
-    r.h = (i - even * hk) / (n - even);
-  }
+  r.h = head_of(blockIdx.x, gridDim.x / a.hk, a.hk, &item);
   r.rt = item % a.rtiles;
   item /= a.rtiles;
   r.split = item % a.nsplit;
@@ -207,10 +201,11 @@ __device__ __forceinline__ const float *scales_at(const Source &s, int block, in
 
 // The scores s of 32 keys from key0 on (each lane's, times ks already) become
 // weights, and o, m and l move with the maximum.
-template <class T, int D, int M, int E, class Acc>
-__device__ __forceinline__ void softmax8(const AttnArgs &a, const Row &r, int32_t key0, int lane, float c, float (&s)[E],
-                                         Stats &st, Acc *o) {
+template <class T, int D, int M, class Acc>
+__device__ __forceinline__ void softmax8(const AttnArgs &a, const Row &r, int32_t key0, int lane, float c,
+                                         Scores<M> &s, Stats &st, Acc *o) {
   using F = Form<T, M>;
+  constexpr int E = M / 2;
   if (key0 + 32 > r.open) {
     if (a.tree) {
       const int32_t before = r.start - (key0 + F::first_key(lane));  // keys of the text
@@ -345,7 +340,7 @@ __device__ __forceinline__ void store8(const AttnArgs &a, const Item &it, const 
 // softmax and the product with the values, the next of values during the
 // scores.  KW waves share a list's tiles and join their sums.
 template <class T, int D, int M, int KW>
-__global__ __launch_bounds__(64 * KW, M == 16 ? 4 : 3) void attn_stream8(const AttnArgs a, const AttnScales scales) {
+__global__ __launch_bounds__(64 * KW, M == 16 ? 4 : 2) void attn_stream8(const AttnArgs a, const AttnScales scales) {
   using F = Form<T, M>;
   using V = Form<Bf16, M>;
   using L = Codes<D>;
@@ -417,7 +412,8 @@ __global__ __launch_bounds__(64 * KW, M == 16 ? 4 : 3) void attn_stream8(const A
     for (int t = wave; t < tiles; t += KW) {
       const int32_t key0 = __builtin_amdgcn_readlane(blocks.id, t / kSubs) * kAttnPage + (t % kSubs) * 32;
       wait_vm<kLoads>();
-      float s[kE], w[kE];
+      Scores<M> s;
+      float w[kE];
 #pragma unroll
       for (int i = 0; i < kE / 4; ++i) {
         const f32x4 x = *reinterpret_cast<const f32x4 *>(ks + 4 * (F::first_key(lane) + F::key(4 * i)));
@@ -622,7 +618,7 @@ __global__ __launch_bounds__(64 * RW * KW, 2) void attn_forward8(const AttnArgs 
         auto kx = operands<D / 16, kAhead>([&](int x) { return L::operand(kt, 32 * n, x, lane); });
         kx.begin();
         kx.run([&](int x, u32x4 k) { acc = T::mma(k, q[x], acc); });
-        float s[16];
+        Scores<32> s;
         const float *x = xs + 32 * n + F::first_key(lane);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {

@@ -111,6 +111,21 @@ __device__ __forceinline__ float add_halves(float x) {
   return h.lo + h.hi;
 }
 
+// Workgroup i of n * heads as a head and one of n items.  Workgroups go to the
+// XCDs in turn; each XCD takes all heads of an item one after another, so that
+// what stands side by side of a token is read and written by one XCD at about one
+// time.
+__device__ __forceinline__ uint32_t head_of(uint32_t i, uint32_t n, uint32_t heads, uint32_t *item) {
+  const uint32_t even = n / 8 * 8;  // items that go round all XCDs
+  if (i < even * heads) {
+    *item = i / (8 * heads) * 8 + i % 8;
+    return i % (8 * heads) / 8;
+  }
+  i -= even * heads;
+  *item = even + i % (n - even);
+  return i / (n - even);
+}
+
 // Reductions over aligned groups of N = 8 or 16 lanes: neighbours, pairs, then
 // the mirror images of 8 and 16 lanes, whose partners hold the other half.
 template <int CTRL>

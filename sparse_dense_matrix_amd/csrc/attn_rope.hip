@@ -19,32 +19,29 @@ namespace sdm {
 namespace attn {
 namespace {
 
-constexpr int kTile = 4;  // tokens of a workgroup at a time
+constexpr int64_t kRopeRows = 1 << 16;
+constexpr int kTile = 4;  // tokens of a workgroup of the backward kernel at a time
 
-// Tokens t0 .. t0 + count - 1 of all sequences' tokens in one row.
-struct Tokens {
-  int32_t b[kTile], t[kTile];
-  int32_t live[kTile];
-};
-template <int D>
+// TOK tokens from t0 of all sequences' tokens in one row: place and whether they
+// count, and the angles of their pairs.
+template <int D, int TOK>
 struct RopeShared {
-  float cosine[kTile][D / 2], sine[kTile][D / 2];
+  float cosine[TOK][D / 2], sine[TOK][D / 2];
   float w[2][D];
-  Tokens tok;
+  int32_t b[TOK], t[TOK], live[TOK];
 };
 
-template <int D>
-__device__ __forceinline__ void angles(const RopeArgs &a, RopeShared<D> &sh, int64_t t0, int count) {
-  for (int i = threadIdx.x; i < count * max(a.pairs, 1); i += 256) {
-    const int tt = i / max(a.pairs, 1), p = i % max(a.pairs, 1);
-    const int64_t token = t0 + tt;
-    const int64_t b = token / a.n;
-    const int32_t t = static_cast<int32_t>(token % a.n);
+template <int D, int TOK>
+__device__ __forceinline__ void angles(const RopeArgs &a, RopeShared<D, TOK> &sh, uint32_t t0, uint32_t count) {
+  const uint32_t pairs = max(a.pairs, 1), n = a.n;
+  for (uint32_t i = threadIdx.x; i < count * pairs; i += 256) {
+    const uint32_t tt = i / pairs, p = i % pairs;
+    const uint32_t b = (t0 + tt) / n, t = (t0 + tt) % n;
     const int64_t at = static_cast<int64_t>(a.starts ? a.starts[b] : 0) + t;
     if (p == 0) {
-      sh.tok.b[tt] = static_cast<int32_t>(b);
-      sh.tok.t[tt] = t;
-      sh.tok.live[tt] = !a.lens || (at >= 0 && at < a.lens[b]);
+      sh.b[tt] = static_cast<int32_t>(b);
+      sh.t[tt] = static_cast<int32_t>(t);
+      sh.live[tt] = !a.lens || (at >= 0 && at < a.lens[b]);
     }
     if (a.pairs > 0) {
       const double pos = static_cast<double>(
@@ -58,8 +55,8 @@ __device__ __forceinline__ void angles(const RopeArgs &a, RopeShared<D> &sh, int
   }
 }
 
-template <int D>
-__device__ __forceinline__ void load_weights(const RopeArgs &a, RopeShared<D> &sh) {
+template <int D, int TOK>
+__device__ __forceinline__ void load_weights(const RopeArgs &a, RopeShared<D, TOK> &sh) {
   for (int i = threadIdx.x; i < 2 * D; i += 256) {
     const float *w = a.w[i / D];
     sh.w[i / D][i % D] = w ? w[i % D] : 1.0f;
@@ -93,23 +90,38 @@ __device__ __forceinline__ Turn turn_of(const RopeArgs &a, int lane) {
   return u;
 }
 
+// A lane's cosines and sines of one token: of its first 4 pairs where neighbours
+// are pairs, else of 8.
+struct Angles {
+  float c[8], s[8];
+};
+template <int D, int TOK>
+__device__ __forceinline__ Angles angles_of(const RopeArgs &a, const RopeShared<D, TOK> &sh, int tt, const Turn &u) {
+  Angles x;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const bool there = u.turned && (i < 4 || !a.interleaved);
+    x.c[i] = there ? sh.cosine[tt][u.first + i] : 1.0f;
+    x.s[i] = there ? sh.sine[tt][u.first + i] : 0.0f;
+  }
+  return x;
+}
+
 // x turned by its angles (back: the other way).  `other` are the pairs' other
 // channels where the halves are paired.
-template <int D>
-__device__ __forceinline__ void rotate(const RopeArgs &a, const RopeShared<D> &sh, int tt, const Turn &u, bool back, float *x,
+__device__ __forceinline__ void rotate(const RopeArgs &a, const Angles &w, const Turn &u, bool back, float *x,
                                        const float *other) {
   if (!u.turned) return;
-  const float *c = sh.cosine[tt] + u.first, *s = sh.sine[tt] + u.first;
   if (a.interleaved) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float sn = back ? -s[i] : s[i], p = x[2 * i], q = x[2 * i + 1];
-      x[2 * i] = p * c[i] - q * sn;
-      x[2 * i + 1] = p * sn + q * c[i];
+      const float sn = back ? -w.s[i] : w.s[i], p = x[2 * i], q = x[2 * i + 1];
+      x[2 * i] = p * w.c[i] - q * sn;
+      x[2 * i + 1] = p * sn + q * w.c[i];
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = x[i] * c[i] + other[i] * (u.second != back ? s[i] : -s[i]);
+    for (int i = 0; i < 8; ++i) x[i] = x[i] * w.c[i] + other[i] * (u.second != back ? w.s[i] : -w.s[i]);
   }
 }
 
@@ -123,61 +135,112 @@ __device__ __forceinline__ u32x4 from_partner(u32x4 v, const Turn &u) {
   return r;
 }
 
-// D / 8 lanes take a row, kU rows' loads in flight; rows of a tile are its
-// tokens times the heads first .. first + heads - 1 of queries and keys in one.
+// A lane's eight channels of a row, normed where there is a weight (w: of the
+// lane's channels, w2: of its partner's) and turned.
 template <class T, int D>
-__global__ __launch_bounds__(256) void rope_forward(const RopeArgs a, int heads_of, int chunks) {
-  constexpr int kLanes = D / 8, kGroups = 256 / kLanes, kU = 4;
-  __shared__ RopeShared<D> sh;
-  const int64_t tokens = static_cast<int64_t>(a.b) * a.n;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x / chunks) * kTile;
-  const int first = (blockIdx.x % chunks) * heads_of;
-  const int heads = min(heads_of, a.heads[0] + a.heads[1] - first);
-  const int count = static_cast<int>(min(static_cast<int64_t>(kTile), tokens - t0));
+__device__ __forceinline__ u32x4 turned(const RopeArgs &a, u32x4 v, bool norm, const float *w, const float *w2,
+                                        const Angles &turn, const Turn &u) {
+  const u32x4 p = from_partner<D>(v, u);
+  float x[8], y[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    x[e] = elem<T>(v[e / 2], e & 1);
+    y[e] = elem<T>(p[e / 2], e & 1);
+  }
+  if (norm) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum = __builtin_fmaf(x[e], x[e], sum);
+    const float r = rsqrtf(sum_lanes<D / 8>(sum) * (1.0f / D) + a.eps);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[e] = x[e] * r * w[e];
+      y[e] = y[e] * r * w2[e];
+    }
+  }
+  rotate(a, turn, u, false, x, y);
+  u32x4 out;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) out[e] = pack2<T>(x[2 * e], x[2 * e + 1]);
+  return out;
+}
+
+// Few rows: D / 8 lanes take one each, all heads of a token after one another.
+// Bound by its chain of loads and steps; the row loads before the angles are
+// computed.
+template <class T, int D>
+__global__ __launch_bounds__(256) void rope_rows(const RopeArgs a) {
+  constexpr int kLanes = D / 8, kGroups = 256 / kLanes;
+  __shared__ RopeShared<D, kGroups / 2 + 1> sh;  // two heads at least
+  const uint32_t heads = a.heads[0] + a.heads[1], tokens = static_cast<uint32_t>(a.b) * a.n;
+  const uint32_t r0 = blockIdx.x * kGroups, t0 = r0 / heads;  // few rows: below 2^32
+  const uint32_t count = min((r0 + kGroups - 1) / heads + 1, tokens) - t0;
+  const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  const uint32_t r = min(r0 + group, tokens * heads - 1), token = r / heads;
+  const int32_t hh = r % heads, b = token / a.n, t = token % a.n;
+  const bool key = hh >= a.heads[0];
+  const int32_t h = key ? hh - a.heads[0] : hh;
+  const u32x4 v = *reinterpret_cast<const u32x4 *>(row_at(key ? a.x[1] : a.x[0], b, t, h, lane));
   angles<D>(a, sh, t0, count);
   load_weights<D>(a, sh);
   __syncthreads();
-  const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  const int tt = token - t0;
+  if (r0 + group >= tokens * heads || !sh.live[tt]) return;
   const Turn u = turn_of<D>(a, lane);
-  for (int r0 = group; r0 < count * heads; r0 += kU * kGroups) {
-    u32x4 v[kU];
-    int tt[kU], h[kU];
+  const u32x4 out = turned<T, D>(a, v, a.w[key] != nullptr, sh.w[key] + 8 * lane, sh.w[key] + 8 * u.partner,
+                                 angles_of<D>(a, sh, tt, u), u);
+  *reinterpret_cast<u32x4 *>(row_at(key ? a.y[1] : a.y[0], b, t, h, lane)) = out;
+}
+
+// More rows: a token has 256 / (D / 8) / TOK groups of D / 8 lanes, which take its
+// heads in turn, so that a lane keeps its token's angles and its channels'
+// weights; the next rows load while rows are turned.  16k tokens of 32 and 8
+// heads: 67 us, 5.0 TB/s (a row at a time with its heads counted out by divisions:
+// 123 us).
+template <class T, int D, int TOK>
+__global__ __launch_bounds__(256) void rope_forward(const RopeArgs a) {
+  constexpr int kLanes = D / 8, kGroups = 256 / kLanes, kOf = kGroups / TOK, kU = 4;
+  __shared__ RopeShared<D, TOK> sh;
+  const uint32_t tokens = static_cast<uint32_t>(a.b) * a.n, t0 = blockIdx.x * TOK;
+  const uint32_t count = min(static_cast<uint32_t>(TOK), tokens - t0);
+  const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  const int tt = group / kOf, sub = group % kOf;
+  const uint32_t token = t0 + min(static_cast<uint32_t>(tt), count - 1);
+  const int32_t b = token / a.n, t = token % a.n;
+  angles<D>(a, sh, t0, count);
+  load_weights<D>(a, sh);
+  __syncthreads();
+  if (tt >= static_cast<int>(count) || !sh.live[tt]) return;
+  const Turn u = turn_of<D>(a, lane);
+  const Angles turn = angles_of<D>(a, sh, tt, u);
 #pragma unroll
-    for (int i = 0; i < kU; ++i) {
-      const int r = r0 + i * kGroups;
-      tt[i] = min(r / heads, kTile - 1);
-      h[i] = r < count * heads && sh.tok.live[tt[i]] ? first + r % heads : -1;
-      if (h[i] < 0) continue;
-      const bool key = h[i] >= a.heads[0];
-      v[i] = *reinterpret_cast<const u32x4 *>(
-          row_at(key ? a.x[1] : a.x[0], sh.tok.b[tt[i]], sh.tok.t[tt[i]], key ? h[i] - a.heads[0] : h[i], lane));
+  for (int side = 0; side < 2; ++side) {
+    const AttnView &from = a.x[side], &to = a.y[side];
+    const int heads = a.heads[side];
+    const bool norm = a.w[side] != nullptr;
+    float w[8], w2[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      w[e] = sh.w[side][8 * lane + e];
+      w2[e] = sh.w[side][8 * u.partner + e];
     }
+    u32x4 v[kU], next[kU];
+    auto load = [&](int h0, u32x4 *to_regs) {
 #pragma unroll
-    for (int i = 0; i < kU; ++i) {
-      if (h[i] < 0) continue;
-      const bool key = h[i] >= a.heads[0];
-      const u32x4 w = from_partner<D>(v[i], u);
-      float x[8], y[8], sum = 0.0f;
+      for (int i = 0; i < kU; ++i)
+        if (h0 + i * kOf < heads) to_regs[i] = *reinterpret_cast<const u32x4 *>(row_at(from, b, t, h0 + i * kOf, lane));
+    };
+    load(sub, v);
+    for (int h0 = sub; h0 < heads; h0 += kU * kOf) {
+      load(h0 + kU * kOf, next);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[e] = elem<T>(v[i][e / 2], e & 1);
-        y[e] = elem<T>(w[e / 2], e & 1);
-        sum = __builtin_fmaf(x[e], x[e], sum);
+      for (int i = 0; i < kU; ++i) {
+        const int h = h0 + i * kOf;
+        if (h >= heads) break;
+        *reinterpret_cast<u32x4 *>(row_at(to, b, t, h, lane)) = turned<T, D>(a, v[i], norm, w, w2, turn, u);
       }
-      if (a.w[key]) {
-        const float r = rsqrtf(sum_lanes<kLanes>(sum) * (1.0f / D) + a.eps);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[e] = x[e] * r * sh.w[key][8 * lane + e];
-          y[e] = y[e] * r * sh.w[key][8 * u.partner + e];
-        }
-      }
-      rotate<D>(a, sh, tt[i], u, false, x, y);
-      u32x4 out;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) out[e] = pack2<T>(x[2 * e], x[2 * e + 1]);
-      *reinterpret_cast<u32x4 *>(
-          row_at(key ? a.y[1] : a.y[0], sh.tok.b[tt[i]], sh.tok.t[tt[i]], key ? h[i] - a.heads[0] : h[i], lane)) = out;
+      for (int i = 0; i < kU; ++i) v[i] = next[i];
     }
   }
 }
@@ -187,7 +250,7 @@ __global__ __launch_bounds__(256) void rope_forward(const RopeArgs a, int heads_
 template <class T, int D>
 __global__ __launch_bounds__(256) void rope_backward(const RopeArgs a) {
   constexpr int kLanes = D / 8, kGroups = 256 / kLanes, kU = 2;
-  __shared__ RopeShared<D> sh;
+  __shared__ RopeShared<D, kTile> sh;
   __shared__ float sums[kGroups][D];
   const int64_t tokens = static_cast<int64_t>(a.b) * a.n;
   const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
@@ -199,7 +262,7 @@ __global__ __launch_bounds__(256) void rope_backward(const RopeArgs a) {
   for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTile; t0 < tokens; t0 += static_cast<int64_t>(gridDim.x) * kTile) {
     const int count = static_cast<int>(min(static_cast<int64_t>(kTile), tokens - t0));
     __syncthreads();
-    angles<D>(a, sh, t0, count);
+    angles<D>(a, sh, static_cast<uint32_t>(t0), count);
     __syncthreads();
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
@@ -214,9 +277,9 @@ __global__ __launch_bounds__(256) void rope_backward(const RopeArgs a) {
           tt[i] = min(r / heads, kTile - 1);
           h[i] = r < count * heads ? r % heads : -1;
           gv[i] = xv[i] = u32x4{0, 0, 0, 0};
-          if (h[i] < 0 || !sh.tok.live[tt[i]]) continue;
-          gv[i] = *reinterpret_cast<const u32x4 *>(row_at(a.g[side], sh.tok.b[tt[i]], sh.tok.t[tt[i]], h[i], lane));
-          if (norm) xv[i] = *reinterpret_cast<const u32x4 *>(row_at(a.x[side], sh.tok.b[tt[i]], sh.tok.t[tt[i]], h[i], lane));
+          if (h[i] < 0 || !sh.live[tt[i]]) continue;
+          gv[i] = *reinterpret_cast<const u32x4 *>(row_at(a.g[side], sh.b[tt[i]], sh.t[tt[i]], h[i], lane));
+          if (norm) xv[i] = *reinterpret_cast<const u32x4 *>(row_at(a.x[side], sh.b[tt[i]], sh.t[tt[i]], h[i], lane));
         }
 #pragma unroll
         for (int i = 0; i < kU; ++i) {
@@ -228,7 +291,7 @@ __global__ __launch_bounds__(256) void rope_backward(const RopeArgs a) {
             dy[e] = elem<T>(gv[i][e / 2], e & 1);
             other[e] = elem<T>(w[e / 2], e & 1);
           }
-          rotate<D>(a, sh, tt[i], u, true, dy, other);
+          rotate(a, angles_of<D>(a, sh, tt[i], u), u, true, dy, other);
           if (norm) {
             float x[8], sum = 0.0f, dot = 0.0f;
 #pragma unroll
@@ -237,7 +300,7 @@ __global__ __launch_bounds__(256) void rope_backward(const RopeArgs a) {
               sum = __builtin_fmaf(x[e], x[e], sum);
             }
             const float r = rsqrtf(sum_lanes<kLanes>(sum) * (1.0f / D) + a.eps);
-            if (!sh.tok.live[tt[i]]) {
+            if (!sh.live[tt[i]]) {
 #pragma unroll
               for (int e = 0; e < 8; ++e) dy[e] = 0.0f;
             } else {
@@ -255,7 +318,7 @@ __global__ __launch_bounds__(256) void rope_backward(const RopeArgs a) {
           u32x4 out;
 #pragma unroll
           for (int e = 0; e < 4; ++e) out[e] = pack2<T>(dy[2 * e], dy[2 * e + 1]);
-          *reinterpret_cast<u32x4 *>(row_at(a.dx[side], sh.tok.b[tt[i]], sh.tok.t[tt[i]], h[i], lane)) = out;
+          *reinterpret_cast<u32x4 *>(row_at(a.dx[side], sh.b[tt[i]], sh.t[tt[i]], h[i], lane)) = out;
         }
       }
     }
@@ -294,23 +357,28 @@ __global__ __launch_bounds__(256) void rope_weights(const RopeArgs a, int parts)
   to[at % D] = x;
 }
 
-template <class T, int D>
-hipError_t run_forward(const RopeArgs &a, hipStream_t s) {
-  constexpr int kGroups = 256 / (D / 8);
-  const int64_t tiles = rope_tiles(static_cast<int64_t>(a.b) * a.n);
-  const int heads = a.heads[0] + a.heads[1];
-  // few tokens: their heads go to several workgroups, a row a group of lanes at least
-  int heads_of = heads;
-  while (heads_of * kTile > kGroups && tiles * ((heads + heads_of - 1) / heads_of) < 1024) heads_of = (heads_of + 1) / 2;
-  const int chunks = (heads + heads_of - 1) / heads_of;
-  if (tiles * chunks > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((rope_forward<T, D>), dim3(static_cast<unsigned>(tiles * chunks)), dim3(256), 0, s, a, heads_of, chunks);
+template <class T, int D, int TOK>
+hipError_t run_forward(const RopeArgs &a, int64_t tokens, hipStream_t s) {
+  hipLaunchKernelGGL((rope_forward<T, D, TOK>), dim3(static_cast<unsigned>((tokens + TOK - 1) / TOK)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
 template <class T, int D>
+hipError_t run_forward(const RopeArgs &a, hipStream_t s) {
+  constexpr int kGroups = 256 / (D / 8);
+  const int64_t tokens = static_cast<int64_t>(a.b) * a.n, heads = a.heads[0] + a.heads[1];
+  if (tokens * heads <= kRopeRows) {
+    hipLaunchKernelGGL((rope_rows<T, D>), dim3(static_cast<unsigned>((tokens * heads + kGroups - 1) / kGroups)), dim3(256), 0,
+                       s, a);
+    return hipGetLastError();
+  }
+  // few heads: tokens enough that a group of lanes has rows of its own
+  return heads <= 16 ? run_forward<T, D, 16>(a, tokens, s) : run_forward<T, D, 4>(a, tokens, s);
+}
+
+template <class T, int D>
 hipError_t run_backward(const RopeArgs &a, hipStream_t s) {
-  const int64_t tiles = rope_tiles(static_cast<int64_t>(a.b) * a.n);
+  const int64_t tiles = (static_cast<int64_t>(a.b) * a.n + kTile - 1) / kTile;
   const int grid = static_cast<int>(tiles < a.grid ? tiles : a.grid);
   if (grid > 0) {
     hipLaunchKernelGGL((rope_backward<T, D>), dim3(grid), dim3(256), 0, s, a);
@@ -323,9 +391,6 @@ hipError_t run_backward(const RopeArgs &a, hipStream_t s) {
 
 }  // namespace
 }  // namespace attn
-
-int rope_tile() { return attn::kTile; }
-int64_t rope_tiles(int64_t tokens) { return (tokens + attn::kTile - 1) / attn::kTile; }
 
 hipError_t launch_rope(const RopeArgs &a, spmm_dtype_t t, int d, hipStream_t s) {
   if (t == SPMM_BF16) return d == 64 ? attn::run_forward<attn::Bf16, 64>(a, s) : attn::run_forward<attn::Bf16, 128>(a, s);

@@ -101,17 +101,21 @@ __global__ __launch_bounds__(256) void attn_pool(const AttnPoolArgs a) {
 
 // The same from a cache in 8 bits, whose keys are code * scale: a product of 31
 // bits, so that its sums in 64 bits are exact as long as the scales of a block
-// are within 2^16 of one another.  Codes take half the lanes of a row.
-template <int D>
-__global__ __launch_bounds__(256) void attn_pool8(const AttnPoolArgs a) {
-  constexpr int kPieces = D / 16, kStep = 64 / kPieces;
+// are within 2^16 of one another.  W waves pool one block of one head, 8 bytes a
+// lane; a lane ends with the sums of one or two channels.  Bound by the latency of
+// its chain: four waves a block where there are few, else one.
+template <int D, int W>
+__global__ __launch_bounds__(256) void attn_pool8(const AttnPoolArgs a, uint32_t items) {
+  constexpr int kLanes = D / 8, kStep = 64 / kLanes, kRows = 64 / W, kRounds = kRows / kStep;
+  constexpr int kSteps = D == 128 ? 2 : 3, kKept = 8 >> kSteps;
   const int lane = threadIdx.x & 63;
-  int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int h = item % a.hk;
-  item /= a.hk;
-  const int w = item % a.width;
-  const int64_t b = item / a.width;
-  if (b >= a.b) return;
+  const int wave = W > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
+  uint32_t item = W > 1 ? blockIdx.x : blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (item >= items) return;
+  const int h = item % static_cast<uint32_t>(a.hk);
+  item /= static_cast<uint32_t>(a.hk);
+  const int w = item % static_cast<uint32_t>(a.width);
+  const int64_t b = item / static_cast<uint32_t>(a.width);
   const int32_t len = attn_len(a.lens, b, a.nk);
   int32_t first = a.first ? a.first[b] : 0;
   first = first < 0 ? 0 : first;
@@ -128,43 +132,66 @@ __global__ __launch_bounds__(256) void attn_pool8(const AttnPoolArgs a) {
     slot = b * a.nkb + id;
     p = a.k.p + b * a.k.sb + id * kAttnPage * a.k.st;
   }
-  p += h * a.k.sh + (lane % kPieces) * 16;
   const int64_t at = slot * a.hk + h;
-  const float *scale = a.k_scale + at * kAttnPage;
-  constexpr int kRounds = kAttnPage / kStep;
-  u32x4 v[kRounds];
+  p += h * a.k.sh + (lane % kLanes) * 8;
+  u32x2 v[kRounds];
   float x[kRounds];
 #pragma unroll
   for (int i = 0; i < kRounds; ++i) {
-    const int r = i * kStep + lane / kPieces;
-    v[i] = u32x4{0, 0, 0, 0};
-    x[i] = 0.0f;
-    if (r < kept) {
-      v[i] = *reinterpret_cast<const u32x4 *>(p + r * a.k.st);
-      x[i] = scale[r];
-    }
+    const int r = wave * kRows + i * kStep + lane / kLanes;
+    v[i] = *reinterpret_cast<const u32x2 *>(p + min(r, kept - 1) * a.k.st);
+    const float f = a.k_scale[at * kAttnPage + r];  // there for all 64 keys
+    x[i] = r < kept ? f : 0.0f;
   }
-  double sum[16];
-#pragma unroll
-  for (int c = 0; c < 16; ++c) sum[c] = 0.0;
+  double sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
   for (int i = 0; i < kRounds; ++i) {
     const double f = x[i];
 #pragma unroll
-    for (int c = 0; c < 16; ++c)
-      sum[c] = fma(static_cast<double>(static_cast<int8_t>(v[i][c / 4] >> (8 * (c % 4)))), f, sum[c]);
+    for (int c = 0; c < 8; ++c)
+      sum[c] = fma(static_cast<double>(static_cast<float>(static_cast<int8_t>(v[i][c / 4] >> (8 * (c % 4))))), f, sum[c]);
   }
+  // over the lanes of the same channels: each step adds what the lane 32, 16, ..
+  // away has of half the channels
+  int channel = (lane % kLanes) * 8;
 #pragma unroll
-  for (int m = kPieces; m < 64; m *= 2)
+  for (int k = 0; k < kSteps; ++k) {
+    const int m = 32 >> k, n = 4 >> k;  // distance; channels that stay
+    const bool upper = lane & m;
+    channel += upper ? n : 0;
 #pragma unroll
-    for (int c = 0; c < 16; ++c) sum[c] += __shfl_xor(sum[c], m);
+    for (int c = 0; c < n; ++c) {
+      const double mine = upper ? sum[c + n] : sum[c], other = upper ? sum[c] : sum[c + n];
+      sum[c] = mine + __shfl_xor(other, m);
+    }
+  }
+  if constexpr (W > 1) {
+    __shared__ double part[W - 1][kKept][64];
+    if (wave > 0)
+#pragma unroll
+      for (int c = 0; c < kKept; ++c) part[wave - 1][c][lane] = sum[c];
+    __syncthreads();
+    if (wave > 0) return;
+#pragma unroll
+    for (int c = 0; c < kKept; ++c)
+#pragma unroll
+      for (int i = 0; i < W - 1; ++i) sum[c] += part[i][c][lane];
+  }
   double top = 0.0;
 #pragma unroll
-  for (int c = 0; c < 16; ++c) top = top_of(top, fabs(sum[c]));
+  for (int c = 0; c < kKept; ++c) top = top_of(top, fabs(sum[c]));
 #pragma unroll
-  for (int m = 1; m < kPieces; m *= 2) top = top_of(top, __shfl_xor(top, m));
-  const u32x2 lo = round8(sum, top), hi = round8(sum + 8, top);
-  if (lane < kPieces) *reinterpret_cast<u32x4 *>(a.pooled + at * D + lane * 16) = u32x4{lo[0], lo[1], hi[0], hi[1]};
+  for (int m = 1; m < 64; m *= 2) top = top_of(top, __shfl_xor(top, m));
+  const bool fine = top > 0.0 && top < INFINITY;
+  const double by = fine ? 127.0 / top : 0.0;
+  int8_t *to = a.pooled + at * D + channel;
+  unsigned code[kKept];
+#pragma unroll
+  for (int c = 0; c < kKept; ++c) code[c] = fine ? static_cast<int>(rint(sum[c] * by)) & 0xff : 0;
+  if constexpr (kKept == 2)
+    *reinterpret_cast<uint16_t *>(to) = static_cast<uint16_t>(code[0] | code[1] << 8);
+  else
+    *to = static_cast<int8_t>(code[0]);
   if (lane == 0) a.pooled_scale[at] = top == 0.0 ? 0.0f : static_cast<float>(top / (127.0 * kept));
 }
 
@@ -332,11 +359,16 @@ hipError_t run_pool(const AttnPoolArgs &a, hipStream_t s) {
   const int64_t items = static_cast<int64_t>(a.b) * a.width * a.hk;
   if ((items + 3) / 4 > 0x7fffffff) return hipErrorInvalidValue;
   if (items == 0) return hipSuccess;
-  const dim3 grid(static_cast<unsigned>((items + 3) / 4));
-  if (a.k_scale)
-    hipLaunchKernelGGL((attn_pool8<D>), grid, dim3(256), 0, s, a);
-  else
-    hipLaunchKernelGGL((attn_pool<T, D>), grid, dim3(256), 0, s, a);
+  if (a.k_scale) {
+    if (items > 0x7fffffff) return hipErrorInvalidValue;
+    // four waves a block while they fit the chip at once (eight workgroups a CU)
+    if (items <= 2048)
+      hipLaunchKernelGGL((attn_pool8<D, 4>), dim3(static_cast<unsigned>(items)), dim3(256), 0, s, a, items);
+    else
+      hipLaunchKernelGGL((attn_pool8<D, 1>), dim3(static_cast<unsigned>((items + 3) / 4)), dim3(256), 0, s, a, items);
+  } else {
+    hipLaunchKernelGGL((attn_pool<T, D>), dim3(static_cast<unsigned>((items + 3) / 4)), dim3(256), 0, s, a);
+  }
   return hipGetLastError();
 }
 
