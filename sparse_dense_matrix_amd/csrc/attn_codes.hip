@@ -74,9 +74,10 @@ __device__ __forceinline__ u32x2 encode(u32x4 v, float &scale) {
   // reciprocal, taken 2^-21 too large, it is off by up to 127 2^-20, so that what
   // comes that near to a tie is divided: a wave in twelve, but for ties of top / 2,
   // which a row in three of 8-bit values has and which 63.5 and more rounds to their
-  // even code, 64.
+  // even code, 64.  Where the reciprocal or 127 times it leaves the normal numbers,
+  // all are divided.
   const float by = (127.0f + 127.0f * 0x1p-21f) * __builtin_amdgcn_rcpf(top);
-  float x[8], t[8], far = 0.0f;
+  float x[8], t[8], far = top > 0x1p-100f && top < 0x1p120f ? 0.0f : 1.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     x[i] = elem<T>(v[i / 2], i & 1);

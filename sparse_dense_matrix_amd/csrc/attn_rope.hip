@@ -107,21 +107,21 @@ __device__ __forceinline__ Angles angles_of(const RopeArgs &a, const RopeShared<
   return x;
 }
 
-// x turned by its angles (back: the other way).  `other` are the pairs' other
-// channels where the halves are paired.
-__device__ __forceinline__ void rotate(const RopeArgs &a, const Angles &w, const Turn &u, bool back, float *x,
-                                       const float *other) {
+// x turned by its angles c and s (back: the other way), registers or LDS.  `other`
+// are the pairs' other channels where the halves are paired.
+__device__ __forceinline__ void rotate(const RopeArgs &a, const float *c, const float *s, const Turn &u, bool back,
+                                       float *x, const float *other) {
   if (!u.turned) return;
   if (a.interleaved) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float sn = back ? -w.s[i] : w.s[i], p = x[2 * i], q = x[2 * i + 1];
-      x[2 * i] = p * w.c[i] - q * sn;
-      x[2 * i + 1] = p * sn + q * w.c[i];
+      const float sn = back ? -s[i] : s[i], p = x[2 * i], q = x[2 * i + 1];
+      x[2 * i] = p * c[i] - q * sn;
+      x[2 * i + 1] = p * sn + q * c[i];
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = x[i] * w.c[i] + other[i] * (u.second != back ? w.s[i] : -w.s[i]);
+    for (int i = 0; i < 8; ++i) x[i] = x[i] * c[i] + other[i] * (u.second != back ? s[i] : -s[i]);
   }
 }
 
@@ -158,7 +158,7 @@ __device__ __forceinline__ u32x4 turned(const RopeArgs &a, u32x4 v, bool norm, c
       y[e] = y[e] * r * w2[e];
     }
   }
-  rotate(a, turn, u, false, x, y);
+  rotate(a, turn.c, turn.s, u, false, x, y);
   u32x4 out;
 #pragma unroll
   for (int e = 0; e < 4; ++e) out[e] = pack2<T>(x[2 * e], x[2 * e + 1]);
@@ -291,7 +291,7 @@ __global__ __launch_bounds__(256) void rope_backward(const RopeArgs a) {
             dy[e] = elem<T>(gv[i][e / 2], e & 1);
             other[e] = elem<T>(w[e / 2], e & 1);
           }
-          rotate(a, angles_of<D>(a, sh, tt[i], u), u, true, dy, other);
+          rotate(a, sh.cosine[tt[i]] + u.first, sh.sine[tt[i]] + u.first, u, true, dy, other);
           if (norm) {
             float x[8], sum = 0.0f, dot = 0.0f;
 #pragma unroll

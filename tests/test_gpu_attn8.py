@@ -101,6 +101,39 @@ def test_rope(S, n):
             A.check(f"d{name}_weight", dw, *want["dw"])
 
 
+# rows enough for the kernels of many: tokens in groups of 16 (up to 16 heads) and of 4
+MANY = [rope_case(b=2, n=2500, hq=12, hk=4, pairs=24, interleaved=True, lens=[2500, 1777], starts=[0, -3]),
+        rope_case(n=5003, hq=9, hk=5, d=128, dtype=HF, axes=2), rope_case(b=3, n=701, hq=32, hk=8, d=128, pairs=40),
+        rope_case(b=2, n=1399, hq=20, hk=20, dtype=HF, lens=[0, 1399], starts=[5, 40], interleaved=True),
+        rope_case(b=67, n=29, hq=33, hk=2, norm=False, starts=[100 * i for i in range(67)])]
+
+
+@pytest.mark.parametrize("n", range(len(MANY)))
+def test_rope_of_many_rows(S, n):
+    """Against the plain form, as above, and token by token: a short call on the
+    same tokens (another kernel) gives the same bits."""
+    c = MANY[n]
+    q, k, _, _, qw, kw, place, alive, angle, off = rope_inputs(c, 600 + n)
+    w = {} if qw is None else dict(q_weight=qw.cuda(), k_weight=kw.cuda())
+    positions = place.to(torch.int32).cuda() if c["axes"] > 1 else None
+    qo, ko = torch.full_like(q, 7.0).cuda(), torch.full_like(k, 7.0).cuda()
+    S.spmm_execute_attn_rope(rope_plan(S, c), q.cuda(), k.cuda(), qo, ko, positions=positions, lens=ints(c["lens"]),
+                             starts=ints(c["starts"]), **w)
+    dead = ~alive[:, :, None, None]
+    for name, x, o, wt in (("q", q, qo, qw), ("k", k, ko, kw)):
+        value, bound = R.rope(torch.where(dead, 0.0, x.double()), None if wt is None else wt.double(), angle, off,
+                              c["interleaved"], c["eps"], c["dtype"])["o"]
+        A.check(name, o, torch.where(dead, 7.0, value), bound)
+    short = dict(c, n=5)
+    first = c["n"] - 5
+    few = rope_plan(S, short)
+    x, y = (t[:, first:].contiguous().cuda() for t in (q, k))
+    qs, ks = torch.full_like(x, 7.0), torch.full_like(y, 7.0)
+    S.spmm_execute_attn_rope(few, x, y, qs, ks, positions=None if positions is None else positions[:, :, first:].contiguous(),
+                             lens=ints(c["lens"]), starts=ints([s + first for s in c["starts"] or [0] * c["b"]]), **w)
+    assert torch.equal(qs, qo[:, first:]) and torch.equal(ks, ko[:, first:])
+
+
 def test_rope_in_place_and_packed(S):
     """q, k of one packed buffer, turned in place, and gradients over their own inputs."""
     c = rope_case(b=2, n=37, hq=6, hk=2, d=128)
@@ -253,7 +286,7 @@ def test_codes_of_every_value(S):
     bits = torch.arange(-2 ** 15, 2 ** 15).short()
     x = bits.view(BF)
     x = x[torch.isfinite(x)]
-    for top in (1.0, 127.0, 2.0 ** -126, 3.3e38, 0.7578125):
+    for top in (1.0, 127.0, 2.0 ** -126, 3.3e38, 0.7578125, 1.984375, 2.0 ** -121, 2.0 ** -133, 2.0 ** 120, 2.0 ** 127):
         keep = x[x.abs() <= torch.tensor(top).to(BF)]
         keep = keep[:keep.numel() // 63 * 63].reshape(-1, 63)
         r = torch.cat((keep, torch.full((keep.shape[0], 1), top).to(BF)), 1)
@@ -261,6 +294,24 @@ def test_codes_of_every_value(S):
         r = r.reshape(1, n, 1, 64)
         P = S.spmm_plan_attn(1, n, n, 1, 1, 64)
         k8, v8, ks, vs = empty_cache(-(-n // PAGE), 1, 64)
+        k8, v8 = k8.reshape(1, -1, 1, 64)[:, :n], v8.reshape(1, -1, 1, 64)[:, :n]
+        S.spmm_execute_attn_write(P, r.cuda(), r.cuda(), k8, v8, ks, vs)
+        code, scale = R.encode(r)
+        assert torch.equal(k8.cpu(), code) and torch.equal(v8.cpu(), code)
+        assert torch.equal(ks.reshape(-1)[:n].cpu(), scale.reshape(-1))
+
+
+def test_codes_of_ties(S):
+    """fp16 rows whose quotients are half a whole number: the even code."""
+    for e in range(-24, 9):
+        top = 254.0 * 2.0 ** e
+        x = torch.arange(-254, 255, 2)[:252].float() * 0.5 * 2.0 ** (e + 1)
+        x = torch.stack((x + 2.0 ** e, x)).reshape(-1, 63)
+        r = torch.cat((x, torch.full((x.shape[0], 1), top)), 1).to(HF)
+        n = r.shape[0]
+        r = r.reshape(1, n, 1, 64)
+        P = S.spmm_plan_attn(1, n, n, 1, 1, 64, dtype=S.F16)
+        k8, v8, ks, vs = empty_cache(1, 1, 64)
         k8, v8 = k8.reshape(1, -1, 1, 64)[:, :n], v8.reshape(1, -1, 1, 64)[:, :n]
         S.spmm_execute_attn_write(P, r.cuda(), r.cuda(), k8, v8, ks, vs)
         code, scale = R.encode(r)
@@ -285,7 +336,8 @@ def filled(S, c, g, pages=None, far=0):
     return [x.cuda() for x in (out[0][0], out[1][0], out[0][1], out[1][1])], k, v, table
 
 
-POOL = [dict(b=1, nk=64), dict(b=3, nk=200, hk=3, d=128), dict(b=2, nk=1000, hk=8, d=128, nq=70), dict(b=5, nk=130, hk=1)]
+POOL = [dict(b=1, nk=64), dict(b=3, nk=200, hk=3, d=128), dict(b=2, nk=1000, hk=8, d=128, nq=70), dict(b=5, nk=130, hk=1),
+        dict(b=3, nk=6500, nq=6500, hk=7), dict(b=2, nk=8190, nq=8190, hk=9, d=128)]  # blocks enough for a wave each
 
 
 @pytest.mark.parametrize("paged", [True, False])
