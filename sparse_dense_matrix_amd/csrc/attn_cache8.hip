@@ -199,31 +199,40 @@ __device__ __forceinline__ const float *scales_at(const Source &s, int block, in
   return s.scales + static_cast<int64_t>(block) * s.scale_step + first;
 }
 
-// The scores s of 32 keys from key0 on (each lane's, times ks already) become
+// Which of the 32 keys from `key` on a row sees.
+__device__ __forceinline__ uint32_t seen_of(const AttnArgs &a, const Row &r, int32_t key) {
+  if (!a.tree) {
+    const int32_t last = min(r.pos, r.len - 1) - key;
+    return last >= 31 ? ~0u : (last < 0 ? 0u : (2u << last) - 1);
+  }
+  const int32_t drafts = r.len - r.start, before = r.start - key;  // before: keys of the text
+  const uint64_t bits = drafts >= 64 ? r.bits : (drafts <= 0 ? 0 : r.bits & ((uint64_t(1) << drafts) - 1));
+  if (before >= 32) return ~0u;
+  if (before > 0) return static_cast<uint32_t>(bits << before) | ((1u << before) - 1);
+  return before > -64 ? static_cast<uint32_t>(bits >> -before) : 0u;
+}
+
+// The scores s of N * 32 keys from key0 on (each lane's, times ks already) become
 // weights, and o, m and l move with the maximum.
-template <class T, int D, int M, class Acc>
-__device__ __forceinline__ void softmax8(const AttnArgs &a, const Row &r, int32_t key0, int lane, float c,
-                                         Scores<M> &s, Stats &st, Acc *o) {
+template <class T, int D, int M, int N, class Acc>
+__device__ __forceinline__ void softmax8(const AttnArgs &a, const Row &r, int32_t key0, int lane, float c, float shift,
+                                         Scores<M> *s, Stats &st, Acc *o) {
   using F = Form<T, M>;
   constexpr int E = M / 2;
-  if (key0 + 32 > r.open) {
-    if (a.tree) {
-      const int32_t before = r.start - (key0 + F::first_key(lane));  // keys of the text
+  if (key0 + 32 * N > r.open) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const uint32_t seen = seen_of(a, r, key0 + 32 * n + F::first_key(lane));
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const int32_t draft = F::key(e) - before;
-        const uint64_t bit = draft < 64 ? r.bits >> (draft & 63) : 0;
-        s[e] = (draft < 0 || (bit & 1)) && draft < r.len - r.start ? s[e] : -INFINITY;
+        const uint32_t keep = static_cast<int32_t>(seen << (31 - F::key(e))) >> 31;  // a vector register, no mask of lanes
+        s[n][e] = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, static_cast<float>(s[n][e])) & keep) | (0xff800000u & ~keep));
       }
-    } else {
-      const int32_t last = min(r.pos, r.len - 1) - (key0 + F::first_key(lane));
-#pragma unroll
-      for (int e = 0; e < E; ++e) s[e] = F::key(e) <= last ? s[e] : -INFINITY;
     }
   }
-  float top = s[0];
+  float top = s[0][0];
 #pragma unroll
-  for (int e = 1; e < E; ++e) top = fmaxf(top, s[e]);
+  for (int e = 1; e < N * E; ++e) top = fmaxf(top, s[e / E][e % E]);
   top = F::max_row(top) * c;
   if (__any(top > st.m + kSlack)) {
     const float next = fmaxf(st.m, top);
@@ -233,11 +242,11 @@ __device__ __forceinline__ void softmax8(const AttnArgs &a, const Row &r, int32_
     for (int i = 0; i < D * M / 64; ++i) o[i / F::kAcc][i % F::kAcc] *= f;
     st.m = next;
   }
-  const float from = st.m == -INFINITY ? 0.0f : st.m;
+  const float from = (st.m == -INFINITY ? 0.0f : st.m) + shift;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    s[e] = exp2_(__builtin_fmaf(s[e], c, -from));
-    st.l += s[e];
+  for (int e = 0; e < N * E; ++e) {
+    s[e / E][e % E] = exp2_(__builtin_fmaf(s[e / E][e % E], c, -from));
+    st.l += s[e / E][e % E];
   }
 }
 
@@ -246,46 +255,40 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t records(const void *p, int32_t
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, bytes, 0x00020000);
 }
 
-// What O is counted in.  bf16 reaches as far as 32 bits: one.  For f16 a power
-// of two that the largest scale of values so far does not pass, so that a weight
-// times a scale stays below 2^15 in its units; O moves with it, which few tiles
-// ask for.
-__device__ __forceinline__ float largest(float x) {  // of the wave's lanes; NaN and infinity count as 2^100
-  float y = fminf(x, 0x1p100f);
+// What weights are counted in, O and l with them, so that the quotient stays: a
+// weight is 2^(score - m - shift).  bf16 reaches as far as 32 bits: no shift.  For
+// f16 it is that of a power of two that the largest scale of values so far does
+// not pass, less 7, so that a weight times a scale stays below 2^15.  O and l move
+// with it, which few tiles ask for.  From 2^-40 on: scales below that leave f16
+// outputs at zero, and l in range.
+// The largest magnitude of a wave's lanes, NaN and infinity as 2^100, found among
+// the bits.
+__device__ __forceinline__ float largest(float x) {
+  const unsigned u = over_lanes<16>(__builtin_bit_cast(unsigned, x) & 0x7fffffffu,
+                                    [](unsigned p, unsigned q) { return max(p, q); });
+  unsigned most = 0;
 #pragma unroll
-  for (int m = 1; m < 64; m *= 2) y = fmaxf(y, __shfl_xor(y, m));
-  return y;
+  for (int i = 0; i < 64; i += 16) most = max(most, static_cast<unsigned>(__builtin_amdgcn_readlane(u, i)));
+  return __builtin_bit_cast(float, min(most, __builtin_bit_cast(unsigned, 0x1p100f)));
 }
 template <class T>
 struct Unit {
-  __device__ __forceinline__ float in(float x) const { return x; }
-  template <int N, class Acc>
-  __device__ __forceinline__ void out(Acc *) const {}
+  static constexpr float shift = 0.0f;
 };
 template <>
 struct Unit<F16> {
-  float top = 0x1p-100f;
-  // what weights are multiplied by: 2^7 / top, for weights of up to 2^8
-  float by = 0x1p107f;
+  float top = 0x1p-40f, shift = -47.0f;
   template <int N, class Acc>
-  __device__ __forceinline__ void raise(float x, Acc *o) {
+  __device__ __forceinline__ void raise(float x, Stats &st, Acc *o) {
     if (__builtin_amdgcn_readfirstlane(x > top)) {
-      const float next = __builtin_bit_cast(float, (__builtin_bit_cast(unsigned, x) & 0x7f800000u) + 0x00800000u);
-      const float f = top / next;
-      top = next;
-      by = 0x1p7f / next;
-      rescale<N>(f, o);
-    }
-  }
-  __device__ __forceinline__ float in(float x) const { return x * by; }
-  template <int N, class Acc>
-  __device__ __forceinline__ void out(Acc *o) const {
-    rescale<N>(top * 0x1p-7f, o);
-  }
-  template <int N, class Acc>
-  __device__ __forceinline__ static void rescale(float f, Acc *o) {
+      const unsigned next = (__builtin_bit_cast(unsigned, x) & 0x7f800000u) + 0x00800000u;
+      const float f = top / __builtin_bit_cast(float, next);
+      top = __builtin_bit_cast(float, next);
+      shift = static_cast<float>(static_cast<int>(next >> 23) - 134);
+      st.l *= f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) o[i] *= f;
+      for (int i = 0; i < N; ++i) o[i] *= f;
+    }
   }
 };
 
@@ -437,7 +440,7 @@ __global__ __launch_bounds__(64 * KW, M == 16 ? 4 : 2) void attn_stream8(const A
       }
       wait_lds();
       issue(t + KW, false);
-      softmax8<T, D, M>(a, row, key0, lane, c, s, st, o);
+      softmax8<T, D, M, 1>(a, row, key0, lane, c, 0.0f, &s, st, o);
       wait_vm<kLoads>();
 #pragma unroll
       for (int i = 0; i < kE / 4; ++i) {
@@ -611,40 +614,41 @@ __global__ __launch_bounds__(64 * RW * KW, 2) void attn_forward8(const AttnArgs 
       const int t = round * KW + kw;
       if (t >= tiles || !some) continue;
       const int32_t key0 = __builtin_amdgcn_readlane(blocks.id, t / kSubs) * kAttnPage + (t % kSubs) * KT;
-      if constexpr (T::kNarrow) unit.template raise<D / 32>(xs[2 * KT], o);
+      if constexpr (T::kNarrow) unit.template raise<D / 32>(xs[2 * KT], st, o);
+      constexpr int kN = KT / 32, kI = D / 32;
+      const float *x = xs + F::first_key(lane);
+      Scores<32> s[kN];
 #pragma unroll
-      for (int n = 0; n < KT / 32; ++n) {
+      for (int n = 0; n < kN; ++n) {
         f32x16 acc = zero16();
-        auto kx = operands<D / 16, kAhead>([&](int x) { return L::operand(kt, 32 * n, x, lane); });
+        auto kx = operands<D / 16, kAhead>([&](int i) { return L::operand(kt, 32 * n, i, lane); });
         kx.begin();
-        kx.run([&](int x, u32x4 k) { acc = T::mma(k, q[x], acc); });
-        Scores<32> s;
-        const float *x = xs + 32 * n + F::first_key(lane);
+        kx.run([&](int i, u32x4 k) { acc = T::mma(k, q[i], acc); });
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const f32x4 f = *reinterpret_cast<const f32x4 *>(x + 8 * i);
+          const f32x4 f = *reinterpret_cast<const f32x4 *>(x + 32 * n + 8 * i);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s[4 * i + j] = acc[4 * i + j] * f[j];
+          for (int j = 0; j < 4; ++j) s[n][4 * i + j] = acc[4 * i + j] * f[j];
         }
-        constexpr int kI = D / 32;
-        auto vx = operands<2 * kI, kAhead>([&](int i) { return L::operand_t(vt, 32 * n + 16 * (i / kI), i % kI, lane); });
-        vx.begin();
-        softmax8<T, D, 32>(a, row, key0 + 32 * n, lane, c, s, st, o);
-        u32x4 p[2];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const f32x4 f = *reinterpret_cast<const f32x4 *>(x + KT + 8 * i);
-          p[i / 2][2 * (i % 2)] = pack2<T>(s[4 * i] * unit.in(f[0]), s[4 * i + 1] * unit.in(f[1]));
-          p[i / 2][2 * (i % 2) + 1] = pack2<T>(s[4 * i + 2] * unit.in(f[2]), s[4 * i + 3] * unit.in(f[3]));
-        }
-        vx.run([&](int i, u32x4 v) { o[i % kI] = T::mma(v, p[i / kI], o[i % kI]); });
       }
+      auto vx = operands<2 * kN * kI, kAhead>([&](int i) { return L::operand_t(vt, 16 * (i / kI), i % kI, lane); });
+      vx.begin();
+      softmax8<T, D, 32, kN>(a, row, key0, lane, c, unit.shift, s, st, o);
+      u32x4 p[2 * kN];
+#pragma unroll
+      for (int i = 0; i < 4 * kN; ++i) {
+        const f32x4 f = *reinterpret_cast<const f32x4 *>(x + KT + 8 * i);
+        const float *w = reinterpret_cast<const float *>(s) + 4 * i;
+        p[i / 2][2 * (i % 2)] = pack2<T>(w[0] * f[0], w[1] * f[1]);
+        p[i / 2][2 * (i % 2) + 1] = pack2<T>(w[2] * f[2], w[3] * f[3]);
+      }
+      vx.run([&](int i, u32x4 v) { o[i % kI] = T::mma(v, p[i / kI], o[i % kI]); });
     }
     // the next entries' first tiles go where the last ones may still be read
     barrier();
   }
 
-  unit.template out<D / 32>(o);
+  st.m += unit.shift;
   st.l = add_halves(st.l);
   if (!row.live) st = Stats();
   if constexpr (KW > 1) {
@@ -698,7 +702,7 @@ hipError_t run8(const AttnArgs &a, const AttnScales &x, spmm_dtype_t t, hipStrea
     }
     case 2: e = run_forward8<T, D, 2, 2, 32>(a, x, s); break;
     // up to a workgroup a CU, two groups of waves share its list
-    case 4: e = grid_of(a) <= kCus ? run_forward8<T, D, 4, 2, 32>(a, x, s) : run_forward8<T, D, 4, 1, 32>(a, x, s); break;
+    case 4: e = grid_of(a) <= kCus ? run_forward8<T, D, 4, 2, 32>(a, x, s) : run_forward8<T, D, 4, 1, 64>(a, x, s); break;
     default: e = run_forward8<T, D, 8, 1, 64>(a, x, s); break;
   }
   return e != hipSuccess || a.nsplit == 1 ? e : launch_attn_merge(a, t, D, s);
