@@ -341,7 +341,9 @@ __device__ __forceinline__ void store8(const AttnArgs &a, const Item &it, const 
 // Up to 32 rows to a list: each wave streams tiles of 32 keys through LDS of
 // its own, without barriers: the next codes and scales of keys load during the
 // softmax and the product with the values, the next of values during the
-// scores.  KW waves share a list's tiles and join their sums.
+// scores.  KW waves share a list's tiles and join their sums.  Bound by memory:
+// 32 sequences of 21.5k of up to 32k keys, 8 key heads of 4: 258 us for 1.42 GB,
+// 5.5 TB/s, and the join of the ranges 6.
 template <class T, int D, int M, int KW>
 __global__ __launch_bounds__(64 * KW, M == 16 ? 4 : 2) void attn_stream8(const AttnArgs a, const AttnScales scales) {
   using F = Form<T, M>;
@@ -504,9 +506,14 @@ __global__ __launch_bounds__(64 * KW, M == 16 ? 4 : 2) void attn_stream8(const A
 // their way through registers to LDS, which then holds the tiles that the 16-bit
 // kernel stages; the next tile's codes load during this one's products.  A
 // group's first wave brings the scales, and the largest of the values'.
+//
+// Bound by vector instructions: a wave's 64 keys take 1024 cycles of the matrix
+// unit and about 1900 of the softmax and of widening.  64 keys to a softmax have one
+// maximum, one test and one barrier where 32 have two: 24 drafted tokens of 32 heads
+// over 16 sequences of up to 8k keys take 96 us (bf16) and 105 us (f16), in tiles of
+// 32 114 and 135; with all pages in L2 83 and 92.
 template <class T, int D, int RW, int KW, int KT>
-__global__ __launch_bounds__(64 * RW * KW, 2) void attn_forward8(const AttnArgs a,
-                                                                                         const AttnScales scales) {
+__global__ __launch_bounds__(64 * RW * KW, 2) void attn_forward8(const AttnArgs a, const AttnScales scales) {
   using L = Tile<D>;
   using F = Form<T, 32>;
   constexpr int kThreads = 64 * RW;
@@ -691,18 +698,23 @@ hipError_t run8(const AttnArgs &a, const AttnScales &x, spmm_dtype_t t, hipStrea
   if (grid_of(a) > 0x7fffffff) return hipErrorInvalidValue;
   hipError_t e;
   switch (attn_tile(a.rows, a.nqb).row_waves) {
-    // a wave a list where there are enough lists to fill the chip twice over
+    // A wave a list where there are lists enough to fill the chip, and rows of 16
+    // where they fit.  8 blocks for every query, 8 key heads of 4: 2048 lists take 35
+    // us, with four waves each 40, 1024 27 and 25.5, 32k 325 and (rows of 32) 725.  32
+    // tokens over 8k keys each: rows of 16 119 us, of 32 140.
     case 1: {
-      const bool alone = grid_of(a) >= 4096 && a.nsplit == 1;
+      const bool alone = grid_of(a) >= 2048 && a.nsplit == 1;
       if (a.rows <= 16)
         e = alone ? run_stream8<T, D, 16, 1>(a, x, s) : run_stream8<T, D, 16, 4>(a, x, s);
       else
         e = alone ? run_stream8<T, D, 32, 1>(a, x, s) : run_stream8<T, D, 32, 4>(a, x, s);
       break;
     }
+    // 2048 queries of 8 heads, 16 blocks for each 64: two groups of waves to a list
+    // 27 us, one 43.  With four waves of rows a second group gains nothing (25.0 us
+    // for 24 drafted tokens over 8k keys, 24.4 without).
     case 2: e = run_forward8<T, D, 2, 2, 32>(a, x, s); break;
-    // up to a workgroup a CU, two groups of waves share its list
-    case 4: e = grid_of(a) <= kCus ? run_forward8<T, D, 4, 2, 32>(a, x, s) : run_forward8<T, D, 4, 1, 64>(a, x, s); break;
+    case 4: e = run_forward8<T, D, 4, 1, 64>(a, x, s); break;
     default: e = run_forward8<T, D, 8, 1, 64>(a, x, s); break;
   }
   return e != hipSuccess || a.nsplit == 1 ? e : launch_attn_merge(a, t, D, s);

@@ -19,7 +19,6 @@ namespace sdm {
 namespace attn {
 namespace {
 
-constexpr int64_t kRopeRows = 1 << 16;
 constexpr int kTile = 4;  // tokens of a workgroup of the backward kernel at a time
 
 // TOK tokens from t0 of all sequences' tokens in one row: place and whether they
@@ -167,7 +166,7 @@ __device__ __forceinline__ u32x4 turned(const RopeArgs &a, u32x4 v, bool norm, c
 
 // Few rows: D / 8 lanes take one each, all heads of a token after one another.
 // Bound by its chain of loads and steps; the row loads before the angles are
-// computed.
+// computed.  32 tokens of 32 and 8 heads of 128: 4.4 us, a launch of nothing 3.
 template <class T, int D>
 __global__ __launch_bounds__(256) void rope_rows(const RopeArgs a) {
   constexpr int kLanes = D / 8, kGroups = 256 / kLanes;
@@ -246,7 +245,10 @@ __global__ __launch_bounds__(256) void rope_forward(const RopeArgs a) {
 }
 
 // Workgroups take tiles in turn; each lane sums the weights' gradients of its
-// channels over its rows, and the workgroup's sums go to the workspace.
+// channels over its rows, and the workgroup's sums go to the workspace.  16k tokens
+// of 32 and 8 heads of 128: 106 us for 503 MB, 4.75 TB/s, bound by memory: tiles of
+// 2 and 8 tokens and 4 rows in flight take as long.  Angles kept in registers, as
+// forward, leave room for too few rows: 112 us.
 template <class T, int D>
 __global__ __launch_bounds__(256) void rope_backward(const RopeArgs a) {
   constexpr int kLanes = D / 8, kGroups = 256 / kLanes, kU = 2;
@@ -367,12 +369,16 @@ template <class T, int D>
 hipError_t run_forward(const RopeArgs &a, hipStream_t s) {
   constexpr int kGroups = 256 / (D / 8);
   const int64_t tokens = static_cast<int64_t>(a.b) * a.n, heads = a.heads[0] + a.heads[1];
-  if (tokens * heads <= kRopeRows) {
-    hipLaunchKernelGGL((rope_rows<T, D>), dim3(static_cast<unsigned>((tokens * heads + kGroups - 1) / kGroups)), dim3(256), 0,
-                       s, a);
+  // A row a group of lanes up to eight workgroups a CU: 800 tokens of 32 and 8 heads
+  // of 128 take 8.1 us, by tokens 9.2; 1600 tokens 12.7 and 10.8; 6400 39 and 27.
+  const int64_t few = (tokens * heads + kGroups - 1) / kGroups;
+  if (few <= 8 * kCus) {
+    hipLaunchKernelGGL((rope_rows<T, D>), dim3(static_cast<unsigned>(few)), dim3(256), 0, s, a);
     return hipGetLastError();
   }
-  // few heads: tokens enough that a group of lanes has rows of its own
+  // Few heads: tokens enough that a group of lanes has rows of its own.  32k tokens
+  // of 12 and 4 heads of 64 take 26 us in sixteens, in fours 41; 6400 of 32 and 8 heads
+  // of 128 27 us in fours.
   return heads <= 16 ? run_forward<T, D, 16>(a, tokens, s) : run_forward<T, D, 4>(a, tokens, s);
 }
 

@@ -361,8 +361,9 @@ hipError_t run_pool(const AttnPoolArgs &a, hipStream_t s) {
   if (items == 0) return hipSuccess;
   if (a.k_scale) {
     if (items > 0x7fffffff) return hipErrorInvalidValue;
-    // four waves a block while they fit the chip at once (eight workgroups a CU)
-    if (items <= 2048)
+    // four waves a block up to two blocks a CU: 256 blocks take 3.9 us, with a wave
+    // each 4.7; 512 4.7 both; 1024 6.4 and 4.9; 4096 16.2 and 10.4
+    if (items <= 512)
       hipLaunchKernelGGL((attn_pool8<D, 4>), dim3(static_cast<unsigned>(items)), dim3(256), 0, s, a, items);
     else
       hipLaunchKernelGGL((attn_pool8<D, 1>), dim3(static_cast<unsigned>((items + 3) / 4)), dim3(256), 0, s, a, items);

@@ -217,7 +217,8 @@ def rows(shape, dtype, g):
 
 
 WRITE = [dict(b=1, n=1, nk=64), dict(b=3, n=5, nk=200, hk=3, d=128), dict(b=2, n=130, nk=130, dtype=HF),
-         dict(b=40, n=1, nk=1000, hk=8, d=128), dict(b=1, n=1000, nk=1000, hk=1, dtype=HF, d=128)]
+         dict(b=40, n=1, nk=1000, hk=8, d=128), dict(b=1, n=1000, nk=1000, hk=1, dtype=HF, d=128),
+         dict(b=3, n=1500, nk=1601, hk=8, dtype=HF, d=128), dict(b=2, n=2100, nk=2100, hk=8)]  # enough to go by blocks
 
 
 @pytest.mark.parametrize("paged", [True, False])
