@@ -655,7 +655,12 @@ __global__ __launch_bounds__(64 * RW * KW, 2) void attn_forward8(const AttnArgs 
     barrier();
   }
 
-  st.m += unit.shift;
+  if constexpr (T::kNarrow) {  // back from the unit, exactly
+    const float f = unit.top * 0x1p-7f;
+    st.l *= f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) o[i] *= f;
+  }
   st.l = add_halves(st.l);
   if (!row.live) st = Stats();
   if constexpr (KW > 1) {

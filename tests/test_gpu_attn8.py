@@ -543,6 +543,51 @@ def test_cache8_values_of_any_size(S, dtype, hq, nq):
     A.check("lse", lse, *want["lse"])
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("hq", [1, 12])
+def test_cache8_large_values_that_few_rows_see(S, dtype, hq):
+    """Values near the type's end: at a drafted token that only the last row sees,
+    and at a key whose weight is about 2^-60, read before the others.  The other
+    rows' values are 2^-28 of it, and come out as if it were not there."""
+    c = case(nq=24, nk=700, hq=hq, hk=1, d=128, dtype=dtype)
+    g = torch.Generator().manual_seed(33)
+    cache, _, _, table = filled(S, c, g)
+    at = table.long()[0]
+    slots = at.repeat_interleave(PAGE)[:700], torch.arange(700) % PAGE
+    ks, vs = torch.full((700,), 1 / 700.0), torch.full((700,), 500.0 * 2.0 ** -28)
+    vs[[3, 699]] = 500.0
+    code, values = cache[0].cpu(), cache[1].cpu()
+    code[slots[0][3], 3] = -127  # against queries that are all positive
+    q = torch.rand((1, 24, hq, 128), generator=g).add(0.5).to(dtype)
+    ks[3] = 0.03
+    cache[0].copy_(code)
+    cache[2][slots[0].cuda(), 0, slots[1].cuda()] = ks.cuda()
+    cache[3][slots[0].cuda(), 0, slots[1].cuda()] = vs.cuda()
+    k = code[slots].reshape(1, 700, 1, 128).double() * ks.double()[None, :, None, None]
+    v = values[slots].reshape(1, 700, 1, 128).double() * vs.double()[None, :, None, None]
+    tree = torch.full((1, 24), 1, dtype=torch.int64)
+    tree[0] |= torch.tensor([1 << t for t in range(24)])
+    o, lse = outputs(c)
+    S.spmm_execute_attn_cache8(plan(S, c), q.cuda(), *cache, o, lse, table=table.cuda(), tree=tree.cuda(), starts=ints([676]))
+    want = R.attention(c, q.double(), k, v, A.sees(c, None, [700], [676], tree))
+    A.check("o", o, *want["o"])
+    A.check("lse", lse, *want["lse"])
+
+
+@pytest.mark.parametrize("nq", [1, 24])
+def test_cache8_values_of_zero(S, nq):
+    """Zero scales, as rows of zeros have them: outputs of zero, and lse as it is."""
+    c = case(nq=nq, nk=300, hq=8, hk=2, d=64, dtype=HF)
+    g = torch.Generator().manual_seed(34)
+    cache, k, v, table = filled(S, c, g)
+    cache[3].zero_()
+    q = torch.randn((1, nq, 8, 64), generator=g).to(HF)
+    o, lse = outputs(c)
+    S.spmm_execute_attn_cache8(plan(S, c), q.cuda(), *cache, o, lse, table=table.cuda(), starts=ints([300 - nq]))
+    assert (o == 0).all()
+    A.check("lse", lse, *R.attention(c, q.double(), k, 0 * v, A.sees(c, None, [300], [300 - nq], None))["lse"])
+
+
 def test_cache8_far_pages_and_strides(S):
     """Pages beyond 4 GiB of codes, k and v side by side in a page, heads first."""
     c = case(b=2, nq=2, nk=300, hq=8, hk=2, d=128)
