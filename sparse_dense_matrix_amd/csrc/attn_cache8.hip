@@ -703,12 +703,14 @@ hipError_t run8(const AttnArgs &a, const AttnScales &x, spmm_dtype_t t, hipStrea
   if (grid_of(a) > 0x7fffffff) return hipErrorInvalidValue;
   hipError_t e;
   switch (attn_tile(a.rows, a.nqb).row_waves) {
-    // A wave a list where there are lists enough to fill the chip, and rows of 16
-    // where they fit.  8 blocks for every query, 8 key heads of 4: 2048 lists take 35
-    // us, with four waves each 40, 1024 27 and 25.5, 32k 325 and (rows of 32) 725.  32
-    // tokens over 8k keys each: rows of 16 119 us, of 32 140.
+    // A wave a list where there are lists enough to fill the chip and a sequence's
+    // queries read keys of each other's from L2; rows of 16 where they fit.  8 blocks
+    // for every query, 8 key heads of 4: 2048 lists take 35 us, with four waves each 40,
+    // 1024 27 and 25.5, 32k 325 and (rows of 32) 725.  One query each, from memory: 300
+    // sequences of 2k keys take 291 us with a wave a head, 245 with four.  32 tokens over
+    // 8k keys each: rows of 16 119 us, of 32 140.
     case 1: {
-      const bool alone = grid_of(a) >= 2048 && a.nsplit == 1;
+      const bool alone = a.nqb > 1 && grid_of(a) >= 2048 && a.nsplit == 1;
       if (a.rows <= 16)
         e = alone ? run_stream8<T, D, 16, 1>(a, x, s) : run_stream8<T, D, 16, 4>(a, x, s);
       else
