@@ -8,10 +8,12 @@
 // nothing is rounded on the way to the products: a score is the sum of q_t's
 // elements times the codes in 32 bits, then times ks_j.  The value's scale goes
 // to the weight: p_tj vs_j is rounded to bf16 for the product with d_j, at most
-// half a step of each weight.  For f16 outputs, whose step is eight times
-// finer, it goes as two bf16 operands, the weight and what its rounding left
-// out (2^-17 of it): a weight times a value's scale can pass f16's range both
-// ways, bf16 reaches as far as 32 bits.  The sum that divides is of p_tj itself.
+// half a step of each weight.  For f16 outputs, whose step is eight times finer,
+// up to 32 rows to a list, which reading the codes bounds, give it as two bf16
+// operands, the weight and what its rounding left out (2^-17 of it): a weight times a
+// value's scale can pass f16's range both ways, bf16 reaches as far as 32 bits.  More
+// rows, which products bound too, give it as one f16 operand in units that follow the
+// largest scale (Unit).  The sum that divides is of p_tj itself.
 #include "attn_rows.h"
 #include "internal.h"
 
