@@ -512,7 +512,7 @@ __global__ __launch_bounds__(64 * KW, M == 16 ? 4 : 2) void attn_stream8(const A
 // Bound by vector instructions: a wave's 64 keys take 1024 cycles of the matrix
 // unit and about 1900 of the softmax and of widening.  64 keys to a softmax have one
 // maximum, one test and one barrier where 32 have two: 24 drafted tokens of 32 heads
-// over 16 sequences of up to 8k keys take 96 us (bf16) and 105 us (f16), in tiles of
+// over 16 sequences of up to 8k keys take 95 us (bf16) and 101 us (f16), in tiles of
 // 32 114 and 135; with all pages in L2 83 and 92.
 template <class T, int D, int RW, int KW, int KT>
 __global__ __launch_bounds__(64 * RW * KW, 2) void attn_forward8(const AttnArgs a, const AttnScales scales) {
