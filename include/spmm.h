@@ -544,11 +544,9 @@ spmm_status_t spmm_execute_attn_pool8(spmm_plan_t p, const spmm_attn_tensor_t *k
 
 /* spmm_execute_attn_cache over such a cache.  Codes enter the products as they
  * are: a score is the 32-bit sum of q times codes, times the key's scale, and
- * a weight takes the value's scale before it is rounded: bf16 plans to bf16, within
- * 2^-8 of itself; f16 plans with up to 32 rows to a list (queries times heads of a
- * key head) to two bf16 parts, 2^-16, with more to f16, within 2^-11 of itself or
- * 2^-32 of the largest scale of the list's values.  A key or value that stands for
- * NaN spreads as one does there. */
+ * a weight takes the value's scale and goes in as two bf16 parts, within 2^-16
+ * of itself (what is below 2^-126 counts as zero).  A key or value that stands
+ * for NaN spreads as one does there. */
 spmm_status_t spmm_execute_attn_cache8(spmm_plan_t p, const spmm_attn_tensor_t *q, const spmm_attn_tensor_t *k8,
                                        const spmm_attn_tensor_t *v8, const float *k_scale_dev,
                                        const float *v_scale_dev, int64_t pages, const spmm_attn_tensor_t *o,

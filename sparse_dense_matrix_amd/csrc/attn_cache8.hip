@@ -7,13 +7,10 @@
 // The codes are whole numbers up to 127, which bf16 and f16 hold exactly, so
 // nothing is rounded on the way to the products: a score is the sum of q_t's
 // elements times the codes in 32 bits, then times ks_j.  The value's scale goes
-// to the weight: p_tj vs_j is rounded to bf16 for the product with d_j, at most
-// half a step of each weight.  For f16 outputs, whose step is eight times finer,
-// up to 32 rows to a list, which reading the codes bounds, give it as two bf16
-// operands, the weight and what its rounding left out (2^-17 of it): a weight times a
-// value's scale can pass f16's range both ways, bf16 reaches as far as 32 bits.  More
-// rows, which products bound too, give it as one f16 operand in units that follow the
-// largest scale (Unit).  The sum that divides is of p_tj itself.
+// to the weight: p_tj vs_j is two bf16 operands for the products with d_j, the
+// weight and what its rounding left out, and so within 2^-16 of itself: a weight
+// times a value's scale can pass f16's range both ways, bf16 reaches as far as 32
+// bits.  The sum that divides is of p_tj itself.
 #include "attn_rows.h"
 #include "internal.h"
 
@@ -217,8 +214,8 @@ __device__ __forceinline__ uint32_t seen_of(const AttnArgs &a, const Row &r, int
 // The scores s of N * 32 keys from key0 on (each lane's, times ks already) become
 // weights, and o, m and l move with the maximum.
 template <class T, int D, int M, int N, class Acc>
-__device__ __forceinline__ void softmax8(const AttnArgs &a, const Row &r, int32_t key0, int lane, float c, float shift,
-                                         Scores<M> *s, Stats &st, Acc *o) {
+__device__ __forceinline__ void softmax8(const AttnArgs &a, const Row &r, int32_t key0, int lane, float c, Scores<M> *s,
+                                         Stats &st, Acc *o) {
   using F = Form<T, M>;
   constexpr int E = M / 2;
   if (key0 + 32 * N > r.open) {
@@ -244,7 +241,7 @@ __device__ __forceinline__ void softmax8(const AttnArgs &a, const Row &r, int32_
     for (int i = 0; i < D * M / 64; ++i) o[i / F::kAcc][i % F::kAcc] *= f;
     st.m = next;
   }
-  const float from = (st.m == -INFINITY ? 0.0f : st.m) + shift;
+  const float from = st.m == -INFINITY ? 0.0f : st.m;
 #pragma unroll
   for (int e = 0; e < N * E; ++e) {
     s[e / E][e % E] = exp2_(__builtin_fmaf(s[e / E][e % E], c, -from));
@@ -257,51 +254,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t records(const void *p, int32_t
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, bytes, 0x00020000);
 }
 
-// What weights are counted in, O and l with them, so that the quotient stays: a
-// weight is 2^(score - m - shift).  bf16 reaches as far as 32 bits: no shift.  For
-// f16 it is that of a power of two that the largest scale of values so far does
-// not pass, less 7, so that a weight times a scale stays below 2^15.  O and l move
-// with it, which few tiles ask for.  From 2^-40 on: scales below that leave f16
-// outputs at zero, and l in range.
-// The largest magnitude of a wave's lanes, NaN and infinity as 2^100, found among
-// the bits.
-__device__ __forceinline__ float largest(float x) {
-  const unsigned u = over_lanes<16>(__builtin_bit_cast(unsigned, x) & 0x7fffffffu,
-                                    [](unsigned p, unsigned q) { return max(p, q); });
-  unsigned most = 0;
-#pragma unroll
-  for (int i = 0; i < 64; i += 16) most = max(most, static_cast<unsigned>(__builtin_amdgcn_readlane(u, i)));
-  return __builtin_bit_cast(float, min(most, __builtin_bit_cast(unsigned, 0x1p100f)));
-}
-template <class T>
-struct Unit {
-  static constexpr float shift = 0.0f;
-};
-template <>
-struct Unit<F16> {
-  float top = 0x1p-40f, shift = -47.0f;
-  template <int N, class Acc>
-  __device__ __forceinline__ void raise(float x, Stats &st, Acc *o) {
-    if (__builtin_amdgcn_readfirstlane(x > top)) {
-      const unsigned next = (__builtin_bit_cast(unsigned, x) & 0x7f800000u) + 0x00800000u;
-      const float f = top / __builtin_bit_cast(float, next);
-      top = __builtin_bit_cast(float, next);
-      shift = static_cast<float>(static_cast<int>(next >> 23) - 134);
-      st.l *= f;
-#pragma unroll
-      for (int i = 0; i < N; ++i) o[i] *= f;
-    }
-  }
-};
-
-// Eight weights as the operand of a product with codes, and what their
-// rounding left out (f16 outputs).
-__device__ __forceinline__ void weights8(const float *w, u32x4 &hi, u32x4 *lo) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    hi[i] = pack2<Bf16>(w[2 * i], w[2 * i + 1]);
-    if (lo) (*lo)[i] = pack2<Bf16>(w[2 * i] - elem<Bf16>(hi[i], 0), w[2 * i + 1] - elem<Bf16>(hi[i], 1));
-  }
+// Two weights as words of the two operands of a product with codes.
+__device__ __forceinline__ void weights2(float a, float b, unsigned &hi, unsigned &lo) {
+  hi = pack2<Bf16>(a, b);
+  lo = pack2<Bf16>(a - elem<Bf16>(hi, 0), b - elem<Bf16>(hi, 1));
 }
 
 // o and lse of a lane's row, or its part of them where a list is cut into ranges.
@@ -444,7 +400,7 @@ __global__ __launch_bounds__(64 * KW, M == 16 ? 4 : 2) void attn_stream8(const A
       }
       wait_lds();
       issue(t + KW, false);
-      softmax8<T, D, M, 1>(a, row, key0, lane, c, 0.0f, &s, st, o);
+      softmax8<T, D, M, 1>(a, row, key0, lane, c, &s, st, o);
       wait_vm<kLoads>();
 #pragma unroll
       for (int i = 0; i < kE / 4; ++i) {
@@ -455,14 +411,20 @@ __global__ __launch_bounds__(64 * KW, M == 16 ? 4 : 2) void attn_stream8(const A
 #pragma unroll
       for (int n = 0; n < kE / 8; ++n) {
         u32x4 hi, lo;
-        weights8(w + 8 * n, hi, T::kNarrow ? &lo : nullptr);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          unsigned x, y;
+          weights2(w[8 * n + 2 * i], w[8 * n + 2 * i + 1], x, y);
+          hi[i] = x;
+          lo[i] = y;
+        }
         const int vrow = M == 32 ? 16 * n + 4 * g + (i8 & 3) + 2 * (i8 & 4) : 8 * g + i8;
 #pragma unroll
         for (int i = 0; i < kO; ++i) {
           const u32x2 x = L::column(vt, vrow, M == 32 ? 2 * i + ((lane >> 4) & 1) : i, lane);
           const u32x4 v = widen8<Bf16>(x[0], x[1]);
           o[i] = V::mma(v, hi, o[i]);
-          if constexpr (T::kNarrow) o[i] = V::mma(v, lo, o[i]);
+          o[i] = V::mma(v, lo, o[i]);
         }
       }
       wait_lds();
@@ -506,14 +468,18 @@ __global__ __launch_bounds__(64 * KW, M == 16 ? 4 : 2) void attn_stream8(const A
 // More rows to a list: RW waves of 32 rows share each staged tile of KT keys,
 // KW groups of them take the tiles in turn.  The codes are widened once, on
 // their way through registers to LDS, which then holds the tiles that the 16-bit
-// kernel stages; the next tile's codes load during this one's products.  A
-// group's first wave brings the scales, and the largest of the values'.
+// kernel stages (the values' as bf16); the next tile's codes load during this
+// one's products.  A group's first wave brings the scales.
 //
-// Bound by vector instructions: a wave's 64 keys take 1024 cycles of the matrix
-// unit and about 1900 of the softmax and of widening.  64 keys to a softmax have one
-// maximum, one test and one barrier where 32 have two: 24 drafted tokens of 32 heads
-// over 16 sequences of up to 8k keys take 95 us (bf16) and 101 us (f16), in tiles of
-// 32 114 and 135; with all pages in L2 83 and 92.
+// Bound by matrix and vector instructions, which the two waves of a SIMD hardly
+// overlap: a wave's 64 keys take 1536 cycles of the matrix unit, a third of them
+// for the weights' second operand, and about 2200 of the softmax, of widening and
+// of splitting weights.  24 drafted tokens of 32 heads over 16 sequences of up to
+// 8k keys, the same inputs again and again: 105 us (bf16) and 107 us (f16); with
+// one operand of the element type 85 and 88 us, which left outputs at 1.4 times
+// their own rounding's error, and f16 without digits beside values 2^27 as large.
+// 64 keys to a softmax have one maximum, one test and one barrier where 32 have two
+// (a fifth less time).
 template <class T, int D, int RW, int KW, int KT>
 __global__ __launch_bounds__(64 * RW * KW, 2) void attn_forward8(const AttnArgs a, const AttnScales scales) {
   using L = Tile<D>;
@@ -522,9 +488,10 @@ __global__ __launch_bounds__(64 * RW * KW, 2) void attn_forward8(const AttnArgs 
   constexpr int kHalf = KT * L::kRowBytes;
   constexpr int kPieces = D / 16;                      // 16-byte pieces of codes in a row
   constexpr int kFetch = 2 * KT * kPieces / kThreads;  // of K and V together, a thread's
-  static_assert(kFetch >= 1 && kFetch * kThreads == 2 * KT * kPieces && KT * kPieces % 64 == 0, "pieces of a tile");
+  static_assert((kFetch == 1 || kFetch % 2 == 0) && kFetch * kThreads == 2 * KT * kPieces && KT * kPieces % 64 == 0,
+                "pieces of a tile");
   constexpr int kSubs = kAttnPage / KT;
-  constexpr int kScales = 2 * KT + 4;  // floats of a stage: K's, V's, the largest of V's
+  constexpr int kScales = 2 * KT;  // floats of a stage: K's, V's
   extern __shared__ __attribute__((aligned(1024))) char lds[];
 
   const int lane = threadIdx.x & 63;
@@ -540,13 +507,14 @@ __global__ __launch_bounds__(64 * RW * KW, 2) void attn_forward8(const AttnArgs 
 
   char *tiles_at = lds + kw * 4 * kHalf;  // two stages of K and V
   float *scales_of = reinterpret_cast<float *>(lds + KW * 4 * kHalf) + kw * 2 * kScales;
-  // a thread's pieces: where they stand in the block, and in the stage (the
-  // second half of the widened piece at ^ 16)
+  // a thread's pieces, those of K first: where they stand in the block, and in
+  // the stage (the second half of the widened piece at ^ 16)
+  auto of_values = [&](int i) { return kFetch > 1 ? i >= kFetch / 2 : 64 * rw >= KT * kPieces; };
   uint32_t from[kFetch], to[kFetch];
 #pragma unroll
   for (int i = 0; i < kFetch; ++i) {
     const int at = 64 * rw + lane + i * kThreads;
-    const bool values = 64 * rw + i * kThreads >= KT * kPieces;
+    const bool values = of_values(i);
     const int r = at / kPieces % KT, p = at % kPieces;
     from[i] = static_cast<uint32_t>(r * (values ? vsrc.row : ksrc.row) + 16 * p);
     to[i] = (values ? kHalf : 0) + r * L::kRowBytes + (((2 * p) ^ L::f(r)) << 4);
@@ -556,7 +524,6 @@ __global__ __launch_bounds__(64 * RW * KW, 2) void attn_forward8(const AttnArgs 
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) o[i] = zero16();
   Stats st;
-  Unit<T> unit;
   const float c = a.scale * kLog2e;
 
   for (int32_t e = range.e0; e < range.e1; e += 64) {
@@ -577,7 +544,7 @@ __global__ __launch_bounds__(64 * RW * KW, 2) void attn_forward8(const AttnArgs 
       const auto vbuf = records(codes_at(vsrc, page, first), kept > 0 ? (kept - 1) * vsrc.row + D : 0);
 #pragma unroll
       for (int i = 0; i < kFetch; ++i) {
-        const bool values = 64 * rw + i * kThreads >= KT * kPieces;
+        const bool values = of_values(i);
         codes[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(values ? vbuf : kbuf, from[i], 0, 0));
       }
       if (rw == 0) {
@@ -592,18 +559,16 @@ __global__ __launch_bounds__(64 * RW * KW, 2) void attn_forward8(const AttnArgs 
       char *dst = tiles_at + (round & 1) * 2 * kHalf;
 #pragma unroll
       for (int i = 0; i < kFetch; ++i) {
-        *reinterpret_cast<u32x4 *>(dst + to[i]) = widen8<T>(codes[i][0], codes[i][1]);
-        *reinterpret_cast<u32x4 *>(dst + (to[i] ^ 16)) = widen8<T>(codes[i][2], codes[i][3]);
+        const bool values = of_values(i);
+        const u32x4 x = codes[i];
+        *reinterpret_cast<u32x4 *>(dst + to[i]) = values ? widen8<Bf16>(x[0], x[1]) : widen8<T>(x[0], x[1]);
+        *reinterpret_cast<u32x4 *>(dst + (to[i] ^ 16)) = values ? widen8<Bf16>(x[2], x[3]) : widen8<T>(x[2], x[3]);
       }
       if (rw == 0) {
         float *x = scales_of + (round & 1) * kScales;
         if (lane < KT) {
           x[lane] = ks;
           x[KT + lane] = vs;
-        }
-        if constexpr (T::kNarrow) {
-          const float top = largest(vs);
-          if (lane == 0) x[2 * KT] = top;
         }
       }
     };
@@ -623,7 +588,6 @@ __global__ __launch_bounds__(64 * RW * KW, 2) void attn_forward8(const AttnArgs 
       const int t = round * KW + kw;
       if (t >= tiles || !some) continue;
       const int32_t key0 = __builtin_amdgcn_readlane(blocks.id, t / kSubs) * kAttnPage + (t % kSubs) * KT;
-      if constexpr (T::kNarrow) unit.template raise<D / 32>(xs[2 * KT], st, o);
       constexpr int kN = KT / 32, kI = D / 32;
       const float *x = xs + F::first_key(lane);
       Scores<32> s[kN];
@@ -642,27 +606,29 @@ __global__ __launch_bounds__(64 * RW * KW, 2) void attn_forward8(const AttnArgs 
       }
       auto vx = operands<2 * kN * kI, kAhead>([&](int i) { return L::operand_t(vt, 16 * (i / kI), i % kI, lane); });
       vx.begin();
-      softmax8<T, D, 32, kN>(a, row, key0, lane, c, unit.shift, s, st, o);
-      u32x4 p[2 * kN];
+      softmax8<T, D, 32, kN>(a, row, key0, lane, c, s, st, o);
+      u32x4 hi[2 * kN], lo[2 * kN];
 #pragma unroll
       for (int i = 0; i < 4 * kN; ++i) {
         const f32x4 f = *reinterpret_cast<const f32x4 *>(x + KT + 8 * i);
         const float *w = reinterpret_cast<const float *>(s) + 4 * i;
-        p[i / 2][2 * (i % 2)] = pack2<T>(w[0] * f[0], w[1] * f[1]);
-        p[i / 2][2 * (i % 2) + 1] = pack2<T>(w[2] * f[2], w[3] * f[3]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          unsigned h, l;
+          weights2(w[2 * j] * f[2 * j], w[2 * j + 1] * f[2 * j + 1], h, l);
+          hi[i / 2][2 * (i % 2) + j] = h;
+          lo[i / 2][2 * (i % 2) + j] = l;
+        }
       }
-      vx.run([&](int i, u32x4 v) { o[i % kI] = T::mma(v, p[i / kI], o[i % kI]); });
+      vx.run([&](int i, u32x4 v) {
+        o[i % kI] = Bf16::mma(v, hi[i / kI], o[i % kI]);
+        o[i % kI] = Bf16::mma(v, lo[i / kI], o[i % kI]);
+      });
     }
     // the next entries' first tiles go where the last ones may still be read
     barrier();
   }
 
-  if constexpr (T::kNarrow) {  // back from the unit, exactly
-    const float f = unit.top * 0x1p-7f;
-    st.l *= f;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) o[i] *= f;
-  }
   st.l = add_halves(st.l);
   if (!row.live) st = Stats();
   if constexpr (KW > 1) {
@@ -689,7 +655,7 @@ hipError_t run_stream8(const AttnArgs &a, const AttnScales &x, hipStream_t s) {
 
 template <class T, int D, int RW, int KW, int KT>
 hipError_t run_forward8(const AttnArgs &a, const AttnScales &x, hipStream_t s) {
-  constexpr size_t kTiles = KW * (static_cast<size_t>(8) * KT * D + 2 * (2 * KT + 4) * 4);
+  constexpr size_t kTiles = KW * (static_cast<size_t>(8) * KT * D + 16 * KT);
   constexpr size_t kSums = static_cast<size_t>(KW - 1) * RW * (D / 2 + 2) * 256;
   constexpr size_t kLds = kTiles > kSums ? kTiles : kSums;
   hipError_t e = allow_dynamic_lds(reinterpret_cast<const void *>(&attn_forward8<T, D, RW, KW, KT>), kLds);

@@ -131,6 +131,30 @@ def attention(c, q, k, v, w):
     return out
 
 
+def attention8(c, q, k, v, w):
+    """The same where each weight, times its value's scale, enters as two bf16
+    parts: within 2^-16 of itself, and what is below 2^-126 counts as zero (127
+    of it at most with the code, against a sum of weights of at least 1).  The
+    rest as attn_ref.attention counts it; only the output is rounded to the type."""
+    out = A.attention(c, q, k, v, w)
+    u, e32 = torch.finfo(c["dtype"]).eps / 2, E32
+    g, d, n = c["hq"] // c["hk"], c["d"], c["nk"]
+    scale = c.get("scale") or 1.0 / math.sqrt(d)
+    on = (w > 0).repeat_interleave(g, 1)
+    seen = (w > 0).any(-2)[..., None]
+    kt, vt = (torch.where(seen, x.permute(0, 2, 1, 3), 0.0).repeat_interleave(g, 1) for x in (k, v))
+    qt = torch.where(on.any(-1)[..., None], q.permute(0, 2, 1, 3), 0.0)
+    s = scale * (qt @ kt.transpose(-1, -2)) + torch.log(w.clamp(min=1e-300)).repeat_interleave(g, 1)
+    far = torch.where(on, s - torch.where(on.any(-1), out["lse"][0], 0.0)[..., None], -math.inf)
+    es = torch.where(on, (d + 2) * e32 * scale * (qt.abs() @ kt.abs().transpose(-1, -2)), 0.0).amax(-1, keepdim=True)
+    ew = 2 * es + (24 + n) * e32 + 4 * e32 * torch.where(on, far.abs(), 0.0).amax(-1, keepdim=True)
+    value = out["o"][0].permute(0, 2, 1, 3)
+    bound = ((u + 4 * e32) * value.abs() + 1.02 * (2.0 ** -16 + ew) * (torch.exp(far) @ vt.abs())
+             + 2.0 ** -119 * on.sum(-1, keepdim=True) + 2.0 ** -126 * (on.double() @ vt.abs())
+             + torch.finfo(c["dtype"]).smallest_normal * u)
+    return {"o": (out["o"][0], bound.permute(0, 2, 1, 3)), "lse": out["lse"]}
+
+
 def freqs(pairs, base=10000.0):
     return [base ** (-p / max(1, pairs)) for p in range(pairs)]
 

@@ -588,6 +588,72 @@ def test_cache8_values_of_zero(S, nq):
     A.check("lse", lse, *R.attention(c, q.double(), k, 0 * v, A.sees(c, None, [300], [300 - nq], None))["lse"])
 
 
+# and 33 to 64 rows of a list in both types, in ranges and whole
+WEIGHTS = CACHE + [case(nq=24, nk=777, hq=8, hk=4, dtype=HF), case(b=2, nq=24, nk=900, hq=4, hk=2, d=128, dtype=HF),
+                   case(b=3, nq=17, nk=4000, hq=3, hk=1, d=128), case(b=2, nq=150, nk=300, hq=4, hk=2, dtype=HF)]
+
+
+def contiguous(cache, table, nk):
+    """The same cache without a table: [b, nk, hk, d] and [b * nkb, hk, 64]."""
+    at = table.long().cuda()
+    return [x[at].flatten(1, 2)[:, :nk].contiguous() for x in cache[:2]] + [x[at].flatten(0, 1).contiguous() for x in cache[2:]]
+
+
+@pytest.mark.parametrize("paged", [True, False])
+@pytest.mark.parametrize("how", ["full", "ragged"])
+@pytest.mark.parametrize("n", range(len(WEIGHTS)))
+def test_cache8_rounds_the_output_alone(S, n, how, paged):
+    """Weights keep 16 bits in every kernel: what is left is the output's own rounding."""
+    c = WEIGHTS[n]
+    g = torch.Generator().manual_seed(650 + n)
+    cache, k, v, table = filled(S, c, g)
+    q = torch.randn((c["b"], c["nq"], c["hq"], c["d"]), generator=g).to(c["dtype"])
+    lens, starts = new_tokens(c, how)
+    o, lse = outputs(c)
+    S.spmm_execute_attn_cache8(plan(S, c), q.cuda(), *(cache if paged else contiguous(cache, table, c["nk"])), o, lse,
+                               table=table.cuda() if paged else None, lens=ints(lens), starts=ints(starts))
+    want = R.attention8(c, q.double(), k, v, A.sees(c, None, lens, starts, None))
+    A.check("o", o, *want["o"])
+    A.check("lse", lse, *want["lse"])
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("hq", [1, 2, 4, 12])
+@pytest.mark.parametrize("large", [(3,), (40,), (699,), (3, 699), (40, 675, 699)])
+def test_cache8_large_values_leave_the_others(S, dtype, hq, large):
+    """Values near f16's end, 2^27 times the others: at keys whose weight is about
+    2^-60, and at a drafted token that only the last row sees.  The other rows
+    keep all digits of their type: values of one sign, so that no output is small
+    against them, and bounds in which a large value counts by its weight."""
+    c = case(nq=24, nk=700, hq=hq, hk=1, d=128, dtype=dtype)
+    g = torch.Generator().manual_seed(35)
+    cache, _, _, table = filled(S, c, g)
+    at = table.long()[0]
+    slots = at.repeat_interleave(PAGE)[:700], torch.arange(700) % PAGE
+    ks, vs = torch.full((700,), 1 / 700.0), torch.full((700,), 500.0 * 2.0 ** -27)
+    code = cache[0].cpu()
+    values = torch.randint(60, 128, cache[1].shape, generator=g).to(torch.int8)
+    for j in large:
+        vs[j] = 500.0
+        if j < 676:  # against queries that are all positive
+            code[slots[0][j], j % PAGE] = -127
+            ks[j] = 0.03
+    q = torch.rand((1, 24, hq, 128), generator=g).add(0.5).to(dtype)
+    cache[0].copy_(code)
+    cache[1].copy_(values)
+    cache[2][slots[0].cuda(), 0, slots[1].cuda()] = ks.cuda()
+    cache[3][slots[0].cuda(), 0, slots[1].cuda()] = vs.cuda()
+    k = code[slots].reshape(1, 700, 1, 128).double() * ks.double()[None, :, None, None]
+    v = values[slots].reshape(1, 700, 1, 128).double() * vs.double()[None, :, None, None]
+    tree = torch.full((1, 24), 1, dtype=torch.int64)
+    tree[0] |= torch.tensor([1 << t for t in range(24)])
+    o, lse = outputs(c)
+    S.spmm_execute_attn_cache8(plan(S, c), q.cuda(), *cache, o, lse, table=table.cuda(), tree=tree.cuda(), starts=ints([676]))
+    want = R.attention8(c, q.double(), k, v, A.sees(c, None, [700], [676], tree))
+    A.check("o", o, *want["o"])
+    A.check("lse", lse, *want["lse"])
+
+
 def test_cache8_far_pages_and_strides(S):
     """Pages beyond 4 GiB of codes, k and v side by side in a page, heads first."""
     c = case(b=2, nq=2, nk=300, hq=8, hk=2, d=128)
