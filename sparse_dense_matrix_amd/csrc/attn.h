@@ -131,6 +131,20 @@ __host__ __device__ inline bool attn_names(int32_t id, int32_t last_key) {
   return id >= 0 && id <= last_key / kAttnPage && last_key >= 0;
 }
 
+// Where tokens go that stand from position `start` on, `n` of them, of which those
+// in [0, len) count: in block w of the ones they can lie in, its keys [lo, hi)
+// (none where lo >= hi).  Cut off to the block in 64 bits: a position at either
+// end of 32 bits is further from a block than 32 bits reach.
+struct AttnTaken {
+  int32_t id, lo, hi;
+};
+__host__ __device__ inline AttnTaken attn_taken(int64_t start, int32_t n, int32_t len, uint32_t w) {
+  const int64_t end = start + n < len ? start + n : len;
+  const int64_t id = (start > 0 ? start : 0) / kAttnPage + w, lo = start - id * kAttnPage, hi = end - id * kAttnPage;
+  const auto cut = [](int64_t x) { return static_cast<int32_t>(x < 0 ? 0 : (x > kAttnPage ? kAttnPage : x)); };
+  return {static_cast<int32_t>(id), cut(lo), cut(hi)};
+}
+
 // Row tile of the forward kernels and the rows of a workgroup.
 struct AttnTile {
   int32_t row_waves, key_waves, key_tile, rows;

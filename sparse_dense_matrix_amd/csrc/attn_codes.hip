@@ -29,24 +29,6 @@ __device__ __forceinline__ int32_t page_of(const AttnCodesArgs &a, int32_t b, in
   return attn_page(a.table ? a.table + static_cast<int64_t>(b) * a.nkb : nullptr, block, a.pages);
 }
 
-// A workgroup's block of one head of a sequence, for `width` blocks a sequence from
-// the first that counts on, and the keys [lo, hi) of it that do.
-struct Block {
-  int32_t b, h, id, lo, hi;
-};
-__device__ __forceinline__ Block block_of(const AttnCodesArgs &a, int64_t start, int32_t b, int32_t h,
-                                          uint32_t w) {
-  Block x;
-  x.b = b;
-  x.h = h;
-  const int64_t end = min(static_cast<int64_t>(attn_len(a.lens, b, a.nk)), start + a.n);
-  const int64_t id = max(start, int64_t(0)) / kAttnPage + w;
-  x.id = static_cast<int32_t>(min(id, static_cast<int64_t>(a.nkb)));
-  x.lo = static_cast<int32_t>(max(start - id * kAttnPage, int64_t(0)));
-  x.hi = static_cast<int32_t>(min(end - id * kAttnPage, static_cast<int64_t>(kAttnPage)));
-  return x;
-}
-
 // top / 127, correctly rounded: a quotient that is off by a step corrected by its
 // remainder, which is exact (Markstein), where no result is subnormal.
 __device__ __forceinline__ float scale_of(float top) {
@@ -143,7 +125,7 @@ __global__ __launch_bounds__(256) void attn_write(const AttnCodesArgs a, uint32_
   const int32_t h = static_cast<int32_t>(head_of(blockIdx.x, gridDim.x / a.hk, a.hk, &item));
   const int32_t b = static_cast<int32_t>(item / width);
   const int64_t start = a.starts ? a.starts[b] : 0;
-  const Block x = block_of(a, start, b, h, item % width);
+  const AttnTaken x = attn_taken(start, a.n, attn_len(a.lens, b, a.nk), item % width);
   if (x.lo >= x.hi) return;
   const int32_t page = page_of(a, b, x.id);
   const int lane = threadIdx.x % (D / 8), group = threadIdx.x / (D / 8);
@@ -190,7 +172,7 @@ __global__ __launch_bounds__(256) void attn_read(const AttnCodesArgs a, uint32_t
   uint32_t item;
   const int32_t h = static_cast<int32_t>(head_of(blockIdx.x, gridDim.x / a.hk, a.hk, &item));
   const int32_t b = static_cast<int32_t>(item / width);
-  const Block x = block_of(a, 0, b, h, item % width);
+  const AttnTaken x = attn_taken(0, a.n, attn_len(a.lens, b, a.nk), item % width);
   if (x.hi <= 0) return;
   const int32_t page = page_of(a, b, x.id);
   const int lane = threadIdx.x % (D / 8), group = threadIdx.x / (D / 8);

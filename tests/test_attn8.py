@@ -137,6 +137,35 @@ def test_codes_survive_a_32_bit_division(dtype):
             assert (got == want).all()
 
 
+def test_tokens_go_to_their_blocks(tmp_path):
+    """Each position in [0, len) once, in its block, and nothing else: at every
+    32-bit start (idle sequences are often marked by one of its ends)."""
+    hipcc = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
+    if not os.path.exists(hipcc):
+        pytest.skip("hipcc not found")
+    exe = str(tmp_path / "taken")
+    subprocess.run([hipcc, "-O1", "-std=c++17", os.path.join(ROOT, "tests", "attn_taken_driver.cpp"), "-o", exe],
+                   check=True, capture_output=True)
+    least, most = -2 ** 31, 2 ** 31 - 1
+    rng = np.random.default_rng(7)
+    starts = [least + d for d in (0, 1, 60, 61, 62, 63, 64, 1000)] + [most - d for d in (0, 1, 62, 63, 64, 129, 4096)]
+    starts += [-1000, -65, -64, -1, 0, 1, 63, 64, 65, 4000] + rng.integers(-3000, 6000, 40).tolist()
+    cases = [(s, n, n_i) for s in starts for n in (65, 66, 127, 1000, 4097) for n_i in (0, 1, 10, 64, 777, 4096, most - 256)]
+    rows, lines = [], []
+    for s, n, n_i in cases:
+        width = (n + 62) // 64 + 1
+        rows += [(s, n, n_i)] * width
+        lines += [f"{s} {n} {n_i} {w}" for w in range(width)]
+    out = subprocess.run([exe], input="\n".join(lines) + "\n", capture_output=True, text=True, check=True).stdout.split("\n")
+    taken = {c: [] for c in cases}
+    for c, line in zip(rows, out):
+        block, lo, hi = map(int, line.split())
+        assert lo >= hi or (0 <= lo and hi <= 64 and block >= 0), (c, line)
+        taken[c] += range(block * 64 + lo, block * 64 + hi)
+    for (s, n, n_i), got in taken.items():
+        assert got == list(range(max(s, 0), min(s + n, n_i))), (s, n, n_i)
+
+
 def test_reference_codes():
     x = torch.tensor([[127.0, 0.5, 1.5, -2.5, 0.25, -127.0], [0.0] * 6, [1.0, float("nan"), 0, 0, 0, 0]])
     code, scale = R.encode(x.to(torch.bfloat16))

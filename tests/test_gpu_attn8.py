@@ -282,6 +282,38 @@ def test_write_and_read(S, n, paged):
         A.check("read", got, value, (u + 2 * R.E32) * value.abs() + torch.finfo(c["dtype"]).smallest_normal * u)
 
 
+@pytest.mark.parametrize("paged", [True, False])
+@pytest.mark.parametrize("n", [66, 1500])
+def test_write_of_sequences_far_from_their_keys(S, n, paged):
+    """Positions at the ends of 32 bits, as idle sequences may have: nothing of
+    theirs is read or written, in the kernel that goes by blocks and the other."""
+    starts = [-2 ** 31, -2 ** 31 + 61, 2 ** 31 - 1, 100, 2 ** 31 - 65, -n + 30, 2 ** 31 - 129]
+    b, nk, hk, d = len(starts), 4096, 8 if n == 1500 else 72, 64
+    nkb = nk // PAGE
+    g = torch.Generator().manual_seed(450)
+    k, v = rows((b, n, hk, d), BF, g), rows((b, n, hk, d), BF, g)
+    for i in (0, 1, 2, 4, 6):
+        k[i], v[i] = float("nan"), float("nan")
+    lens = [nk, nk, nk, nk, 10, nk, 0]
+    table = torch.randperm(b * nkb, generator=g).reshape(b, nkb).int() if paged else None
+    cache = empty_cache(b * nkb, hk, d)
+    want = [x.clone() for x in cache]
+    k8, v8, ks, vs = cache
+    if not paged:
+        k8, v8 = (x.view(b, nk, hk, d) for x in (k8, v8))
+    P = S.spmm_plan_attn(b, n, nk, hk, hk, d)
+    S.spmm_execute_attn_write(P, k.cuda(), v.cuda(), k8, v8, ks, vs, table=cuda(table), lens=ints(lens), starts=ints(starts))
+    for i, first, t in ((3, 100, 0), (5, 0, n - 30)):  # positions from `first` on, of tokens from t on
+        pos = torch.arange(first, first + n - t)
+        slot = table[i, pos // PAGE].long() if paged else i * nkb + pos // PAGE
+        for x, code, scale in ((k, 0, 2), (v, 1, 3)):
+            c, f = R.encode(x[i, t:])
+            want[code][slot.cuda(), (pos % PAGE).cuda()] = c.cuda()
+            want[scale][slot.cuda(), :, (pos % PAGE).cuda()] = f.cuda()
+    for got, w in zip(cache, want):
+        assert torch.equal(torch.nan_to_num(got.float(), 1e30), torch.nan_to_num(w.float(), 1e30))
+
+
 def test_codes_of_every_value(S):
     """Each finite bf16 number next to each of a few tops: the code is the rounded quotient's."""
     bits = torch.arange(-2 ** 15, 2 ** 15).short()
