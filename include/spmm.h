@@ -578,7 +578,8 @@ spmm_status_t spmm_execute_attn_cache8(spmm_plan_t p, const spmm_attn_tensor_t *
  * rounded once; squares of a row must sum up below 2^128.  Same inputs, same
  * bits.  The calls only launch kernels on `stream`. */
 typedef struct {
-  int64_t batch, tokens;        /* batch * tokens at most 2^31 - 1 (else UNSUPPORTED)   */
+  int64_t batch, tokens;        /* batch * tokens at most 2^28 - 16, with more than 16
+                                   heads of q and k together 2^26 - 4 (else UNSUPPORTED) */
   int32_t heads_q, heads_kv;
   int32_t dim;                  /* 64 or 128 (else UNSUPPORTED)                         */
   int32_t dtype;                /* SPMM_BF16 or SPMM_F16 (else UNSUPPORTED)             */

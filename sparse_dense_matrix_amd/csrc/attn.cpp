@@ -280,7 +280,9 @@ spmm_status_t rope_shape(const spmm_rope_desc_t &d, spmm_plan_s *p) {
   if (d.pairs % 8 != 0) return fail(SPMM_ERR_UNSUPPORTED, std::string(fn) + ": pairs must be a multiple of 8");
   if (d.heads_q > 65536 || d.heads_kv > 65536)
     return fail(SPMM_ERR_UNSUPPORTED, std::string(fn) + ": more than 65536 heads");
-  if (d.batch * d.tokens > INT32_MAX) return fail(SPMM_ERR_UNSUPPORTED, std::string(fn) + ": batch * tokens above 2^31 - 1");
+  if (const int64_t most = kAttnMaxGroups * rope_tokens(d.heads_q + d.heads_kv); d.batch * d.tokens > most)
+    return fail(SPMM_ERR_UNSUPPORTED, std::string(fn) + ": batch * tokens above " + std::to_string(most) +
+                                          ", more than a launch holds");
   p->rope = true;
   p->rope_desc = d;
   p->rope_desc.freqs = nullptr;

@@ -145,6 +145,14 @@ __host__ __device__ inline AttnTaken attn_taken(int64_t start, int32_t n, int32_
   return {static_cast<int32_t>(id), cut(lo), cut(hi)};
 }
 
+// Workgroups of 256 threads that a launch holds: work-items are counted in 32 bits.
+constexpr int64_t kAttnMaxGroups = (int64_t(1) << 24) - 1;
+
+// Tokens of a workgroup that turns rows.  Few heads: tokens enough that a group of
+// lanes has rows of its own.  32k tokens of 12 and 4 heads of 64 take 26 us in
+// sixteens, in fours 41; 6400 of 32 and 8 heads of 128 27 us in fours.
+inline int32_t rope_tokens(int32_t heads) { return heads <= 16 ? 16 : 4; }
+
 // Row tile of the forward kernels and the rows of a workgroup.
 struct AttnTile {
   int32_t row_waves, key_waves, key_tile, rows;

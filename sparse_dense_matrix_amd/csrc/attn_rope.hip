@@ -376,10 +376,7 @@ hipError_t run_forward(const RopeArgs &a, hipStream_t s) {
     hipLaunchKernelGGL((rope_rows<T, D>), dim3(static_cast<unsigned>(few)), dim3(256), 0, s, a);
     return hipGetLastError();
   }
-  // Few heads: tokens enough that a group of lanes has rows of its own.  32k tokens
-  // of 12 and 4 heads of 64 take 26 us in sixteens, in fours 41; 6400 of 32 and 8 heads
-  // of 128 27 us in fours.
-  return heads <= 16 ? run_forward<T, D, 16>(a, tokens, s) : run_forward<T, D, 4>(a, tokens, s);
+  return rope_tokens(static_cast<int32_t>(heads)) == 16 ? run_forward<T, D, 16>(a, tokens, s) : run_forward<T, D, 4>(a, tokens, s);
 }
 
 template <class T, int D>

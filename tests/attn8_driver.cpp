@@ -95,6 +95,9 @@ spmm_status_t rope_calls(bool back, const std::string &what) {
   if (what == "batch") d.batch = -1;
   if (what == "tokens") d.tokens = int64_t(1) << 31;
   if (what == "too_many") d.batch = d.tokens = 1 << 16;
+  if (what == "launch" || what == "launch_holds") d.batch = 4, d.tokens = (1 << 24) - (what == "launch" ? 0 : 1), d.heads_q = 15;
+  if (what == "launch_few" || what == "launch_few_holds")
+    d.batch = 16, d.tokens = (1 << 24) - (what == "launch_few" ? 0 : 1), d.heads_q = 14;
   if (what == "heads") d.heads_kv = 0;
   if (what == "heads_many") d.heads_q = 65537;
   if (what == "pairs") d.pairs = 40;
@@ -110,7 +113,7 @@ spmm_status_t rope_calls(bool back, const std::string &what) {
   if (what == "interleaved") d.interleaved = 2;
   spmm_plan_s p;
   const spmm_status_t s = sdm::rope_shape(d, &p);
-  if (s != SPMM_OK) return s;
+  if (s != SPMM_OK || what.compare(0, 6, "launch") == 0) return s;
   spmm_attn_tensor_t q = {memory, 16 * 256, 256, 64}, k = {memory, 16 * 128, 128, 64}, q2 = q, k2 = k, q3 = q, k3 = k;
   const float *qw = reinterpret_cast<const float *>(memory), *kw = qw;
   float *dqw = reinterpret_cast<float *>(memory), *dkw = dqw;

@@ -85,6 +85,15 @@ def test_rope_calls_refuse(ask, call):
     assert ask("rope nothing")[0].split()[0] == "SPMM_OK"
 
 
+def test_rope_plans_hold_what_a_launch_does(ask):
+    """2^24 - 1 workgroups of 256 threads, of 4 tokens (more than 16 heads) or 16:
+    one row of tokens more is refused before the first call."""
+    for what, limit in (("launch", 4 * (2 ** 24 - 1)), ("launch_few", 16 * (2 ** 24 - 1))):
+        status, _, message = ask(f"rope {what}")[0].partition(" ")
+        assert status == "SPMM_ERR_UNSUPPORTED" and str(limit) in message, message
+        assert ask(f"rope {what}_holds")[0].split()[0] == "SPMM_OK"
+
+
 def test_binding_refuses(S):
     with pytest.raises(ValueError):
         S.spmm_plan_attn_rope(1, 4, 2, 1, 64, [[1.0] * 8])
