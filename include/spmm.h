@@ -514,7 +514,9 @@ spmm_status_t spmm_execute_attn_cache(spmm_plan_t p, const spmm_attn_tensor_t *q
  * strides in elements, multiples of 16, 16-byte aligned.  k_scale and v_scale
  * are float[slots][heads_kv][64], slot = the block's page with a table, else
  * i * ceil(keys / 64) + block, and the key's place in its block last.  All
- * calls take a plan of spmm_plan_attn, whose dtype is that of q, k, v and o. */
+ * calls take a plan of spmm_plan_attn, whose dtype is that of q, k, v and o.  A
+ * call writes or reads back up to 2^24 - 1 blocks of a head (up to 64 tokens of a
+ * sequence: 2048 / dim * (2^24 - 1) rows), else it is UNSUPPORTED. */
 
 /* New tokens to the cache: token t of sequence i, k and v [batch][queries]
  * [heads_kv][dim], goes to position starts[i] + t.  Tokens whose position is not

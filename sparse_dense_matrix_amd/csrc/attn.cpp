@@ -552,8 +552,6 @@ spmm_status_t codes(const char *fn, bool read, spmm_plan_t p, const spmm_attn_te
     ATTN_TRY(codes_args(fn, a, dim, k8, v8, k_scale, v_scale, outer, table, !read, &x.k8, &x.v8));
     ATTN_TRY(whole(fn, "lens", lens, 4, false));
     ATTN_TRY(whole(fn, "starts", starts, 4, false));
-    if (static_cast<double>(a.b) * x.n * a.hk > 8.0 * 0x7fffffff)  // eight rows a workgroup at least
-      return fail(SPMM_ERR_UNSUPPORTED, std::string(fn) + ": more workgroups than a launch holds");
     x.k_scale = k_scale;
     x.v_scale = v_scale;
     x.table = table;
@@ -564,6 +562,8 @@ spmm_status_t codes(const char *fn, bool read, spmm_plan_t p, const spmm_attn_te
     x.hk = a.hk;
     x.nkb = a.nkb;
     x.pages = static_cast<int32_t>(pages);
+    if (attn_codes_launch(x, p->attn_desc.dim, read).groups > kAttnMaxGroups)
+      return fail(SPMM_ERR_UNSUPPORTED, std::string(fn) + ": more workgroups than a launch holds");
     if (a.b == 0 || x.n == 0 || a.nkb == 0) return SPMM_OK;
     const spmm_dtype_t t = static_cast<spmm_dtype_t>(p->attn_desc.dtype);
     DeviceScope ds(p->device);

@@ -148,6 +148,25 @@ __host__ __device__ inline AttnTaken attn_taken(int64_t start, int32_t n, int32_
 // Workgroups of 256 threads that a launch holds: work-items are counted in 32 bits.
 constexpr int64_t kAttnMaxGroups = (int64_t(1) << 24) - 1;
 
+// How the rows of a cache in 8 bits are written or read back: row by row, or by
+// blocks (`width` of a sequence); and workgroups.
+//
+// Written row by row up to 32k rows, or sequences' parts of up to a block, which fill
+// half of the two blocks that they may lie in: 32 sequences of 8 tokens of 8 heads of
+// 128 take 3.5 us row by row, by blocks 6.1; 4096 tokens 8.0 and 8.1, 16k 22 and 18;
+// 256 of 64 tokens 21 and 25, of 128 38 and 34.
+struct AttnCodesLaunch {
+  bool rows;
+  int64_t width, groups;
+};
+inline AttnCodesLaunch attn_codes_launch(const AttnCodesArgs &a, int d, bool read) {
+  const int64_t n = a.n, rows = static_cast<int64_t>(a.b) * n * a.hk, per = 256 / (d / 8);
+  // the blocks that n tokens from any position on can lie in
+  const int64_t reach = (n + kAttnPage - 2) / kAttnPage + 1, width = read || reach > a.nkb ? a.nkb : reach;
+  const bool by_rows = !read && (rows <= 32768 || n <= kAttnPage);
+  return {by_rows, width, by_rows ? (rows + per - 1) / per : static_cast<int64_t>(a.b) * width * a.hk};
+}
+
 // Tokens of a workgroup that turns rows.  Few heads: tokens enough that a group of
 // lanes has rows of its own.  32k tokens of 12 and 4 heads of 64 take 26 us in
 // sixteens, in fours 41; 6400 of 32 and 8 heads of 128 27 us in fours.

@@ -210,25 +210,17 @@ __global__ __launch_bounds__(256) void attn_read(const AttnCodesArgs a, uint32_t
 
 template <class T, int D, bool READ>
 hipError_t run_codes(const AttnCodesArgs &a, hipStream_t s) {
-  constexpr int64_t kRows = 256 / (D / 8);
-  const int64_t heads = a.hk, b = a.b, n = a.n;
-  // the blocks that n tokens from any position on can lie in
-  const int64_t width = READ ? a.nkb : (n + kAttnPage - 2) / kAttnPage + 1 < a.nkb ? (n + kAttnPage - 2) / kAttnPage + 1 : a.nkb;
-  // Up to 32k rows, or sequences' parts of up to a block, which fill half of the two
-  // blocks that they may lie in: 32 sequences of 8 tokens of 8 heads of 128 take 3.5
-  // us row by row, by blocks 6.1; 4096 tokens 8.0 and 8.1, 16k 22 and 18; 256 of 64
-  // tokens 21 and 25, of 128 38 and 34.
-  const bool few = !READ && (b * n * heads <= 32768 || n <= kAttnPage);
-  const int64_t grid = few ? (b * n * heads + kRows - 1) / kRows : b * width * heads;
-  if (grid == 0) return hipSuccess;
-  if (grid > 0x7fffffff) return hipErrorInvalidValue;
-  const dim3 blocks(static_cast<unsigned>(grid));
-  if (few)
+  const AttnCodesLaunch x = attn_codes_launch(a, D, READ);
+  if (x.groups == 0) return hipSuccess;
+  if (x.groups > kAttnMaxGroups) return hipErrorInvalidValue;
+  const dim3 blocks(static_cast<unsigned>(x.groups));
+  const uint32_t width = static_cast<uint32_t>(x.width);
+  if (x.rows)
     hipLaunchKernelGGL((attn_write_rows<T, D>), blocks, dim3(256), 0, s, a);
   else if constexpr (READ)
-    hipLaunchKernelGGL((attn_read<T, D>), blocks, dim3(256), 0, s, a, static_cast<uint32_t>(width));
+    hipLaunchKernelGGL((attn_read<T, D>), blocks, dim3(256), 0, s, a, width);
   else
-    hipLaunchKernelGGL((attn_write<T, D>), blocks, dim3(256), 0, s, a, static_cast<uint32_t>(width));
+    hipLaunchKernelGGL((attn_write<T, D>), blocks, dim3(256), 0, s, a, width);
   return hipGetLastError();
 }
 

@@ -29,6 +29,8 @@ spmm_status_t cache_calls(const std::string &call, const std::string &what) {
     d.heads_q = d.heads_kv = call == "read" ? 2 : 4;
     d.q_block = 64;
   }
+  if (what == "rows_launch") d.batch = 1 << 26, d.queries = 1, d.heads_q = d.heads_kv = 8;  // 2^24 times 32 rows
+  if (what == "blocks_launch") d.batch = 1 << 20, d.queries = call == "read" ? 1 : 128, d.keys = 256, d.heads_q = d.heads_kv = 8;
   spmm_plan_s p;
   const spmm_status_t s = sdm::attn_shape(d, &p);
   if (s != SPMM_OK) return s;

@@ -85,6 +85,13 @@ def test_rope_calls_refuse(ask, call):
     assert ask("rope nothing")[0].split()[0] == "SPMM_OK"
 
 
+def test_writing_and_reading_back_hold_what_a_launch_does(ask):
+    """2^24 workgroups or more are refused before any of them starts."""
+    for what in ("write rows_launch", "write blocks_launch", "read blocks_launch"):
+        status, _, message = ask(what)[0].partition(" ")
+        assert status == "SPMM_ERR_UNSUPPORTED" and "more workgroups than a launch holds" in message, (what, message)
+
+
 def test_rope_plans_hold_what_a_launch_does(ask):
     """2^24 - 1 workgroups of 256 threads, of 4 tokens (more than 16 heads) or 16:
     one row of tokens more is refused before the first call."""
