@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 import numpy as np
 
@@ -503,11 +504,33 @@ _bind = None
 # then goes as a pointer, a tensor of heads with strides.
 
 
+class _PythonChecks:
+    """What csrc/binding.cpp does, where that module is not built (a library
+    given in SPMM_LIBRARY) or was built for another Python or torch: 0.3 us a
+    tensor more."""
+
+    @staticmethod
+    def heads(t, want, device, pack=struct.Struct("=4q").pack):
+        if t.dtype is not want[1] or t.shape != want[0] or t.get_device() != device:
+            return None
+        sb, st, sh, sd = t.stride()
+        return pack(t.data_ptr(), sb, st, sh) if sd == 1 or not t.numel() else False
+
+    @staticmethod
+    def flat(t, want, device):
+        if t.dtype is not want[1] or t.shape != want[0] or t.get_device() != device:
+            return None
+        return t.data_ptr() if t.is_contiguous() else False
+
+
 def _load_binding():
     global _bind
-    import torch  # noqa: F401
-    from . import _binding
-    _bind = _binding
+    import torch
+    try:
+        from . import _binding
+        _bind = _binding if torch.__version__.split("+")[0] == _binding.torch_version else _PythonChecks
+    except ImportError:
+        _bind = _PythonChecks
     return _bind
 
 

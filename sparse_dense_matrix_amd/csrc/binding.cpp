@@ -1,10 +1,12 @@
 // binding.cpp -- the checks of the Python binding's attention tensors, as a
 // Python module: type, shape and device against what the plan takes, then the
 // pointer (and strides) that the C ABI takes.  From Python a tensor's attributes
-// take 0.4 us, ten of them more than a launch; from here all of them 0.1 us.
+// take 0.4 us, ten of them more than a launch; from here all of them 0.1 us.  It
+// fits the torch that it was compiled with: torch_version is compared on import.
 #include <Python.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include <cstdint>
 #include <exception>
@@ -79,4 +81,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, n
 
 }  // namespace
 
-extern "C" __attribute__((visibility("default"))) PyObject *PyInit__binding() { return PyModule_Create(&module); }
+extern "C" __attribute__((visibility("default"))) PyObject *PyInit__binding() {
+  PyObject *m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

@@ -3,7 +3,9 @@ call (tests/attn8_driver.cpp drives the library without a device), the
 binding's checks, and the reference that the GPU tests use."""
 import os
 import shutil
+import struct
 import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -109,6 +111,35 @@ def test_binding_refuses(S):
     with pytest.raises(S.SpmmError) as e:
         S.spmm_plan_attn_rope(1, 4, 2, 1, 64, [1.0] * 8, axis=[0] * 7 + [2], axes=2)
     assert e.value.name == "SPMM_ERR_INVALID_ARG" and "axis" in e.value.message
+
+
+def test_tensor_checks_without_the_module(S, monkeypatch):
+    """Without csrc/binding.cpp's module (a library given alone), or with one of
+    another torch, the checks run in Python: what fits goes on, the rest is refused."""
+    if not os.path.exists(os.path.join(LIBDIR, "_binding.so")):
+        pytest.skip("module not built")
+    monkeypatch.setattr(S, "_bind", None)
+    module = S._load_binding()
+    assert module.__name__.endswith("_binding") and module.torch_version == torch.__version__.split("+")[0]
+    monkeypatch.setattr(module, "torch_version", "1.0.0")
+    assert S._load_binding() is S._PythonChecks
+    monkeypatch.delattr(S, "_binding")
+    monkeypatch.setitem(sys.modules, S.__name__ + "._binding", None)
+    monkeypatch.setattr(S, "_bind", None)
+    x = torch.zeros((2, 3, 8, 64), dtype=torch.bfloat16)
+    want, here = ((2, 3, 4, 64), torch.bfloat16), -1  # the device of CPU tensors
+    y = x[:, :, 4:]
+    assert struct.unpack("=4q", S._heads("q", y, want, here)) == (y.data_ptr(), 3 * 512, 512, 64)
+    assert S._bind is S._PythonChecks
+    for bad in (x, y.half(), y.transpose(2, 3).contiguous().transpose(2, 3)):
+        with pytest.raises(ValueError):
+            S._heads("q", bad, want, here)
+    with pytest.raises(ValueError):
+        S._heads("q", y, want, 0)
+    assert S._flat("k", y.contiguous(), want, here) and S._opt("k", None, want, here) is None
+    for bad in (y, y.contiguous().half(), x):
+        with pytest.raises(ValueError):
+            S._flat("k", bad, want, here)
 
 
 @pytest.mark.parametrize("interleaved", [False, True])

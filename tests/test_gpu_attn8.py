@@ -852,6 +852,22 @@ def test_two_plans_on_two_streams(S):
         assert all(torch.equal(a, b) for a, b in zip(alone, got))
 
 
+def test_calls_without_the_module(S, monkeypatch):
+    """The same results and refusals where the tensors are checked in Python."""
+    c = case(b=2, nq=1, nk=300, hq=8, hk=2, d=128)
+    g = torch.Generator().manual_seed(63)
+    cache, _, _, table = filled(S, c, g)
+    q = torch.randn((2, 1, 8, 128), generator=g).to(BF).cuda()
+    outs = []
+    for checks in (S._load_binding(), S._PythonChecks):
+        monkeypatch.setattr(S, "_bind", checks)
+        o, lse = outputs(c)
+        S.spmm_execute_attn_cache8(plan(S, c), q, *cache, o, lse, table=table.cuda(), starts=ints([299, 100]))
+        outs.append((o, lse))
+        test_binding_refuses_tensors(S)
+    assert all(torch.equal(x, y) for x, y in zip(*outs))
+
+
 def test_binding_refuses_tensors(S):
     P = S.spmm_plan_attn(1, 1, 64, 2, 1, 64)
     Q = S.spmm_plan_attn_rope(1, 1, 2, 1, 64, R.freqs(32))
