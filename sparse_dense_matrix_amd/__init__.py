@@ -488,7 +488,7 @@ def _attn_expect(d: AttnDesc, device: int) -> dict:
     b, nq, nk, hq, hk, dim = d.batch, d.queries, d.keys, d.heads_q, d.heads_kv, d.dim
     t = torch.bfloat16 if d.dtype == BF16 else torch.float16
     nkb, nqb = -(-nk // 64), -(-nq // d.q_block)
-    return {"device": device, "attn": {
+    return {"device": int(device), "attn": {
         "q": ((b, nq, hq, dim), t), "k": ((b, nk, hk, dim), t), "page": ((64, hk, dim), t),
         "lse": ((b, hq, nq), torch.float32), "lists": ((b, hk, nqb, d.max_blocks), torch.int32),
         "table": ((b, nkb), torch.int32), "seq": ((b,), torch.int32), "tree": ((b, nq), torch.int64),
@@ -763,12 +763,17 @@ def spmm_plan_attn_rope(batch: int, tokens: int, heads_q: int, heads_kv: int, di
                     int(bool(backward)), eps, _ptr(f), None if x is None else _ptr(x))
     h = C.c_void_p()
     _check(_lib.spmm_plan_attn_rope(C.byref(desc), device, C.byref(h)), "spmm_plan_attn_rope")
+    return Plan(h, _rope_expect(desc, device))
+
+
+def _rope_expect(d: RopeDesc, device: int) -> dict:
+    """Shapes and types of a rotation plan's tensors."""
     import torch
-    t = torch.bfloat16 if dtype == BF16 else torch.float16
-    return Plan(h, {"device": device, "rope": {
-        "q": ((batch, tokens, heads_q, dim), t), "k": ((batch, tokens, heads_kv, dim), t),
-        "weight": ((dim,), torch.float32), "positions": ((axes, batch, tokens), torch.int32),
-        "seq": ((batch,), torch.int32)}})
+    t = torch.bfloat16 if d.dtype == BF16 else torch.float16
+    return {"device": int(device), "rope": {
+        "q": ((d.batch, d.tokens, d.heads_q, d.dim), t), "k": ((d.batch, d.tokens, d.heads_kv, d.dim), t),
+        "weight": ((d.dim,), torch.float32), "positions": ((d.axes, d.batch, d.tokens), torch.int32),
+        "seq": ((d.batch,), torch.int32)}}
 
 
 def _rope_want(plan: Plan) -> dict:

@@ -2,6 +2,7 @@
 64 bits (attn8_ref.py, attn_ref.py), whose bounds count roundings."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -850,6 +851,20 @@ def test_two_plans_on_two_streams(S):
     torch.cuda.synchronize()
     for got in outs:
         assert all(torch.equal(a, b) for a, b in zip(alone, got))
+
+
+def test_plans_from_numpy_sizes(S):
+    """Sizes and a device that are numpy's whole numbers plan for the same tensors."""
+    i = np.int64
+    q, k = torch.ones((1, 2, 2, 64), dtype=BF, device="cuda"), torch.ones((1, 2, 1, 64), dtype=BF, device="cuda")
+    R1 = S.spmm_plan_attn_rope(i(1), i(2), i(2), i(1), i(64), R.freqs(32), axes=i(1), device=i(0))
+    S.spmm_execute_attn_rope(R1, q, k, q, k, q_weight=torch.ones(64, device="cuda"))
+    P = S.spmm_plan_attn(i(1), i(2), i(64), i(2), i(1), i(64), device=i(0))
+    k8, v8, ks, vs = empty_cache(1, 1, 64)
+    S.spmm_execute_attn_write(P, k, k, k8, v8, ks, vs, table=ints([[0]]))
+    o, lse = torch.empty_like(q), torch.empty((1, 2, 2), device="cuda")
+    S.spmm_execute_attn_cache8(P, q, k8, v8, ks, vs, o, lse, table=ints([[0]]), lens=ints([2]))
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
 
 
 def test_calls_without_the_module(S, monkeypatch):
