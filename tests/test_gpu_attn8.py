@@ -687,6 +687,36 @@ def test_cache8_large_values_leave_the_others(S, dtype, hq, large):
     A.check("lse", lse, *want["lse"])
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("nq,hq,nk", [(1, 4, 4097), (1, 1, 1), (24, 1, 300), (3, 4, 65), (24, 2, 900), (24, 4, 900), (24, 12, 700)])
+@pytest.mark.parametrize("what", ["k", "v"])
+@pytest.mark.parametrize("scale", [math.nan, math.inf])
+def test_cache8_keys_and_values_that_stand_for_nan(S, dtype, nq, hq, nk, what, scale):
+    """A row of codes 0 with a scale that is NaN or infinite, at a key that every
+    query sees, at the first key of the last block, or at one that the last query
+    alone sees: whoever sees it comes out as NaN, whoever does not as NaN or right
+    (its block may spread it), and no score or sum of another row takes part."""
+    c = case(nq=nq, nk=nk, hq=hq, hk=1, d=128, dtype=dtype)
+    for at in sorted({0, nk // 2, (nk - nq) // PAGE * PAGE, nk - 1}):
+        g = torch.Generator().manual_seed(36)
+        cache, k, v, table = filled(S, c, g)
+        q = torch.randn((1, nq, hq, 128), generator=g).to(dtype)
+        want = R.attention8(c, q.double(), k, v, A.sees(c, None, [nk], [nk - nq], None))
+        slot = int(table[0, at // PAGE])
+        code, x = (cache[0], cache[2]) if what == "k" else (cache[1], cache[3])
+        code[slot, at % PAGE], x[slot, :, at % PAGE] = 0, scale
+        o, lse = outputs(c)
+        S.spmm_execute_attn_cache8(plan(S, c), q.cuda(), *cache, o, lse, table=table.cuda(), starts=ints([nk - nq]))
+        o, lse = o.cpu().double()[0], lse.cpu().double()[0].transpose(0, 1)  # [nq, hq, ..]
+        sees = torch.arange(nk - nq, nk) >= at
+        value, bound = want["o"][0][0], want["o"][1][0]
+        assert o[sees].isnan().all(), at
+        assert (o[~sees].isnan() | ((o - value).abs() <= bound)[~sees]).all(), at
+        exact, off = (x[0].transpose(0, 1) for x in want["lse"])
+        kept = torch.ones(nq, dtype=torch.bool) if what == "v" else ~sees
+        assert lse[~kept].isnan().all() and ((lse - exact).abs() <= off)[kept].all(), at
+
+
 def test_cache8_far_pages_and_strides(S):
     """Pages beyond 4 GiB of codes, k and v side by side in a page, heads first."""
     c = case(b=2, nq=2, nk=300, hq=8, hk=2, d=128)
