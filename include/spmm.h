@@ -576,9 +576,10 @@ spmm_status_t spmm_execute_attn_cache8(spmm_plan_t p, const spmm_attn_tensor_t *
  *
  * Tensors are [batch][tokens][heads][dim] as above, q and k of one buffer
  * among them.  An output may be its own input (same data and strides); else it
- * must not overlap one.  Angles are taken in 64 bits, the rest in 32, outputs
- * rounded once; squares of a row must sum up below 2^128.  Same inputs, same
- * bits.  The calls only launch kernels on `stream`. */
+ * must not overlap one.  Angles are taken in 64 bits (off by 2^-26 of a turn and
+ * 3 2^-53 of their turns), the rest in 32, outputs rounded once; squares of a row
+ * must sum up below 2^128, and their mean and eps to 2^-100 or more.  Same inputs,
+ * same bits.  The calls only launch kernels on `stream`. */
 typedef struct {
   int64_t batch, tokens;        /* batch * tokens at most 2^28 - 16, with more than 16
                                    heads of q and k together 2^26 - 4 (else UNSUPPORTED) */

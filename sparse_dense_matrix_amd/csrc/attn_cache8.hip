@@ -300,8 +300,8 @@ __device__ __forceinline__ void store8(const AttnArgs &a, const Item &it, const 
 // its own, without barriers: the next codes and scales of keys load during the
 // softmax and the product with the values, the next of values during the
 // scores.  KW waves share a list's tiles and join their sums.  Bound by memory:
-// 32 sequences of 21.5k of up to 32k keys, 8 key heads of 4: 258 us for 1.42 GB,
-// 5.5 TB/s, and the join of the ranges 6.
+// 32 sequences of 21.5k of up to 32k keys, 8 key heads of 4: 263 us for 1.42 GB,
+// 5.4 TB/s, and the join of the ranges 6.
 template <class T, int D, int M, int KW>
 __global__ __launch_bounds__(64 * KW, M == 16 ? 4 : 2) void attn_stream8(const AttnArgs a, const AttnScales scales) {
   using F = Form<T, M>;
@@ -673,10 +673,10 @@ hipError_t run8(const AttnArgs &a, const AttnScales &x, spmm_dtype_t t, hipStrea
   switch (attn_tile(a.rows, a.nqb).row_waves) {
     // A wave a list where there are lists enough to fill the chip and a sequence's
     // queries read keys of each other's from L2; rows of 16 where they fit.  8 blocks
-    // for every query, 8 key heads of 4: 2048 lists take 35 us, with four waves each 40,
-    // 1024 27 and 25.5, 32k 325 and (rows of 32) 725.  One query each, from memory: 300
-    // sequences of 2k keys take 291 us with a wave a head, 245 with four.  32 tokens over
-    // 8k keys each: rows of 16 119 us, of 32 140.
+    // for every query, 8 key heads of 4: 2048 lists take 39 us, with four waves each 43,
+    // 1024 28 and 26.5, 32k 333 and 401, with rows of 32 441.  One query each, from
+    // memory: 300 sequences of 2k keys take 294 us with a wave a head, 245 with four.  32
+    // sequences of 8k keys: rows of 16 119 us, of 32 147.
     case 1: {
       const bool alone = a.nqb > 1 && grid_of(a) >= 2048 && a.nsplit == 1;
       if (a.rows <= 16)
@@ -686,8 +686,9 @@ hipError_t run8(const AttnArgs &a, const AttnScales &x, spmm_dtype_t t, hipStrea
       break;
     }
     // 2048 queries of 8 heads, 16 blocks for each 64: two groups of waves to a list
-    // 27 us, one 43.  With four waves of rows a second group gains nothing (25.0 us
-    // for 24 drafted tokens over 8k keys, 24.4 without).
+    // 31 us, one 49.  With four waves of rows a second group gains little or loses:
+    // 26.4 us for 24 drafted tokens over 8k keys, 25.8 without; over 16 sequences 112
+    // and 107; 2048 queries of 16 heads over lists 38 and 41.
     case 2: e = run_forward8<T, D, 2, 2, 32>(a, x, s); break;
     case 4: e = run_forward8<T, D, 4, 1, 64>(a, x, s); break;
     default: e = run_forward8<T, D, 8, 1, 64>(a, x, s); break;

@@ -8,10 +8,12 @@
 //   dw_c = sum over rows of dy_c x_c r,
 //   dx_c = r (dy_c w_c - x_c r^2 mean_c(dy_c w_c x_c)).
 //
-// An angle is taken in turns, in 64 bits: the fraction of a turn is then good
-// to 2^-24 of a turn at any 32-bit position.  Each token's angles are computed
-// once for all heads, one a thread, and kept in LDS.  Everything else is in 32
-// bits, rounded once at the output.
+// An angle is taken in turns, in 64 bits: 2 pi, the frequency over it and the
+// product with the position leave 3 2^-53 of the turns, and the fraction of a turn
+// is rounded to 32 bits, 2^-26 of a turn (position 2^31 at one radian each: 2^-22.9
+// of a turn in all; positions below 2^20: 2^-26).  Each token's angles are computed
+// once for all heads, one a thread, and kept in LDS.  Everything else is in 32 bits,
+// rounded once at the output.
 #include "attn_dev.h"
 #include "internal.h"
 
@@ -194,7 +196,7 @@ __global__ __launch_bounds__(256) void rope_rows(const RopeArgs a) {
 // More rows: a token has 256 / (D / 8) / TOK groups of D / 8 lanes, which take its
 // heads in turn, so that a lane keeps its token's angles and its channels'
 // weights; the next rows load while rows are turned.  16k tokens of 32 and 8
-// heads: 67 us, 5.0 TB/s (a row at a time with its heads counted out by divisions:
+// heads: 72 us, 4.7 TB/s (a row at a time with its heads counted out by divisions:
 // 123 us).
 template <class T, int D, int TOK>
 __global__ __launch_bounds__(256) void rope_forward(const RopeArgs a) {
@@ -246,7 +248,7 @@ __global__ __launch_bounds__(256) void rope_forward(const RopeArgs a) {
 
 // Workgroups take tiles in turn; each lane sums the weights' gradients of its
 // channels over its rows, and the workgroup's sums go to the workspace.  16k tokens
-// of 32 and 8 heads of 128: 106 us for 503 MB, 4.75 TB/s, bound by memory: tiles of
+// of 32 and 8 heads of 128: 108 us for 503 MB, 4.7 TB/s, bound by memory: tiles of
 // 2 and 8 tokens and 4 rows in flight take as long.  Angles kept in registers, as
 // forward, leave room for too few rows: 112 us.
 template <class T, int D>
